@@ -515,6 +515,136 @@ kq_status kq_calib_step_noalloc(const uint16_t *A, const float *W, int64_t M, in
                                 float *lambdas, int auto_lambda, float *losses, float *grad_theta,
                                 kq_stream_t stream);
 
+/* Element types of the layer norm's and the epilogue product's activations. */
+typedef enum { KQ_F32 = 0, KQ_BF16 = 1 } kq_type;
+
+/*
+ * Activations of the product's epilogue (kq_mxfp4_linear), in fp32:
+ *   KQ_ACT_NONE       z
+ *   KQ_ACT_RELU       max(z, 0); slope 1 where z > 0, else 0
+ *   KQ_ACT_SILU       z / (1 + exp(-z))
+ *   KQ_ACT_GELU       z (1 + erf(z / sqrt 2)) / 2 (erf to 1.5e-7 absolute)
+ *   KQ_ACT_GELU_TANH  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
+ */
+typedef enum {
+    KQ_ACT_NONE = 0,
+    KQ_ACT_RELU = 1,
+    KQ_ACT_SILU = 2,
+    KQ_ACT_GELU = 3,
+    KQ_ACT_GELU_TANH = 4
+} kq_act;
+
+/*
+ * Layer norm over the rows of X, the norm in front of a quantized layer:
+ *   mean_i = sum_c x_ic / d,  rstd_i = 1 / sqrt(sum_c (x_ic - mean_i)^2 / d + eps),
+ *   y_ic = (x_ic - mean_i) rstd_i weight_c + bias_c,
+ * all in fp32 (the squares are summed around the mean), y rounded once to its
+ * type (nearest, ties to even).
+ *   X, Y          device, `type` (a kq_type) [m][ldx] and [m][ldy], ldx, ldy >= d;
+ *                 aligned to their elements. Both 16-byte aligned with rows of a
+ *                 multiple of 16 bytes (and weight, bias 16-byte aligned) run
+ *                 the vector path; d > 65536 bytes of a row and all other
+ *                 layouts the general one. Elements past d of a row are neither
+ *                 read nor written.
+ *   weight, bias  device, fp32 [d], or NULL (1 and 0)
+ *   eps           >= 0 and finite (KQ_ERR_SHAPE)
+ *   mean, rstd    device, fp32 [m], or NULL (not written); what
+ *                 kq_layernorm_backward reads
+ * Any d >= 1. Sizes or leading
+ * dimensions of 2^31 or more: KQ_ERR_UNSUPPORTED. An unknown type:
+ * KQ_ERR_UNSUPPORTED. A NaN or an infinity makes its own row NaN and no other.
+ */
+kq_status kq_layernorm(const void *X, int type, int64_t m, int64_t d, int64_t ldx, const float *weight,
+                       const float *bias, float eps, void *Y, int64_t ldy, float *mean, float *rstd,
+                       kq_stream_t stream);
+
+/*
+ * The gradients of kq_layernorm for the gradient dY of its output: with
+ * h = (x - mean) rstd and g = dy weight, per row
+ *   dx = rstd (g - sum_c g / d - h sum_c g h / d),
+ * and, summed over the rows in fp32 in a fixed order (the same result on every call),
+ *   dweight_c = sum_i dy_ic h_ic,  dbias_c = sum_i dy_ic.
+ *   dY, X, dX      device, `type` [m][lddy], [m][ldx], [m][lddx] (all >= d); vector
+ *                  path as kq_layernorm
+ *   weight         device, fp32 [d], or NULL (1)
+ *   mean, rstd     device, fp32 [m], as kq_layernorm wrote them
+ *   dweight, dbias device, fp32 [d], or NULL (not wanted); written, not added to
+ *   workspace      device, 16-byte aligned, at least
+ *                  kq_layernorm_backward_workspace_bytes(m, d) bytes (KQ_ERR_SHAPE
+ *                  when less); may be NULL when that is 0 or neither dweight nor
+ *                  dbias is wanted. Calls that may overlap need one each.
+ * With m == 0 and d > 0, dweight and dbias are set to zeros.
+ */
+kq_status kq_layernorm_backward_workspace_bytes(int64_t m, int64_t d, int64_t *bytes);
+kq_status kq_layernorm_backward(const void *dY, int64_t lddy, const void *X, int64_t ldx, int type, int64_t m,
+                                int64_t d, const float *weight, const float *mean, const float *rstd, void *dX,
+                                int64_t lddx, float *dweight, float *dbias, void *workspace, int64_t workspace_bytes,
+                                kq_stream_t stream);
+
+/*
+ * Layer norm straight into the quantizer: codes and scales of y T, where y is
+ * kq_layernorm's output before its rounding (fp32) and T the Kronecker transform of
+ * kq_transform_quantize_mxfp4 (same range rule, on |y|), or T = I when factors is
+ * NULL -- the norm, Sec. 1 Eq. 1's A T and Sec. 3.1's quantizer in one pass over X,
+ * without the bf16 activation between them.
+ *   X, type, m, d, ldx    as kq_layernorm, X 16-byte aligned, rows of a multiple
+ *                         of 16 bytes (KQ_ERR_ALIGN); d % 32 == 0 (KQ_ERR_SHAPE),
+ *                         d <= 32768 (KQ_ERR_UNSUPPORTED)
+ *   weight, bias, factors device, 16-byte aligned, or NULL
+ *   codes                 device, [m][d/2], 16-byte aligned
+ *   scales                device, [m][d/32], or with packed != 0 in the layout of
+ *                         kq_pack_mxfp4_scales (d % 256 == 0: KQ_ERR_SHAPE; m d/32
+ *                         below 2^31 - 16: KQ_ERR_UNSUPPORTED)
+ *   y_debug               device, fp32 [m][d], 16-byte aligned, or NULL: receives y T
+ *                         (check mode; the same codes)
+ *   mean, rstd            as kq_layernorm
+ */
+kq_status kq_layernorm_quantize_mxfp4(const void *X, int type, int64_t m, int64_t d, int64_t ldx, const float *weight,
+                                      const float *bias, float eps, const float *factors, uint8_t *codes,
+                                      uint8_t *scales, int packed, float *y_debug, float *mean, float *rstd,
+                                      kq_stream_t stream);
+
+/*
+ * The W4A4 product of Eq. 2 with the rest of a linear layer in its epilogue:
+ *   z = deq(A) deq(W)^T + bias,  O = act(z) + residual,
+ * fp32 up to one rounding of each output to its type (nearest, ties to even).
+ *   codes_a .. k          as kq_mxfp4_gemm, scales in the MX layout [rows][k/32]; with
+ *                         packed != 0 in the layout of kq_pack_mxfp4_scales (8-byte
+ *                         aligned; k % 256 == 0: KQ_ERR_SHAPE)
+ *   bias                  device, fp32 [n], or NULL (0)
+ *   act                   a kq_act value (any other: KQ_ERR_UNSUPPORTED)
+ *   type                  type of residual, O and Z (a kq_type)
+ *   residual              device, `type` [m][ldr], ldr >= n, or NULL (0); element aligned
+ *   O                     device, `type` [m][ldo], ldo >= n; element aligned, written
+ *   Z                     device, `type` [m][ldz], ldz >= n, or NULL: receives z (what
+ *                         kq_mxfp4_linear_backward reads)
+ * Any m, n >= 0 and k % 32 == 0 (KQ_ERR_SHAPE; k == 0: z = bias, the operands are not
+ * read). 256 rows of codes, m k/32 and n k/32 scale bytes and 256 rows of the outputs
+ * and the residual must each span fewer than 2^31 bytes (KQ_ERR_UNSUPPORTED). A few rows (tokens being generated) run on a kernel that
+ * streams W once with k split over the waves of a workgroup, many on the 256 x 256
+ * tiles of kq_mxfp4_gemm_packed; the sums agree to fp32 rounding.
+ */
+kq_status kq_mxfp4_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
+                          const uint8_t *scales_w, int packed, int64_t m, int64_t n, int64_t k, const float *bias,
+                          int act, int type, const void *residual, int64_t ldr, void *O, int64_t ldo, void *Z,
+                          int64_t ldz, kq_stream_t stream);
+
+/*
+ * The gradients of kq_mxfp4_linear's epilogue for the gradient dO of its output:
+ *   dZ = dO act'(Z),  dbias_j = sum_i dZ_ij (before dZ's rounding; fp32, fixed order).
+ * The residual's gradient is dO; the operands' follow from dZ (straight through the
+ * quantizer): dA = dZ deq(W), dW = dZ^T deq(A).
+ *   dO, Z, dZ   device, `type` [m][lddo], [m][ldz], [m][lddz] (all >= n), element
+ *               aligned; Z may be NULL with KQ_ACT_NONE, dZ NULL when not wanted
+ *   dbias       device, fp32 [n], or NULL; written, not added to
+ *   workspace   as kq_layernorm_backward, kq_mxfp4_linear_backward_workspace_bytes(m, n)
+ * With m == 0 and n > 0, dbias is set to zeros.
+ */
+kq_status kq_mxfp4_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t *bytes);
+kq_status kq_mxfp4_linear_backward(const void *dO, int64_t lddo, const void *Z, int64_t ldz, int type, int64_t m,
+                                   int64_t n, int act, void *dZ, int64_t lddz, float *dbias, void *workspace,
+                                   int64_t workspace_bytes, kq_stream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *kq_status_string(kq_status s);
 

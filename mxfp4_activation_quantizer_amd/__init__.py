@@ -50,6 +50,13 @@ EXPORTS = (
     "kq_calib_init",
     "kq_calib_step",
     "kq_calib_step_noalloc",
+    "kq_layernorm",
+    "kq_layernorm_backward_workspace_bytes",
+    "kq_layernorm_backward",
+    "kq_layernorm_quantize_mxfp4",
+    "kq_mxfp4_linear",
+    "kq_mxfp4_linear_backward_workspace_bytes",
+    "kq_mxfp4_linear_backward",
     "kq_status_string",
     "kq_last_hip_error",
     "kq_factors_from_lu",
@@ -108,6 +115,13 @@ def lib():
                               ctypes.c_float, p, st, p, p, p, i64, p],
             "kq_calib_step_noalloc": [p, p, i64, i64, i64, p, p, p, i64, ctypes.c_float, ctypes.c_float,
                                       ctypes.c_float, ctypes.c_float, p, st, p, p, p],
+            "kq_layernorm": [p, st, i64, i64, i64, p, p, ctypes.c_float, p, i64, p, p, p],
+            "kq_layernorm_backward_workspace_bytes": [i64, i64, p],
+            "kq_layernorm_backward": [p, i64, p, i64, st, i64, i64, p, p, p, p, i64, p, p, p, i64, p],
+            "kq_layernorm_quantize_mxfp4": [p, st, i64, i64, i64, p, p, ctypes.c_float, p, p, p, st, p, p, p, p],
+            "kq_mxfp4_linear": [p, p, p, p, st, i64, i64, i64, p, st, st, p, i64, p, i64, p, i64, p],
+            "kq_mxfp4_linear_backward_workspace_bytes": [i64, i64, p],
+            "kq_mxfp4_linear_backward": [p, i64, p, i64, st, i64, i64, st, p, i64, p, p, i64, p],
         }.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -755,6 +769,282 @@ def calib_step_noalloc(A, W, theta, adam_m, adam_v, t, lambdas, losses, grad=Non
                                        float(beta1), float(beta2), float(eps), _p(lambdas), int(bool(auto_lambda)),
                                        _p(losses), _p(grad) if grad is not None else None, _stream_ptr(stream)))
     return losses
+
+
+# ---------------------------------------------------------------------------
+# The layer around the W4A4 product: norm in front, epilogue behind, gradients
+# ---------------------------------------------------------------------------
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # kq_act
+
+
+def _elsewhere(t, stream):
+    """The context a call on ``t`` has to run in when it was given a stream or t's device is not
+    the current one (its allocations then belong to that stream too), else None."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return None
+
+
+def _matrix(t, name, dtype, device, shape=None):
+    """t's row stride: t must be a [rows][columns] tensor of dtype on device with unit column
+    stride (of that shape). A single row's stride does not matter."""
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape),
+                                                            "[rows][columns]" if shape is None else tuple(shape)))
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have unit column stride" % name)
+    return t.stride(0) if rows > 1 else cols
+
+
+def _vector(t, name, d, device):
+    """Pointer of the fp32 vector t of length d (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != _torch().float32:
+        raise TypeError("%s has dtype %s, expected torch.float32" % (name, t.dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.numel() != d or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous fp32 vector of length %d" % (name, d))
+    return t.data_ptr()
+
+
+def _packed_scales(t, name, rows, k, device, packed):
+    torch = _torch()
+    if t.dtype != torch.uint8 or t.device != device:
+        raise TypeError("%s must be a uint8 tensor on %s" % (name, device))
+    if not t.is_contiguous() or (t.numel() != rows * (k // 32) if packed else tuple(t.shape) != (rows, k // 32)):
+        raise ValueError("%s must be contiguous, %s" % (name, "rows * k/32 bytes" if packed else "[rows][k/32]"))
+    return t.data_ptr()
+
+
+def _workspace(name, rows, cols, workspace, device):
+    """(tensor, its bytes) for a call that sums over rows: the caller's, or one of this call's own."""
+    n = ctypes.c_int64(0)
+    _check(name, getattr(lib(), name)(rows, cols, ctypes.byref(n)))
+    if workspace is None:
+        workspace = _torch().empty(n.value, dtype=_torch().uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def layernorm(x, weight=None, bias=None, eps=1e-5, out=None, stats=False, mean=None, rstd=None, stream=None):
+    """Layer norm of the rows of x (bf16 or fp32 [m][d]): (x - mean) rstd weight + bias, in x's type.
+
+    weight, bias: fp32 [d] or None (1 and 0). ``stats=True`` (or mean, rstd: fp32 [m] to write
+    into) returns (y, mean, rstd), what layernorm_backward takes.
+    """
+    torch = _torch()
+    _dev(x, "x", (torch.bfloat16, torch.float32))
+    here = _elsewhere(x, stream)
+    if here is not None:
+        with here:
+            return layernorm(x, weight, bias, eps, out, stats, mean, rstd)
+    dtype, dev = x.dtype, x.device
+    ldx = _matrix(x, "x", dtype, dev)
+    m, d = x.shape
+    if out is None:
+        out = torch.empty((m, d), dtype=dtype, device=dev)
+    ldy = _matrix(out, "out", dtype, dev, x.shape)
+    stats = stats or mean is not None or rstd is not None
+    if stats:
+        if mean is None:
+            mean = torch.empty(m, dtype=torch.float32, device=dev)
+        if rstd is None:
+            rstd = torch.empty(m, dtype=torch.float32, device=dev)
+    _check("kq_layernorm",
+           lib().kq_layernorm(x.data_ptr(), 1 if dtype == torch.bfloat16 else 0, m, d, ldx,
+                              _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), eps, out.data_ptr(),
+                              ldy, _vector(mean, "mean", m, dev), _vector(rstd, "rstd", m, dev),
+                              torch.cuda.current_stream().cuda_stream))
+    return (out, mean, rstd) if stats else out
+
+
+def layernorm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, params=True,
+                       workspace=None, stream=None):
+    """Gradients of layernorm for its output's gradient dy (x's type and shape): (dx, dweight, dbias).
+
+    mean, rstd: fp32 [m] as layernorm returned them. ``params=False`` computes dx alone (and
+    returns None for the others). workspace: at least kq_layernorm_backward_workspace_bytes
+    bytes, or None (allocated for this call).
+    """
+    torch = _torch()
+    _dev(x, "x", (torch.bfloat16, torch.float32))
+    _dev(dy, "dy", (x.dtype,))
+    here = _elsewhere(x, stream)
+    if here is not None:
+        with here:
+            return layernorm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, params, workspace)
+    dtype, dev = x.dtype, x.device
+    ldx = _matrix(x, "x", dtype, dev)
+    lddy = _matrix(dy, "dy", dtype, dev, x.shape)
+    m, d = x.shape
+    if dx is None:
+        dx = torch.empty((m, d), dtype=dtype, device=dev)
+    lddx = _matrix(dx, "dx", dtype, dev, x.shape)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd of the forward pass are required")
+    ws, ws_bytes = None, 0
+    if params:
+        if dweight is None:
+            dweight = torch.empty(d, dtype=torch.float32, device=dev)
+        if dbias is None:
+            dbias = torch.empty(d, dtype=torch.float32, device=dev)
+        ws, ws_bytes = _workspace("kq_layernorm_backward_workspace_bytes", m, d, workspace, dev)
+    elif dweight is not None or dbias is not None:
+        raise ValueError("params=False computes neither dweight nor dbias")
+    _check("kq_layernorm_backward",
+           lib().kq_layernorm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, 1 if dtype == torch.bfloat16 else 0,
+                                       m, d, _vector(weight, "weight", d, dev), _vector(mean, "mean", m, dev),
+                                       _vector(rstd, "rstd", m, dev), dx.data_ptr(), lddx,
+                                       _vector(dweight, "dweight", d, dev), _vector(dbias, "dbias", d, dev),
+                                       ws.data_ptr() if ws is not None else None, ws_bytes,
+                                       torch.cuda.current_stream().cuda_stream))
+    return dx, dweight, dbias
+
+
+def layernorm_quantize_mxfp4(x, weight=None, bias=None, factors=None, eps=1e-5, packed=False, codes=None,
+                             scales=None, y_debug=None, stats=False, mean=None, rstd=None, stream=None):
+    """Layer norm, Kronecker transform (factors fp32 [d/32][5][2][2]; None: T = I) and MXFP4 in one
+    pass over x (bf16 or fp32 [m][d]): codes [m][d/2] and scales [m][d/32], or with ``packed``
+    in the layout of pack_mxfp4_scales ([d/256][m][8]). No bf16 rounding in between.
+
+    ``y_debug``: optional fp32 [m][d] tensor that receives the transformed norm (check mode).
+    ``stats=True`` (or mean, rstd given) returns (codes, scales, mean, rstd).
+    """
+    torch = _torch()
+    _dev(x, "x", (torch.bfloat16, torch.float32))
+    here = _elsewhere(x, stream)
+    if here is not None:
+        with here:
+            return layernorm_quantize_mxfp4(x, weight, bias, factors, eps, packed, codes, scales, y_debug, stats,
+                                            mean, rstd)
+    dtype, dev = x.dtype, x.device
+    ldx = _matrix(x, "x", dtype, dev)
+    m, d = x.shape
+    if codes is None:
+        codes = torch.empty((m, d // 2), dtype=torch.uint8, device=dev)
+    if codes.dtype != torch.uint8 or codes.device != dev or tuple(codes.shape) != (m, d // 2) or \
+            not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous [m][d/2] uint8 tensor on %s" % dev)
+    if scales is None:
+        scales = torch.empty((d // 256, m, 8) if packed and d % 256 == 0 else (m, d // 32), dtype=torch.uint8,
+                             device=dev)
+    sp = _packed_scales(scales, "scales", m, d, dev, packed)
+    if y_debug is not None:
+        _dev(y_debug, "y_debug", (torch.float32,))
+        if y_debug.device != dev or tuple(y_debug.shape) != (m, d) or not y_debug.is_contiguous():
+            raise ValueError("y_debug must be a contiguous fp32 [m][d] tensor on %s" % dev)
+    stats = stats or mean is not None or rstd is not None
+    if stats:
+        if mean is None:
+            mean = torch.empty(m, dtype=torch.float32, device=dev)
+        if rstd is None:
+            rstd = torch.empty(m, dtype=torch.float32, device=dev)
+    _check("kq_layernorm_quantize_mxfp4",
+           lib().kq_layernorm_quantize_mxfp4(x.data_ptr(), 1 if dtype == torch.bfloat16 else 0, m, d, ldx,
+                                             _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), eps,
+                                             _vector(factors, "factors", (d // 32) * 20, dev), codes.data_ptr(), sp,
+                                             1 if packed else 0, _p(y_debug), _vector(mean, "mean", m, dev),
+                                             _vector(rstd, "rstd", m, dev), torch.cuda.current_stream().cuda_stream))
+    return (codes, scales, mean, rstd) if stats else (codes, scales)
+
+
+def mxfp4_linear(codes_a, scales_a, codes_w, scales_w, bias=None, act="none", residual=None, out=None, pre=None,
+                 bf16=True, packed=False, want_pre=False, stream=None):
+    """act(deq(A) deq(W)^T + bias) + residual from MXFP4 operands, bf16 (or fp32) [m][n].
+
+    Operands as mxfp4_gemm (scales [rows][k/32]; any k % 32 == 0) or, with ``packed``, as
+    mxfp4_gemm_packed (k % 256 == 0). bias: fp32 [n]; act: one of ACTS; residual, out, pre: [m][n]
+    of the output's type. ``want_pre=True`` (or pre given) also returns the values in front of
+    the activation, (out, pre), what mxfp4_linear_backward takes.
+    """
+    torch = _torch()
+    _dev(codes_a, "codes_a", (torch.uint8,))
+    here = _elsewhere(codes_a, stream)
+    if here is not None:
+        with here:
+            return mxfp4_linear(codes_a, scales_a, codes_w, scales_w, bias, act, residual, out, pre, bf16, packed,
+                                want_pre)
+    dev = codes_a.device
+    if act not in ACTS:
+        raise ValueError("act must be one of %s" % ", ".join(ACTS))
+    if codes_w.dtype != torch.uint8 or codes_w.device != dev:
+        raise TypeError("codes_w must be a uint8 tensor on %s" % dev)
+    if codes_a.dim() != 2 or codes_w.dim() != 2 or codes_a.shape[1] != codes_w.shape[1] or \
+            not codes_a.is_contiguous() or not codes_w.is_contiguous():
+        raise ValueError("codes_a [m][k/2] and codes_w [n][k/2] must be contiguous")
+    m, kb = codes_a.shape
+    n, k = codes_w.shape[0], 2 * kb
+    sa = _packed_scales(scales_a, "scales_a", m, k, dev, packed)
+    sw = _packed_scales(scales_w, "scales_w", n, k, dev, packed)
+    dtype = torch.bfloat16 if bf16 else torch.float32
+    shape = (m, n)
+    ldr = ldz = 0
+    if residual is not None:
+        ldr = _matrix(residual, "residual", dtype, dev, shape)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    ldo = _matrix(out, "out", dtype, dev, shape)
+    if pre is None and want_pre:
+        pre = torch.empty(shape, dtype=dtype, device=dev)
+    if pre is not None:
+        ldz = _matrix(pre, "pre", dtype, dev, shape)
+    _check("kq_mxfp4_linear",
+           lib().kq_mxfp4_linear(codes_a.data_ptr(), sa, codes_w.data_ptr(), sw, 1 if packed else 0, m, n, k,
+                                 _vector(bias, "bias", n, dev), ACTS[act], 1 if bf16 else 0,
+                                 None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldo,
+                                 None if pre is None else pre.data_ptr(), ldz,
+                                 torch.cuda.current_stream().cuda_stream))
+    return out if pre is None else (out, pre)
+
+
+def mxfp4_linear_backward(dout, z=None, act="none", dz=None, dbias=None, workspace=None, stream=None):
+    """Gradients of mxfp4_linear's epilogue for its output's gradient dout (bf16 or fp32 [m][n]):
+    (dz, dbias) with dz = dout act'(z) and dbias its column sums (fp32 [n]).
+
+    z: the values in front of the activation (mxfp4_linear's pre), may be None with act "none". The
+    residual's gradient is dout; the operands' are dz deq(W) and dz^T deq(A).
+    """
+    torch = _torch()
+    _dev(dout, "dout", (torch.bfloat16, torch.float32))
+    here = _elsewhere(dout, stream)
+    if here is not None:
+        with here:
+            return mxfp4_linear_backward(dout, z, act, dz, dbias, workspace)
+    dtype, dev = dout.dtype, dout.device
+    if act not in ACTS:
+        raise ValueError("act must be one of %s" % ", ".join(ACTS))
+    lddo = _matrix(dout, "dout", dtype, dev)
+    m, n = dout.shape
+    ldz = 0
+    if z is not None:
+        ldz = _matrix(z, "z", dtype, dev, dout.shape)
+    elif act != "none":
+        raise ValueError("z is required with act %r" % act)
+    if dz is None:
+        dz = torch.empty((m, n), dtype=dtype, device=dev)
+    lddz = _matrix(dz, "dz", dtype, dev, dout.shape)
+    if dbias is None:
+        dbias = torch.empty(n, dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace("kq_mxfp4_linear_backward_workspace_bytes", m, n, workspace, dev)
+    _check("kq_mxfp4_linear_backward",
+           lib().kq_mxfp4_linear_backward(dout.data_ptr(), lddo, None if z is None else z.data_ptr(), ldz,
+                                          1 if dtype == torch.bfloat16 else 0, m, n, ACTS[act], dz.data_ptr(), lddz,
+                                          _vector(dbias, "dbias", n, dev), ws.data_ptr(), ws_bytes,
+                                          torch.cuda.current_stream().cuda_stream))
+    return dz, dbias
 
 
 def factors_from_lu(abc):

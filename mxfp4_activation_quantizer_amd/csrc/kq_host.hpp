@@ -52,4 +52,17 @@ inline kq_status launched() {
     return KQ_OK;
 }
 
+// Partial sums kept for a sum over m rows (the gradients of a norm's parameters and of a
+// bias): 16 rows each, at most 512. A function of m alone, so that a workspace's size and
+// the order of the sums do not depend on the device.
+inline int64_t row_parts(int64_t m) {
+    const int64_t p = (m + 15) / 16;
+    return p < 512 ? p : 512;
+}
+
+// out0[c] = sum over p < parts of part0[p][c] for c < d, likewise part1 into out1 (a NULL
+// output is skipped); zeros for parts == 0. Defined in kq_norm.hip.
+kq_status reduce_parts(const float *part0, const float *part1, int64_t parts, int64_t d, float *out0, float *out1,
+                       kq_stream_t stream);
+
 }  // namespace kqhost

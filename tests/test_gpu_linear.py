@@ -1,0 +1,224 @@
+"""GPU: the W4A4 product with bias, activation and residual in its epilogue, and that epilogue's
+gradients, against 64-bit plain forms (tests/layer_ref.py), within bounds derived there."""
+import pytest
+
+from tests import layer_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
+
+
+def case(msg):
+    print("[case] " + msg, flush=True)
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    return torch
+
+
+@pytest.fixture(scope="module")
+def kq():
+    import mxfp4_activation_quantizer_amd as kq
+    kq.lib()
+    return kq
+
+
+def gen(torch, seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def operand(torch, kq, rows, k, seed, scale=1.0):
+    """MXFP4 codes and scales of normal values."""
+    if k == 0 or rows == 0:
+        return (torch.empty((rows, k // 2), dtype=torch.uint8, device="cuda"),
+                torch.empty((rows, k // 32), dtype=torch.uint8, device="cuda"))
+    x = torch.randn(rows, k, generator=gen(torch, seed), device="cuda") * scale
+    return kq.quantize_mxfp4_f32(x)
+
+
+def check(torch, kq, m, n, k, name, dt, packed, bias=True, residual=True, seed=0, pad=0):
+    dtype = getattr(torch, dt)
+    case("linear %dx%dx%d %s %s packed=%d" % (m, n, k, name, dt, packed))
+    ca, sa = operand(torch, kq, m, k, seed + 1)
+    cw, sw = operand(torch, kq, n, k, seed + 2, 1.0 if k == 0 else k ** -0.5)
+    b = torch.randn(n, generator=gen(torch, seed + 3), device="cuda") if bias else None
+
+    def room():
+        buf = torch.full((m, n + pad), float("nan"), dtype=dtype, device="cuda")
+        return buf, buf[:, :n]
+
+    res = None
+    if residual:
+        _, res = room()
+        res.copy_(torch.randn(m, n, generator=gen(torch, seed + 4), device="cuda"))
+    pa, pw = (kq.pack_mxfp4_scales(sa), kq.pack_mxfp4_scales(sw)) if packed else (sa, sw)
+    (obuf, out), (zbuf, pre) = room(), room()
+    kq.mxfp4_linear(ca, pa, cw, pw, bias=b, act=name, residual=res, out=out, pre=pre, bf16=dt == "bfloat16",
+                    packed=packed)
+    o, z, o_tol, z_tol = ref.linear(ca, sa, cw, sw, b, name, res)
+    ref.assert_near(pre, z, z_tol, "z")
+    ref.assert_near(out, o, o_tol, "out")
+    assert int(obuf.isnan().sum()) == m * pad and int(zbuf.isnan().sum()) == m * pad  # the padding is left alone
+    alone = kq.mxfp4_linear(ca, pa, cw, pw, bias=b, act=name, residual=res, bf16=dt == "bfloat16", packed=packed)
+    assert torch.equal(alone, out)  # z asked for or not, padded or not, twice: the same output
+
+
+# one token, a few, one past and one short of a tile; k of one block, of part of a stage, of many; odd n
+SMALL = [(1, 16, 32), (1, 1, 64), (2, 33, 96), (7, 100, 1152), (16, 256, 512), (17, 130, 4096), (1, 1000, 2080),
+         (33, 515, 288), (45, 1000, 1152), (64, 64, 2048), (65, 257, 640), (130, 300, 1056), (250, 129, 4608),
+         (1, 16384, 256), (3, 5, 8192)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,n,k", SMALL)
+def test_few_rows(torch, kq, m, n, k, dt):
+    for i, packed in enumerate([False, True] if k % 256 == 0 else [False]):
+        check(torch, kq, m, n, k, ACTS[(m + n) % 5], dt, packed, seed=m)
+        check(torch, kq, m, n, k, ACTS[(m + n + 1) % 5], dt, packed, bias=False, residual=i == 0, seed=n, pad=3)
+
+
+# whole and ragged tiles of the many-row kernel, k of whole stages, of half ones, of neither
+LARGE = [(256, 256, 256), (1024, 4096, 512), (700, 1300, 1152), (2048, 2048, 384), (1111, 2222, 768),
+         (3000, 4104, 128), (513, 8191, 256), (4096, 520, 1056), (5000, 1024, 96)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_many_rows(torch, kq, m, n, k, dt):
+    for packed in [False, True] if k % 256 == 0 else [False]:
+        check(torch, kq, m, n, k, ACTS[(m + k // 32) % 5], dt, packed, seed=m, pad=8 * packed)
+
+
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_activations(torch, kq, name, dt):
+    """Every activation over a wide range of z (the bias spreads it), on both kernels."""
+    for m in (5, 1030):
+        n, k = 1024, 256
+        ca, sa = operand(torch, kq, m, k, 1)
+        cw, sw = operand(torch, kq, n, k, 2, k ** -0.5)
+        b = torch.linspace(-12, 12, n, device="cuda")
+        out, pre = kq.mxfp4_linear(ca, sa, cw, sw, bias=b, act=name, bf16=dt == "bfloat16", want_pre=True)
+        o, z, o_tol, z_tol = ref.linear(ca, sa, cw, sw, b, name, None)
+        ref.assert_near(pre, z, z_tol, "z")
+        ref.assert_near(out, o, o_tol, "out")
+
+
+def test_no_inner_dimension_and_empty(torch, kq):
+    """k = 0: act(bias) + residual; no rows or columns: nothing."""
+    check(torch, kq, 5, 40, 0, "silu", "float32", False)
+    check(torch, kq, 600, 700, 0, "gelu", "bfloat16", True)
+    for m, n in ((0, 8), (8, 0), (0, 0)):
+        ca, sa = operand(torch, kq, m, 64, 1)
+        cw, sw = operand(torch, kq, n, 64, 2)
+        assert kq.mxfp4_linear(ca, sa, cw, sw).shape == (m, n)
+
+
+def test_matches_plain_product(torch, kq):
+    """Without bias, activation and residual: the product's own fp32 sums, rounded once for bf16."""
+    ca, sa = operand(torch, kq, 1024, 768, 1)
+    cw, sw = operand(torch, kq, 2048, 768, 2)
+    pa, pw = kq.pack_mxfp4_scales(sa), kq.pack_mxfp4_scales(sw)
+    want = kq.mxfp4_gemm_packed(ca, pa, cw, pw)
+    for packed, a, w in ((True, pa, pw), (False, sa, sw)):
+        f32 = kq.mxfp4_linear(ca, a, cw, w, bf16=False, packed=packed)
+        o, z, o_tol, z_tol = ref.linear(ca, sa, cw, sw, None, "none", None)
+        ref.assert_near(f32, o, o_tol)
+        assert bool(((f32 - want).abs().double() <= 2 * z_tol).all())
+        assert torch.equal(kq.mxfp4_linear(ca, a, cw, w, packed=packed), f32.bfloat16())
+
+
+def test_extreme_scales(torch, kq):
+    """Scale bytes 0 .. 2 against 250 .. 254, whose products are in range, and zero codes."""
+    for m in (3, 520):
+        n, k = 300, 512
+        g = gen(torch, 5)
+        ca = torch.randint(0, 256, (m, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+        cw = torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+        sa = torch.randint(0, 3, (m, k // 32), generator=g, device="cuda", dtype=torch.uint8)
+        sw = torch.randint(250, 255, (n, k // 32), generator=g, device="cuda", dtype=torch.uint8)
+        ca[1] = 0
+        got = kq.mxfp4_linear(ca, sa, cw, sw, bf16=False)
+        o, z, o_tol, z_tol = ref.linear(ca, sa, cw, sw, None, "none", None)
+        ref.assert_near(got, o, o_tol)
+        assert not bool(got[1].any())
+
+
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,n", [(1, 1), (1, 4096), (16, 100), (17, 64), (301, 1003), (40, 4608), (9000, 72), (700, 2056)])
+def test_backward(torch, kq, m, n, dt, name):
+    dtype = getattr(torch, dt)
+    case("linear_grad %dx%d %s %s" % (m, n, dt, name))
+    dout = torch.randn(m, n, generator=gen(torch, 1), device="cuda").to(dtype)
+    z = (2.5 * torch.randn(m, n, generator=gen(torch, 2), device="cuda")).to(dtype)
+    got = kq.mxfp4_linear_backward(dout, z, act=name)
+    want, tol = ref.linear_grad(dout, z, name)
+    for g, v, t, what in zip(got, want, tol, ("dz", "dbias")):
+        ref.assert_near(g, v, t, what)
+    again = kq.mxfp4_linear_backward(dout, z, act=name)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    if name == "none":
+        alone = kq.mxfp4_linear_backward(dout)
+        assert torch.equal(alone[0], got[0]) and torch.equal(alone[1], got[1])
+
+
+@pytest.mark.parametrize("extra,offset", [(8, 0), (3, 0), (0, 1)])
+def test_backward_strides_and_alignment(torch, kq, extra, offset):
+    m, n = 50, 712
+    for dtype in (torch.bfloat16, torch.float32):
+        def place(v):
+            buf = torch.full((m * (n + extra) + offset + 64,), float("nan"), dtype=dtype, device="cuda")
+            view = buf[offset:offset + m * (n + extra)].view(m, n + extra)[:, :n]
+            view.copy_(v)
+            return view, buf
+
+        dout, _ = place(torch.randn(m, n, generator=gen(torch, 1), device="cuda"))
+        z, _ = place(torch.randn(m, n, generator=gen(torch, 2), device="cuda"))
+        dz, buf = place(torch.zeros(m, n, device="cuda"))
+        got = kq.mxfp4_linear_backward(dout, z, act="gelu", dz=dz)
+        want, tol = ref.linear_grad(dout, z, "gelu")
+        for g, v, t in zip(got, want, tol):
+            ref.assert_near(g, v, t)
+        assert int(buf.isnan().sum()) == buf.numel() - m * n
+
+
+def test_backward_far_arguments(torch, kq):
+    """Slopes where the activation is saturated, and far beyond: finite, 0 or 1 times dout."""
+    z = torch.tensor([[-1e30, -3e19, -200.0, -60.0, 0.0, 60.0, 200.0, 3e19, 1e30]], device="cuda")
+    d = torch.ones_like(z)
+    for name in ACTS:
+        dz = kq.mxfp4_linear_backward(d, z, act=name)[0]
+        assert bool(dz.isfinite().all()), name
+        if name != "none":
+            assert not bool((dz[0, :4].abs() > 1e-20).any()) and torch.equal(dz[0, 5:], d[0, 5:]), name
+
+
+def test_refusals(torch, kq):
+    ca, sa = operand(torch, kq, 4, 64, 1)
+    cw, sw = operand(torch, kq, 8, 64, 2)
+    with pytest.raises(ValueError):
+        kq.mxfp4_linear(ca, sa, cw, sw, act="tanh")
+    with pytest.raises(ValueError):
+        kq.mxfp4_linear(ca, sa, cw[:, :16], sw)
+    with pytest.raises(ValueError):
+        kq.mxfp4_linear(ca, sa[:3], cw, sw)
+    with pytest.raises(ValueError):
+        kq.mxfp4_linear(ca, sa, cw, sw, bias=torch.zeros(9, device="cuda"))
+    with pytest.raises(TypeError):
+        kq.mxfp4_linear(ca, sa, cw, sw, residual=torch.zeros(4, 8, device="cuda"))  # fp32 beside a bf16 output
+    with pytest.raises(ValueError):
+        kq.mxfp4_linear(ca, sa, cw, sw, out=torch.zeros(4, 9, device="cuda", dtype=torch.bfloat16))
+    with pytest.raises(kq.KQError):
+        kq.mxfp4_linear(ca, sa, cw, sw, packed=True)  # k is no whole number of stages
+    x = torch.zeros(4, 8, device="cuda")
+    with pytest.raises(ValueError):
+        kq.mxfp4_linear_backward(x, None, act="relu")
+    with pytest.raises(TypeError):
+        kq.mxfp4_linear_backward(x, x.bfloat16(), act="relu")
+    with pytest.raises(TypeError):
+        kq.mxfp4_linear_backward(x.double(), x, act="relu")

@@ -1,0 +1,279 @@
+"""GPU: layer norm, its gradients and the norm straight into the MXFP4 quantizer against 64-bit plain
+forms (tests/layer_ref.py), within bounds derived there."""
+import numpy as np
+import pytest
+
+import synth
+from tests import layer_ref as ref
+from tests import parity
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+
+
+def case(msg):
+    print("[case] " + msg, flush=True)
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    return torch
+
+
+@pytest.fixture(scope="module")
+def kq():
+    import mxfp4_activation_quantizer_amd as kq
+    kq.lib()
+    return kq
+
+
+def rand(torch, *shape, seed, scale=1.0, shift=0.0, dtype=None):
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = torch.randn(*shape, generator=g, device="cuda") * scale + shift
+    return x if dtype is None else x.to(dtype)
+
+
+def strided(torch, x, extra, offset=0):
+    """x inside a wider buffer of NaN: row stride columns + extra, starting `offset` elements in."""
+    m, d = x.shape
+    buf = torch.full((m * (d + extra) + offset + 64,), float("nan"), dtype=x.dtype, device="cuda")
+    view = buf[offset:offset + m * (d + extra)].view(m, d + extra)[:, :d]
+    view.copy_(x)
+    return view, buf
+
+
+# (m, d): one element, odd widths, whole and partial vectors, one and several waves per row, rows beyond
+# every register-resident width, more rows than workgroups in flight
+SHAPES = [(1, 1), (1, 7), (3, 8), (5, 31), (2, 64), (300, 40), (4, 520), (37, 1152), (9, 4096), (2, 4104), (3, 8200),
+          (2, 16384), (2, 40000), (1, 70001), (5000, 264)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,d", SHAPES)
+def test_forward(torch, kq, m, d, dt):
+    dtype = getattr(torch, dt)
+    case("norm %dx%d %s" % (m, d, dt))
+    x = rand(torch, m, d, seed=m + d, scale=2.0, shift=0.5, dtype=dtype)
+    w, b = rand(torch, d, seed=1, shift=1.0), rand(torch, d, seed=2)
+    for ww, bb in ((w, b), (None, b), (w, None), (None, None)):
+        y, mean, rstd = kq.layernorm(x, ww, bb, eps=EPS, stats=True)
+        y0, mu, rs, y_tol, mu_tol, rs_tol = ref.norm(x, ww, bb, EPS)
+        ref.assert_near(y, y0, y_tol, "y")
+        ref.assert_near(mean, mu, mu_tol, "mean")
+        ref.assert_near(rstd, rs, rs * rs_tol, "rstd")
+    assert torch.equal(kq.layernorm(x, None, None, eps=EPS), y)  # without the statistics: the same
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("extra,offset", [(8, 0), (3, 0), (0, 1), (16, 8)])
+def test_strides_and_alignment(torch, kq, dt, extra, offset):
+    """Padded and misaligned rows: the padding (NaN) is neither read nor written."""
+    dtype = getattr(torch, dt)
+    m, d = 21, 1160
+    x0 = rand(torch, m, d, seed=5, dtype=dtype)
+    dy0 = rand(torch, m, d, seed=6, dtype=dtype)
+    w, b = rand(torch, d, seed=1, shift=1.0), rand(torch, d, seed=2)
+    x, _ = strided(torch, x0, extra, offset)
+    out, buf = strided(torch, torch.zeros_like(x0), extra, offset)
+    y, mean, rstd = kq.layernorm(x, w, b, eps=EPS, out=out, stats=True)
+    y0, mu, rs, y_tol, _, _ = ref.norm(x0, w, b, EPS)
+    ref.assert_near(out, y0, y_tol, "y")
+    assert int(buf.isnan().sum()) == buf.numel() - m * d
+    dy, _ = strided(torch, dy0, extra, offset)
+    dx, buf = strided(torch, torch.zeros_like(x0), extra, offset)
+    _, dw, db = kq.layernorm_backward(dy, x, mean, rstd, w, dx=dx)
+    want, tol = ref.norm_grad(dy0, x0, mean, rstd, w)
+    for got, v, t, what in zip((dx, dw, db), want, tol, ("dx", "dw", "db")):
+        ref.assert_near(got, v, t, what)
+    assert int(buf.isnan().sum()) == buf.numel() - m * d
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,d", SHAPES + [(16, 96), (17, 96), (9000, 72)])
+def test_backward(torch, kq, m, d, dt):
+    dtype = getattr(torch, dt)
+    case("norm_grad %dx%d %s" % (m, d, dt))
+    x = rand(torch, m, d, seed=m + d, scale=2.0, shift=0.5, dtype=dtype)
+    dy = rand(torch, m, d, seed=m + d + 1, dtype=dtype)
+    w = rand(torch, d, seed=1, shift=1.0)
+    _, mean, rstd = kq.layernorm(x, w, None, eps=EPS, stats=True)
+    for ww in (w, None):
+        got = kq.layernorm_backward(dy, x, mean, rstd, ww)
+        want, tol = ref.norm_grad(dy, x, mean, rstd, ww)
+        for g, v, t, what in zip(got, want, tol, ("dx", "dw", "db")):
+            ref.assert_near(g, v, t, what)
+        again = kq.layernorm_backward(dy, x, mean, rstd, ww)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))  # a fixed order of sums
+    dx, none, nothing = kq.layernorm_backward(dy, x, mean, rstd, None, params=False)
+    assert torch.equal(dx, got[0]) and none is None and nothing is None
+
+
+def test_large_offset_and_equal_rows(torch, kq):
+    """A mean far from zero cancels without loss; a row of equal values gives the bias (x - mean is
+    0 up to 2 u of the first mean's rounding, times rstd = 1 / sqrt(eps))."""
+    for d in (24, 1000, 4096, 5000):
+        x = rand(torch, 6, d, seed=d, shift=3000.0)
+        b = rand(torch, d, seed=3)
+        y, mean, rstd = kq.layernorm(x, None, b, eps=EPS, stats=True)
+        y0, mu, rs, y_tol, mu_tol, rs_tol = ref.norm(x, None, b, EPS)
+        ref.assert_near(y, y0, y_tol, "y")
+        ref.assert_near(mean, mu, mu_tol, "mean")
+        x = torch.full((3, d), 1000.1, device="cuda")
+        y = kq.layernorm(x, None, b, eps=EPS)
+        y0, mu, rs, y_tol, mu_tol, rs_tol = ref.norm(x, None, b, EPS)
+        ref.assert_near(y, y0, y_tol, "equal")
+        z = kq.layernorm(torch.zeros(2, d, device="cuda"), None, b, eps=EPS)
+        assert torch.equal(z, b.expand(2, d))
+
+
+def test_nan_and_infinity_stay_in_their_rows(torch, kq):
+    for d in (100, 1024):
+        x = rand(torch, 9, d, seed=1, dtype=torch.bfloat16)
+        clean = kq.layernorm(x)
+        x[2, 5] = float("nan")
+        x[6, d - 1] = float("inf")
+        y = kq.layernorm(x)
+        assert bool(y[2].isnan().all()) and bool(y[6].isnan().all())
+        keep = [0, 1, 3, 4, 5, 7, 8]
+        assert torch.equal(y[keep], clean[keep])
+
+
+def test_no_rows(torch, kq):
+    x = torch.empty(0, 48, device="cuda")
+    w = torch.ones(48, device="cuda")
+    y, mean, rstd = kq.layernorm(x, w, w, stats=True)
+    assert y.shape == (0, 48) and mean.numel() == 0
+    dw = torch.full((48,), 7.0, device="cuda")
+    dx, dw, db = kq.layernorm_backward(x, x, mean, rstd, w, dweight=dw)
+    assert dx.shape == (0, 48) and not bool(dw.any()) and not bool(db.any())
+    codes, scales = kq.layernorm_quantize_mxfp4(torch.empty(0, 64, device="cuda"))
+    assert codes.shape == (0, 32) and scales.shape == (0, 2)
+
+
+def test_offsets_past_32_bits(torch, kq):
+    """Rows whose element offsets pass 2^31 (a view of a 5 GiB buffer): the last ones are right."""
+    ld, m, d = 1 << 20, 2500, 96
+    buf = torch.empty(m * ld, dtype=torch.bfloat16, device="cuda")
+    x = buf.view(m, ld)[:, 8:8 + d]
+    x.copy_(rand(torch, m, d, seed=11, dtype=torch.bfloat16))
+    w = rand(torch, d, seed=1, shift=1.0)
+    y, mean, rstd = kq.layernorm(x, w, None, eps=EPS, stats=True)
+    ref.assert_near(y, *[ref.norm(x, w, None, EPS)[i] for i in (0, 3)], "y")
+    dy = rand(torch, m, d, seed=12, dtype=torch.bfloat16)
+    out = buf.view(m, ld)[:, 4096:4096 + d]
+    got = kq.layernorm_backward(dy, x, mean, rstd, w, dx=out)
+    want, tol = ref.norm_grad(dy, x, mean, rstd, w)
+    for g, v, t in zip(got, want, tol):
+        ref.assert_near(g, v, t)
+    xq = buf.view(m, ld)[:, 8:8 + d]
+    c1, s1 = kq.layernorm_quantize_mxfp4(xq, w)
+    c2, s2 = kq.layernorm_quantize_mxfp4(xq.contiguous(), w)
+    assert torch.equal(c1, c2) and torch.equal(s1, s2)
+
+
+# one block, widths that fill no wave, whole and partial segments of 512 channels, one to many waves
+QSHAPES = [(1, 32), (3, 96), (70, 160), (5, 512), (33, 544), (19, 1152), (1, 4096), (40, 4608), (6, 8224), (3, 16384),
+           (2, 32768)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,d", QSHAPES)
+def test_quantize(torch, kq, m, d, dt):
+    """In check mode y T is within its bound of 64 bits, and codes and scales are exactly the
+    quantization of that y T; the mode changes neither, nor does the packed layout."""
+    dtype = getattr(torch, dt)
+    case("norm_quant %dx%d %s" % (m, d, dt))
+    x = rand(torch, m, d, seed=m + d, scale=2.0, shift=0.5, dtype=dtype)
+    w, b = rand(torch, d, seed=1, scale=0.3, shift=1.0), rand(torch, d, seed=2, scale=0.2)
+    for kind in ("lu", "mixed", None):
+        f = None if kind is None else (synth.lu_perturbed_factors(d // 32, 4) if kind == "lu" else
+                                       synth.special_factors(d // 32, "mixed"))
+        fac = None if f is None else torch.from_numpy(f).cuda()
+        y = torch.empty((m, d), device="cuda")
+        codes, scales, mean, rstd = kq.layernorm_quantize_mxfp4(x, w, b, fac, eps=EPS, y_debug=y, stats=True)
+        c2, s2 = kq.layernorm_quantize_mxfp4(x, w, b, fac, eps=EPS)
+        assert torch.equal(codes, c2) and torch.equal(scales, s2)
+        parity.check_self_consistent(codes.cpu().numpy(), scales.cpu().numpy(), y.cpu().numpy())
+        y0, mu, rs, y_tol, mu_tol, rs_tol = ref.norm(x, w, b, EPS)
+        ref.assert_near(mean, mu, mu_tol, "mean")
+        ref.assert_near(rstd, rs, rs * rs_tol, "rstd")
+        yb, tb = y0.view(m, -1, 32), y_tol.view(m, -1, 32)
+        if f is not None:
+            k = np.ones((d // 32, 1, 1))
+            for i in range(5):
+                k = np.stack([np.kron(p, q) for p, q in zip(k, f[:, i].astype(np.float64))])
+            k = torch.from_numpy(k).cuda()
+            # per output channel, sum over r of |y_r K_rc|; each stage's mixing rounds by a few u
+            # (the transform's own rule: 1e-5 of the block's norm), and the norm's bound passes through |K|
+            want = torch.stack([yb[:, j] @ k[j] for j in range(d // 32)], 1)
+            tol = torch.stack([tb[:, j] @ k[j].abs() for j in range(d // 32)], 1)
+            tol = tol + 1e-5 * want.norm(dim=2, keepdim=True)
+        else:
+            want, tol = yb, tb
+        ref.assert_near(y.view(m, -1, 32), want, tol, "y T")
+        if d % 256 == 0:
+            c3, p3 = kq.layernorm_quantize_mxfp4(x, w, b, fac, eps=EPS, packed=True)
+            assert torch.equal(c3, codes) and torch.equal(p3.view(-1), kq.pack_mxfp4_scales(scales).view(-1))
+
+
+def test_quantize_strided_and_plain_parameters(torch, kq):
+    """Padded input rows; no weight and no bias."""
+    x0 = rand(torch, 23, 1056, seed=9, dtype=torch.bfloat16)
+    x, _ = strided(torch, x0, 24)
+    a = kq.layernorm_quantize_mxfp4(x)
+    b = kq.layernorm_quantize_mxfp4(x0, torch.ones(1056, device="cuda"), torch.zeros(1056, device="cuda"))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_quantize_is_the_quantizer_of_the_norm(torch, kq):
+    """With T = I the codes are those of quantize_mxfp4_f32 on the 32-bit norm."""
+    x = rand(torch, 64, 2048, seed=4)
+    w, b = rand(torch, 2048, seed=1, shift=1.0), rand(torch, 2048, seed=2)
+    y = torch.empty(64, 2048, device="cuda")
+    codes, scales = kq.layernorm_quantize_mxfp4(x, w, b, y_debug=y)
+    c2, s2 = kq.quantize_mxfp4_f32(y)
+    assert torch.equal(codes, c2) and torch.equal(scales, s2)
+
+
+def test_refusals(torch, kq):
+    x = torch.zeros(4, 64, device="cuda")
+    v = torch.zeros(64, device="cuda")
+    with pytest.raises(TypeError):
+        kq.layernorm(x.half())
+    with pytest.raises(TypeError):
+        kq.layernorm(x, v.bfloat16())
+    with pytest.raises(ValueError):
+        kq.layernorm(x, v[:63])
+    with pytest.raises(ValueError):
+        kq.layernorm(x.t())
+    with pytest.raises(ValueError):
+        kq.layernorm(x[0])
+    with pytest.raises(TypeError):
+        kq.layernorm(x, out=x.bfloat16())
+    with pytest.raises(ValueError):
+        kq.layernorm(x, out=torch.zeros(4, 63, device="cuda"))
+    with pytest.raises(kq.KQError):
+        kq.layernorm(x, eps=-1.0)
+    with pytest.raises(kq.KQError):
+        kq.layernorm(x[:1].expand(4, 64))  # rows that overlap
+    with pytest.raises(ValueError):
+        kq.layernorm_backward(x, x, None, None)
+    with pytest.raises(TypeError):
+        kq.layernorm_backward(x.bfloat16(), x, v[:4], v[:4])
+    with pytest.raises(ValueError):
+        kq.layernorm_backward(x, x, v, v[:4])
+    with pytest.raises(ValueError):
+        kq.layernorm_backward(x, x, v[:4], v[:4], params=False, dbias=v)
+    with pytest.raises(kq.KQError):
+        kq.layernorm_backward(torch.zeros(40, 64, device="cuda"), torch.zeros(40, 64, device="cuda"),
+                              torch.zeros(40, device="cuda"), torch.zeros(40, device="cuda"),
+                              workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(kq.KQError):
+        kq.layernorm_quantize_mxfp4(torch.zeros(2, 48, device="cuda"))
+    with pytest.raises((ValueError, kq.KQError)):
+        kq.layernorm_quantize_mxfp4(x, packed=True)
+    with pytest.raises(ValueError):
+        kq.layernorm_quantize_mxfp4(x, factors=v)
