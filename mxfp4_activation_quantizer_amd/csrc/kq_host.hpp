@@ -52,6 +52,19 @@ inline kq_status launched() {
     return KQ_OK;
 }
 
+// Compute units of the current device (cached per device; 256 on MI355X).
+inline int compute_units() {
+    static int cached[64] = {0};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    if (!cached[dev]) {
+        int n = 0;
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+        cached[dev] = n;
+    }
+    return cached[dev];
+}
+
 // Partial sums kept for a sum over m rows (the gradients of a norm's parameters and of a
 // bias): 16 rows each, at most 512. A function of m alone, so that a workspace's size and
 // the order of the sums do not depend on the device.

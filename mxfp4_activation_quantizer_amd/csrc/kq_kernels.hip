@@ -143,102 +143,6 @@ __device__ __forceinline__ void store_row(const RowRes<YOUT> &r, RowOut &o, cons
     o.y += o.y_step;
 }
 
-// The block's 16 per-lane coefficients, written to LDS by wave 0.
-//
-// Shear form. Each factor splits exactly as G = S D with S = [[1, p], [q, 1]],
-// p = G01 / G11, q = G10 / G00, D = diag(G00, G11), and by the mixed-product
-// rule K = (S1 (x) ... (x) S5)(D1 (x) ... (x) D5): five unit-diagonal shear
-// stages, (x0, x1) -> (x0 + q x1, x1 + p x0), one fma per element each, then
-// one multiply per channel by the product of its five diagonal entries. Every
-// intermediate is the direct butterfly's intermediate divided by a
-// per-channel constant, so rounding errors stay relative to the same
-// quantities. The ratios use the hardware reciprocal (about 1 ulp): they are
-// coefficients of an exact refactoring, so a last-bit difference only moves y
-// by rounding. A block admits the form when every |p|, |q| <= 2^20 (a zero or
-// tiny diagonal entry, a swap say, gives an infinite, NaN or huge ratio).
-// Lane coefficients: c1 (G1, channel bit 4 = bit 1 of sub: this lane's
-// partner weight, q for bit 0 and p for bit 1), c2 (G2, bit 3), p3, q3, p4,
-// q4, p5, q5, then the 8 per-channel diagonal products.
-//
-// General form (any block of the segment without the shear form): the 2x2
-// stages y = x_self G[b][b] + x_partner G[1-b][b] (KronLane layout: s1, o1,
-// s2, o2, then G3, G4, G5 as 4 entries each).
-//
-// Every lane-dependent choice is an explicit select: a lane-dependent index
-// into the factor array would become a chain of compares and selects.
-struct SetupLane {
-    float p[5], q[5];
-    bool shear;
-};
-
-__device__ __forceinline__ void setup_ratios(const float f[20], SetupLane &S) {
-    const float lim = 0x1.0p20f;
-    S.shear = true;
-#pragma unroll
-    for (int k = 0; k < 5; ++k) {
-        S.p[k] = f[4 * k + 1] * __builtin_amdgcn_rcpf(f[4 * k + 3]);
-        S.q[k] = f[4 * k + 2] * __builtin_amdgcn_rcpf(f[4 * k]);
-        S.shear = S.shear && fabsf(S.p[k]) <= lim && fabsf(S.q[k]) <= lim;  // false for inf and NaN
-    }
-}
-
-__device__ __forceinline__ void write_shear_coefs(const float f[20], const SetupLane &S, int sub, float *dst) {
-    const bool b4 = (sub >> 1) & 1, b3 = sub & 1;
-    dst[0] = b4 ? S.p[0] : S.q[0];
-    dst[1] = b3 ? S.p[1] : S.q[1];
-#pragma unroll
-    for (int k = 2; k < 5; ++k) {
-        dst[2 * k - 2] = S.p[k];
-        dst[2 * k - 1] = S.q[k];
-    }
-    // diagonal product of channel (b4, b3, i2, i1, i0): ((d12 G3[i2][i2]) G4[i1][i1]) G5[i0][i0]
-    const float d12 = (b4 ? f[3] : f[0]) * (b3 ? f[7] : f[4]);
-    float t3[2], t4[4];
-#pragma unroll
-    for (int i2 = 0; i2 < 2; ++i2) t3[i2] = d12 * f[8 + 3 * i2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t4[i] = t3[i >> 1] * f[12 + 3 * (i & 1)];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dst[8 + i] = t4[i >> 1] * f[16 + 3 * (i & 1)];
-}
-
-__device__ __forceinline__ void write_general_coefs(const float f[20], int sub, float *dst) {
-    const bool b4 = (sub >> 1) & 1, b3 = sub & 1;
-    dst[0] = b4 ? f[3] : f[0];  // G1[b4][b4]
-    dst[1] = b4 ? f[1] : f[2];  // G1[1-b4][b4]
-    dst[2] = b3 ? f[7] : f[4];  // G2[b3][b3]
-    dst[3] = b3 ? f[5] : f[6];  // G2[1-b3][b3]
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        dst[4 + i] = f[8 + i];
-        dst[8 + i] = f[12 + i];
-        dst[12 + i] = f[16 + i];
-    }
-}
-
-template <bool SHEAR>
-__device__ __forceinline__ void apply_coefs(float y[8], const float c[16]) {
-    if (SHEAR) {
-        fmac_partner_xor2(y, c[0]);  // G1: channel bit 4 = bit 1 of sub
-        fmac_partner_xor1(y, c[1]);  // G2: channel bit 3 = bit 0 of sub
-        shear_stage<4>(y, c[2], c[3]);
-        shear_stage<2>(y, c[4], c[5]);
-        shear_stage<1>(y, c[6], c[7]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * c[8 + i];
-    } else {
-        KronLane L;
-        L.s1 = c[0]; L.o1 = c[1]; L.s2 = c[2]; L.o2 = c[3];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            L.g3[i] = c[4 + i];
-            L.g4[i] = c[8 + i];
-            L.g5[i] = c[12 + i];
-        }
-        kron_apply8(y, L);
-    }
-}
-
 // bf16 input, row-wave strips: SmoothQuant (T = diag(inv_scale)) or the
 // Kronecker transform. Each wave's U row loads are issued at once; for the
 // transform they are in flight while wave 0 derives the segment's

@@ -16,6 +16,9 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+#include <type_traits>
+
 #include "kq.h"
 #include "kq_device.hpp"
 #include "kq_host.hpp"
@@ -30,17 +33,44 @@ __device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_flo
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// Sum over a wave, the same value in every lane (xor tree: a fixed order).
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s, 64);
-    return v;
+// The value of v in the lane that differs: DPP patterns within 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s, 64);
-    return v;
+template <int CTRL>
+__device__ __forceinline__ double moved(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// v + its value 16 (then 32) lanes away, by the swaps of rows and half waves.
+__device__ __forceinline__ float sum_across_rows(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t s = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(s, s, false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+__device__ __forceinline__ double sum_across_rows(double v) {
+    auto join = [](uint32_t lo, uint32_t hi) { return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo); };
+    uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const auto pl = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+    const auto ph = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+    u = __builtin_bit_cast(uint64_t, join(pl[0], ph[0]) + join(pl[1], ph[1]));
+    const auto ql = __builtin_amdgcn_permlane32_swap((uint32_t)u, (uint32_t)u, false, false);
+    const auto qh = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+    return join(ql[0], qh[0]) + join(ql[1], qh[1]);
+}
+// Sum over a wave, the same value in every lane (a fixed tree).
+template <class V>
+__device__ __forceinline__ V wave_sum(V v) {
+    v += moved<0xB1>(v);   // quad_perm [1,0,3,2]
+    v += moved<0x4E>(v);   // quad_perm [2,3,0,1]
+    v += moved<0x141>(v);  // mirrored within 8 lanes
+    v += moved<0x140>(v);  // mirrored within 16 lanes
+    return sum_across_rows(v);
 }
 
 // Sum over a workgroup of 4 waves, in every thread.
@@ -58,13 +88,13 @@ __device__ __forceinline__ V block_sum(V v) {
 struct Stats {
     float c, off, rstd;
     __device__ __forceinline__ float centred(float x) const { return (x - c) - off; }
-    __device__ __forceinline__ void set_mean(double sum, int64_t d) {
-        const double mean = sum / (double)d;
+    __device__ __forceinline__ void set_mean(double sum, double inv) {
+        const double mean = sum * inv;
         c = (float)mean;
         off = (float)(mean - c);
     }
-    __device__ __forceinline__ void set_rstd(float squares, int64_t d, float eps) {
-        rstd = 1.0f / sqrtf(squares / (float)d + eps);
+    __device__ __forceinline__ void set_rstd(float squares, double inv, float eps) {
+        rstd = __builtin_amdgcn_rsqf(fmaf(squares, (float)inv, eps));  // 1 ulp
     }
 };
 
@@ -72,15 +102,16 @@ struct Stats {
 template <class T>
 __device__ __forceinline__ Stats row_stats(const T *x, int64_t d, float eps) {
     Stats st;
+    const double inv = 1.0 / (double)d;
     double s = 0.0;
     for (int64_t c = threadIdx.x; c < d; c += kThreads) s += (double)load1(x + c);
-    st.set_mean(block_sum(s), d);
+    st.set_mean(block_sum(s), inv);
     float q = 0.f;
     for (int64_t c = threadIdx.x; c < d; c += kThreads) {
         const float v = st.centred(load1(x + c));
         q = fmaf(v, v, q);
     }
-    st.set_rstd(block_sum(q), d, eps);
+    st.set_rstd(block_sum(q), inv, eps);
     return st;
 }
 
@@ -152,13 +183,15 @@ __global__ __launch_bounds__(kThreads) void backward_params_any_kernel(
     if (pb) pb[p * d + c] = sb;
 }
 
-// out[c] = sum over p of part[p][c], p ascending in four interleaved chains (one per
-// wave of the workgroup), then the chains: 64 columns per workgroup, y = 0 for the first
-// output, 1 for the second.
-__global__ __launch_bounds__(kThreads) void reduce_parts_kernel(const float *__restrict__ part0,
-                                                                const float *__restrict__ part1, int parts, int64_t d,
-                                                                float *__restrict__ out0, float *__restrict__ out1) {
-    __shared__ float red[4][64];
+// out[c] = sum over p of part[p][c]: 64 columns per workgroup, wave w adds the parts w,
+// w + 16, ... in turn, then the 16 sums in wave order; y = 0 for the first output, 1 for
+// the second.
+constexpr int kChains = 16;
+__global__ __launch_bounds__(64 * kChains) void reduce_parts_kernel(const float *__restrict__ part0,
+                                                                    const float *__restrict__ part1, int parts,
+                                                                    int64_t d, float *__restrict__ out0,
+                                                                    float *__restrict__ out1) {
+    __shared__ float red[kChains][64];
     const float *part = blockIdx.y ? part1 : part0;
     float *out = blockIdx.y ? out1 : out0;
     if (!out) return;
@@ -166,19 +199,25 @@ __global__ __launch_bounds__(kThreads) void reduce_parts_kernel(const float *__r
     for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < d; c0 += (int64_t)gridDim.x * 64) {
         const int64_t c = c0 + lane;
         float s = 0.f;
-        if (c < d)
-            for (int p = w; p < parts; p += 4) s += part[p * d + c];
+        if (c < d) {
+#pragma unroll 8
+            for (int p = w; p < parts; p += kChains) s += part[p * d + c];
+        }
         red[w][lane] = s;
         __syncthreads();
-        if (w == 0 && c < d) out[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        if (w == 0 && c < d) {
+#pragma unroll
+            for (int i = 1; i < kChains; ++i) s += red[i][lane];
+            out[c] = s;
+        }
         __syncthreads();
     }
 }
 
-// Layer norm, transform and quantizer: one workgroup per row, a quad of lanes per
-// 32-channel block (8 channels per lane).
+// Layer norm, transform and quantizer of rows wider than the vector path holds: one
+// workgroup per row, a quad of lanes per 32-channel block, the row read three times.
 template <class T>
-__global__ __launch_bounds__(kThreads) void quantize_kernel(const T *__restrict__ X, int64_t m, int64_t d,
+__global__ __launch_bounds__(kThreads) void quantize_wide_kernel(const T *__restrict__ X, int64_t m, int64_t d,
                                                             int64_t ldx, const float *__restrict__ w,
                                                             const float *__restrict__ b, float eps,
                                                             const float *__restrict__ factors,
@@ -223,6 +262,401 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const T *__restrict_
     }
 }
 
+// ---------------------------------------------------------------------------
+// Vector path: rows of whole 16-byte pieces, up to 16384 channels, held in
+// registers from one read. A row belongs to W waves; lane l of wave w holds the
+// C chunks of 8 channels at 8 (64 (W c + w) + l), c < C, so every access of a
+// wave is one contiguous run (1 KB of bf16). Only chunk C - 1 can lie past the
+// row's end: it reads zeros and its stores are dropped (record counts of the
+// row's bytes), and its centred values are left out of the sum of squares.
+// Rows are walked by a persistent grid, so the parameters (fp32, four times the
+// bytes of a bf16 row) are loaded once per workgroup, and the next row's loads
+// are in flight while a row is summed. With W = 1 a workgroup's 4 waves walk
+// rows of their own and there is no barrier in the loop.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void *p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
+}
+
+// Eight neighbouring channels as they are loaded.
+template <class T>
+struct Chunk;
+template <>
+struct Chunk<uint16_t> {
+    u32x4_t q;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
+        q = __builtin_amdgcn_raw_buffer_load_b128(r, 2 * ch, 0, 0);
+    }
+    __device__ __forceinline__ void widen(float x[8]) const { widen8(make_uint4(q[0], q[1], q[2], q[3]), x); }
+};
+template <>
+struct Chunk<float> {
+    u32x4_t a, b;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
+        a = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * ch, 0, 0);
+        b = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * ch + 16, 0, 0);
+    }
+    __device__ __forceinline__ void widen(float x[8]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[e] = __uint_as_float(a[e]);
+            x[4 + e] = __uint_as_float(b[e]);
+        }
+    }
+};
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const bf16x2_t v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const uint16_t *) {
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                   pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])},
+                                           r, 2 * ch, 0, 0);
+}
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const float *) {
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{__float_as_uint(y[0]), __float_as_uint(y[1]),
+                                                   __float_as_uint(y[2]), __float_as_uint(y[3])},
+                                           r, 4 * ch, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{__float_as_uint(y[4]), __float_as_uint(y[5]),
+                                                   __float_as_uint(y[6]), __float_as_uint(y[7])},
+                                           r, 4 * ch + 16, 0, 0);
+}
+
+// Parameters of a lane's chunk (fp32; `none` where there are none or past d).
+__device__ __forceinline__ void load_params(const float *p, int64_t ch, int64_t d, float none, float v[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = none;
+    if (p && ch < d) {
+        const float4 a = *reinterpret_cast<const float4 *>(p + ch), b = *reinterpret_cast<const float4 *>(p + ch + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+}
+
+// Sum of v over the W waves of a row, in every lane; `red` belongs to this sum alone and
+// is written again only after another row_sum's barrier.
+template <int W, class V>
+__device__ __forceinline__ V row_sum(V v, V *red, int wave) {
+    v = wave_sum(v);
+    if (W == 1) return v;
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    V s = red[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) s += red[w];
+    return s;
+}
+
+template <int W>
+constexpr int kGroupThreads = W == 1 ? 256 : 64 * W;
+
+// A row's statistics from its chunks.
+template <class T, int W, int C>
+__device__ __forceinline__ Stats chunk_stats(const Chunk<T> (&raw)[C], bool last, int64_t d, double inv, float eps,
+                                             double *red_sum, float *red_sq, int wave) {
+    double s = 0.0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        float x[8];
+        raw[c].widen(x);
+        if (sizeof(T) == 2) {
+            // eight bf16 values add up exactly in fp32 unless their exponents differ by 13 or more
+            s += (double)(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += (double)x[e];
+        }
+    }
+    Stats st;
+    st.set_mean(row_sum<W>(s, red_sum, wave), inv);
+    float q = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        float x[8], qc = 0.f;
+        raw[c].widen(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float v = st.centred(x[e]);
+            qc = fmaf(v, v, qc);
+        }
+        q += c < C - 1 || last ? qc : 0.f;
+    }
+    st.set_rstd(row_sum<W>(q, red_sq, wave), inv, eps);
+    return st;
+}
+
+template <class T, int W, int C>
+__global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__restrict__ X, int64_t m, int64_t d,
+                                                                   int64_t ldx, const float *__restrict__ w,
+                                                                   const float *__restrict__ b, float eps,
+                                                                   T *__restrict__ Y, int64_t ldy,
+                                                                   float *__restrict__ mean,
+                                                                   float *__restrict__ rstd) {
+    __shared__ double red_sum[W];
+    __shared__ float red_sq[W];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wr = W == 1 ? 0 : wave;  // this wave's place in its row
+    constexpr int R = W == 1 ? 4 : 1;  // rows a workgroup has at a time
+    const int64_t step = (int64_t)gridDim.x * R;
+    int64_t row = (int64_t)blockIdx.x * R + (W == 1 ? wave : 0);
+    if (row >= m) return;  // whole waves, and with W > 1 whole workgroups
+    uint32_t ch[C];
+    float pw[C][8], pb[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        ch[c] = 8u * (64u * (W * c + wr) + lane);
+        load_params(w, ch[c], d, 1.0f, pw[c]);
+        load_params(b, ch[c], d, 0.0f, pb[c]);
+    }
+    const bool last = ch[C - 1] < d;
+    const double inv = 1.0 / (double)d;
+    const int64_t bytes = d * (int)sizeof(T);
+    Chunk<T> raw[C], next[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) next[c].load(row_rsrc(X + row * ldx, bytes), ch[c]);
+    for (; row < m; row += step) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) raw[c] = next[c];
+        // past the last row: no records, so no access
+        const auto ahead = row_rsrc(X + (row + step < m ? row + step : row) * ldx, row + step < m ? bytes : 0);
+#pragma unroll
+        for (int c = 0; c < C; ++c) next[c].load(ahead, ch[c]);
+        const Stats st = chunk_stats<T, W, C>(raw, last, d, inv, eps, red_sum, red_sq, wr);
+        const auto out = row_rsrc(Y + row * ldy, bytes);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float x[8];
+            raw[c].widen(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = fmaf(st.centred(x[e]) * st.rstd, pw[c][e], pb[c][e]);
+            store8(out, ch[c], x, Y);
+        }
+        if (lane == 0 && wr == 0) {
+            if (mean) mean[row] = st.c;
+            if (rstd) rstd[row] = st.rstd;
+        }
+    }
+}
+
+// Workgroup p of the backward pass walks the rows p, p + parts, ... (with W = 1, every fourth
+// of them per wave), writes their dx and keeps its lanes' columns of dweight and dbias in
+// registers; row p of the partial sums gets them at the end.
+template <class T, int W, int C>
+__global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__restrict__ dY, int64_t lddy,
+                                                                    const T *__restrict__ X, int64_t ldx, int64_t m,
+                                                                    int64_t d, const float *__restrict__ w,
+                                                                    const float *__restrict__ mean,
+                                                                    const float *__restrict__ rstd,
+                                                                    T *__restrict__ dX, int64_t lddx, int parts,
+                                                                    float *__restrict__ pw, float *__restrict__ pb) {
+    __shared__ float red[2][2][W];
+    __shared__ float4 join[W == 1 ? 4 : 1][W == 1 ? C : 1][2][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wr = W == 1 ? 0 : wave;
+    constexpr int R = W == 1 ? 4 : 1;
+    const int64_t p = blockIdx.x, step = (int64_t)parts * R;
+    int64_t row = p + (W == 1 ? (int64_t)parts * wave : 0);
+    uint32_t ch[C];
+    float wv[C][8], aw[C][8], ab[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        ch[c] = 8u * (64u * (W * c + wr) + lane);
+        load_params(w, ch[c], d, 1.0f, wv[c]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) aw[c][e] = ab[c][e] = 0.f;
+    }
+    const float inv = 1.0f / (float)d;
+    const int64_t bytes = d * (int)sizeof(T);
+    Chunk<T> x[C], dy[C], nx[C], ndy[C];
+    float mu = 0.f, rs = 0.f, nmu = 0.f, nrs = 0.f;
+    auto fetch = [&](int64_t r) {
+        const bool in = r < m;
+        const int64_t rr = in ? r : 0;
+        const auto rx = row_rsrc(X + rr * ldx, in ? bytes : 0), rd = row_rsrc(dY + rr * lddy, in ? bytes : 0);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            nx[c].load(rx, ch[c]);
+            ndy[c].load(rd, ch[c]);
+        }
+        nmu = mean[rr];
+        nrs = rstd[rr];
+    };
+    fetch(row);
+    for (int par = 0; row < m; row += step, par ^= 1) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            x[c] = nx[c];
+            dy[c] = ndy[c];
+        }
+        mu = nmu;
+        rs = nrs;
+        fetch(row + step);
+        float g[C][8], h[C][8], a = 0.f, b = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float v[8], t[8];
+            x[c].widen(v);
+            dy[c].widen(t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                h[c][e] = (v[e] - mu) * rs;
+                g[c][e] = t[e] * wv[c][e];
+                aw[c][e] = fmaf(t[e], h[c][e], aw[c][e]);
+                ab[c][e] += t[e];
+                a += g[c][e];
+                b = fmaf(g[c][e], h[c][e], b);
+            }
+        }
+        a = wave_sum(a);
+        b = wave_sum(b);
+        if (W > 1) {
+            // two sets in turn: a set is written again only after the next row's barrier
+            if (lane == 0) {
+                red[par][0][wr] = a;
+                red[par][1][wr] = b;
+            }
+            __syncthreads();
+            a = red[par][0][0];
+            b = red[par][1][0];
+#pragma unroll
+            for (int i = 1; i < W; ++i) {
+                a += red[par][0][i];
+                b += red[par][1][i];
+            }
+        }
+        a *= inv;
+        b *= inv;
+        const auto out = row_rsrc(dX + row * lddx, bytes);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float t[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = rs * fmaf(-h[c][e], b, g[c][e] - a);
+            store8(out, ch[c], t, dX);
+        }
+    }
+    // with W = 1, the four waves' columns meet in LDS, in wave order
+    auto put = [&](float (&v)[C][8], float *to) {
+        if (!to) return;
+        to += p * d;
+        if (W > 1) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (ch[c] < d) {
+                    *reinterpret_cast<float4 *>(to + ch[c]) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+                    *reinterpret_cast<float4 *>(to + ch[c] + 4) = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
+                }
+            return;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            join[wave][c][0][lane] = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+            join[wave][c][1][lane] = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
+        }
+        __syncthreads();
+        for (int i = wave; i < 2 * C; i += 4) {
+            float4 s = join[0][i >> 1][i & 1][lane];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) {
+                const float4 o = join[k][i >> 1][i & 1][lane];
+                s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
+            }
+            const uint32_t cc = 8u * (64u * (i >> 1) + lane) + 4u * (i & 1);
+            if (cc < d) *reinterpret_cast<float4 *>(to + cc) = s;
+        }
+    };
+    put(aw, pw);
+    put(ab, pb);
+}
+
+// Layer norm, transform and quantizer (vector path). A quad of lanes holds a 32-channel block and a wave's
+// chunk 16 of them (the segments of the fused transform kernels), for which every lane keeps
+// its block's 16 coefficients and its channels' parameters over all rows of the workgroup.
+template <class T, int W, int C>
+__global__ __launch_bounds__(kGroupThreads<W>) void quantize_kernel(
+    const T *__restrict__ X, int64_t m, int64_t d, int64_t ldx, const float *__restrict__ w,
+    const float *__restrict__ b, float eps, const float *__restrict__ factors, uint8_t *__restrict__ codes,
+    uint8_t *__restrict__ scales, int packed, float *__restrict__ y_debug, float *__restrict__ mean,
+    float *__restrict__ rstd) {
+    __shared__ double red_sum[W];
+    __shared__ float red_sq[W];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wr = W == 1 ? 0 : wave, sub = lane & 3;
+    constexpr int R = W == 1 ? 4 : 1;
+    const int64_t step = (int64_t)gridDim.x * R;
+    int64_t row = (int64_t)blockIdx.x * R + (W == 1 ? wave : 0);
+    if (row >= m) return;
+    uint32_t ch[C];
+    float pw[C][8], pb[C][8], coef[C][16];
+    bool shear[C];
+    const double inv = 1.0 / (double)d;
+    const int64_t bytes = d * (int)sizeof(T);
+    Chunk<T> raw[C], next[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        ch[c] = 8u * (64u * (W * c + wr) + lane);
+        next[c].load(row_rsrc(X + row * ldx, bytes), ch[c]);
+    }
+    const bool last = ch[C - 1] < d;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        load_params(w, ch[c], d, 1.0f, pw[c]);
+        load_params(b, ch[c], d, 0.0f, pb[c]);
+        shear[c] = true;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) coef[c][i] = 0.f;
+        if (factors) {
+            const bool in = ch[c] < d;
+            float f[20];
+            SetupLane S;
+            S.shear = true;
+            if (in) {
+                load_factors20(factors + (int64_t)(ch[c] / 32) * 20, f);
+                setup_ratios(f, S);
+            }
+            shear[c] = __builtin_amdgcn_ballot_w64(!S.shear) == 0;
+            if (in) {
+                if (shear[c]) write_shear_coefs(f, S, sub, coef[c]);
+                else write_general_coefs(f, sub, coef[c]);
+            }
+        }
+    }
+    for (; row < m; row += step) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) raw[c] = next[c];
+        const auto ahead = row_rsrc(X + (row + step < m ? row + step : row) * ldx, row + step < m ? bytes : 0);
+#pragma unroll
+        for (int c = 0; c < C; ++c) next[c].load(ahead, ch[c]);
+        const Stats st = chunk_stats<T, W, C>(raw, last, d, inv, eps, red_sum, red_sq, wr);
+        const auto rc = row_rsrc(codes + row * (d / 2), d / 2);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float y[8];
+            raw[c].widen(y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = fmaf(st.centred(y[e]) * st.rstd, pw[c][e], pb[c][e]);
+            if (factors) {
+                if (shear[c]) apply_coefs<true>(y, coef[c]);
+                else apply_coefs<false>(y, coef[c]);
+            }
+            uint32_t sbyte;
+            const uint32_t q = quantize_quad_f32(y, sbyte);
+            __builtin_amdgcn_raw_buffer_store_b32(q, rc, ch[c] / 2, 0, 0);
+            if (sub == 0 && ch[c] < d) {
+                const int64_t j = ch[c] / 32;
+                scales[packed ? ((j >> 3) * m + row) * 8 + 4 * (j & 1) + ((j & 7) >> 1) : row * (d / 32) + j] =
+                    (uint8_t)sbyte;
+            }
+            if (y_debug) store8(row_rsrc(y_debug + row * d, 4 * d), ch[c], y, y_debug);
+        }
+        if (lane == 0 && wr == 0) {
+            if (mean) mean[row] = st.c;
+            if (rstd) rstd[row] = st.rstd;
+        }
+    }
+}
+
 }  // namespace norm
 }  // namespace kq
 
@@ -242,6 +676,105 @@ uintptr_t size_of(int type) { return type == KQ_BF16 ? 2 : 4; }
 // Workgroups that walk m rows: enough to fill the chip, the rest by stride.
 unsigned row_grid(int64_t m) { return (unsigned)(m < 65536 ? m : 65536); }
 
+// Rows in whole 16-byte pieces of at most 16384 channels: the vector path.
+bool vector_rows(int type, int64_t d, std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> lds,
+                 std::initializer_list<const float *> params) {
+    if (d % 8 != 0 || d > 16384) return false;
+    for (const void *p : ptrs)
+        if (!aligned(p, 16)) return false;
+    for (const int64_t ld : lds)
+        if (ld % (type == KQ_BF16 ? 8 : 4) != 0) return false;
+    for (const float *p : params)
+        if (!aligned(p, 16)) return false;
+    return true;
+}
+
+// Waves per row and chunks per lane. Many rows: the fewest waves that hold the row at `most`
+// chunks per lane, so that a wave has work between its sums. Rows too few to give every
+// compute unit one: one chunk per lane where 16 waves reach, so that a row's time is one
+// memory latency.
+struct RowShape {
+    int waves, chunks;
+};
+RowShape row_shape(int64_t m, int64_t d, int most) {
+    const int64_t pieces = (d + 511) / 512;  // wave-wide chunks of the row
+    const bool few = m < kqhost::compute_units();
+    RowShape s{1, 0};
+    while (s.waves < (few ? 16 : 8) && pieces > s.waves * (few ? 1 : most)) s.waves *= 2;
+    s.chunks = (int)((pieces + s.waves - 1) / s.waves);
+    return s;
+}
+
+// Calls f(W, C) (integral constants) with the shape; false if it is not built.
+template <class F>
+bool with_shape(RowShape s, F f) {
+    using std::integral_constant;
+#define KQ_SHAPE(W, C) \
+    if (s.waves == W && s.chunks == C) return f(integral_constant<int, W>(), integral_constant<int, C>()), true;
+    KQ_SHAPE(1, 1) KQ_SHAPE(1, 2) KQ_SHAPE(2, 1) KQ_SHAPE(2, 2) KQ_SHAPE(4, 1) KQ_SHAPE(4, 2)
+    KQ_SHAPE(8, 1) KQ_SHAPE(8, 2) KQ_SHAPE(8, 3) KQ_SHAPE(8, 4) KQ_SHAPE(16, 1) KQ_SHAPE(16, 2)
+#undef KQ_SHAPE
+    return false;
+}
+
+// Workgroups of `waves` waves (4 rows at a time when waves == 1) that keep `per_cu` waves on
+// every compute unit, or one per row where there are fewer.
+unsigned persistent_grid(int64_t m, int waves, int per_cu) {
+    const int64_t rows = waves == 1 ? 4 : 1, need = (m + rows - 1) / rows;
+    const int64_t fill = (int64_t)kqhost::compute_units() * per_cu / (waves == 1 ? 4 : waves);
+    return (unsigned)(need < fill ? need : fill);
+}
+
+template <class T>
+kq_status launch_forward(const void *X, int64_t m, int64_t d, int64_t ldx, const float *weight, const float *bias,
+                         float eps, void *Y, int64_t ldy, float *mean, float *rstd, bool vec, kq_stream_t stream) {
+    const RowShape s = row_shape(m, d, 2);
+    if (!vec || !with_shape(s, [&](auto W, auto C) {
+            hipLaunchKernelGGL((kq::norm::forward_kernel<T, W(), C()>), dim3(persistent_grid(m, s.waves, 16)),
+                               dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx,
+                               weight, bias, eps, (T *)Y, ldy, mean, rstd);
+        }))
+        hipLaunchKernelGGL((kq::norm::forward_any_kernel<T>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
+                           (hipStream_t)stream, (const T *)X, m, d, ldx, weight, bias, eps, (T *)Y, ldy, mean, rstd);
+    return launched();
+}
+
+template <class T>
+kq_status launch_backward(const void *dY, int64_t lddy, const void *X, int64_t ldx, int64_t m, int64_t d,
+                          const float *weight, const float *mean, const float *rstd, void *dX, int64_t lddx,
+                          int64_t parts, float *pw, float *pb, bool params, bool vec, kq_stream_t stream) {
+    if (vec && with_shape(row_shape(parts, d, 2), [&](auto W, auto C) {
+            hipLaunchKernelGGL((kq::norm::backward_kernel<T, W(), C()>), dim3((unsigned)parts),
+                               dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)dY, lddy,
+                               (const T *)X, ldx, m, d, weight, mean, rstd, (T *)dX, lddx, (int)parts, pw, pb);
+        }))
+        return launched();
+    hipLaunchKernelGGL((kq::norm::backward_dx_any_kernel<T>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
+                       (hipStream_t)stream, (const T *)dY, lddy, (const T *)X, ldx, m, d, weight, mean, rstd, (T *)dX,
+                       lddx);
+    if (params)
+        hipLaunchKernelGGL((kq::norm::backward_params_any_kernel<T>), dim3((unsigned)((d + 255) / 256), (unsigned)parts),
+                           dim3(kq::norm::kThreads), 0, (hipStream_t)stream, (const T *)dY, lddy, (const T *)X, ldx, m,
+                           d, mean, rstd, (int)parts, pw, pb);
+    return launched();
+}
+
+template <class T>
+kq_status launch_quantize(const void *X, int64_t m, int64_t d, int64_t ldx, const float *weight, const float *bias,
+                          float eps, const float *factors, uint8_t *codes, uint8_t *scales, int packed, float *y_debug,
+                          float *mean, float *rstd, kq_stream_t stream) {
+    const RowShape s = row_shape(m, d, 2);
+    if (d > 16384 || !with_shape(s, [&](auto W, auto C) {
+            hipLaunchKernelGGL((kq::norm::quantize_kernel<T, W(), C()>), dim3(persistent_grid(m, s.waves, 16)),
+                               dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx,
+                               weight, bias, eps, factors, codes, scales, packed, y_debug, mean, rstd);
+        }))
+        hipLaunchKernelGGL((kq::norm::quantize_wide_kernel<T>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
+                           (hipStream_t)stream, (const T *)X, m, d, ldx, weight, bias, eps, factors, codes, scales,
+                           packed, y_debug, mean, rstd);
+    return launched();
+}
+
 }  // namespace
 
 namespace kqhost {
@@ -250,7 +783,7 @@ kq_status reduce_parts(const float *part0, const float *part1, int64_t parts, in
                        kq_stream_t stream) {
     const int64_t groups = (d + 63) / 64;
     hipLaunchKernelGGL(kq::norm::reduce_parts_kernel, dim3((unsigned)(groups < 65536 ? groups : 65536), out1 ? 2 : 1),
-                       dim3(kq::norm::kThreads), 0, (hipStream_t)stream, part0, part1, (int)parts, d, out0, out1);
+                       dim3(64 * kq::norm::kChains), 0, (hipStream_t)stream, part0, part1, (int)parts, d, out0, out1);
     return launched();
 }
 
@@ -269,15 +802,10 @@ kq_status kq_layernorm(const void *X, int type, int64_t m, int64_t d, int64_t ld
     if (!aligned(X, es) || !aligned(Y, es) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) ||
         !aligned(rstd, 4))
         return KQ_ERR_ALIGN;
-    if (type == KQ_BF16)
-        hipLaunchKernelGGL((kq::norm::forward_any_kernel<uint16_t>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
-                           (hipStream_t)stream, (const uint16_t *)X, m, d, ldx, weight, bias, eps, (uint16_t *)Y, ldy,
-                           mean, rstd);
-    else
-        hipLaunchKernelGGL((kq::norm::forward_any_kernel<float>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
-                           (hipStream_t)stream, (const float *)X, m, d, ldx, weight, bias, eps, (float *)Y, ldy, mean,
-                           rstd);
-    return launched();
+    const bool vec = vector_rows(type, d, {X, Y}, {ldx, ldy}, {weight, bias});
+    return type == KQ_BF16
+               ? launch_forward<uint16_t>(X, m, d, ldx, weight, bias, eps, Y, ldy, mean, rstd, vec, stream)
+               : launch_forward<float>(X, m, d, ldx, weight, bias, eps, Y, ldy, mean, rstd, vec, stream);
 }
 
 kq_status kq_layernorm_backward_workspace_bytes(int64_t m, int64_t d, int64_t *bytes) {
@@ -314,26 +842,15 @@ kq_status kq_layernorm_backward(const void *dY, int64_t lddy, const void *X, int
         pw = static_cast<float *>(workspace);
         pb = pw + parts * d;
     }
-    const dim3 pgrid((unsigned)((d + 255) / 256), (unsigned)parts);
-    if (type == KQ_BF16) {
-        hipLaunchKernelGGL((kq::norm::backward_dx_any_kernel<uint16_t>), dim3(row_grid(m)), dim3(kq::norm::kThreads),
-                           0, (hipStream_t)stream, (const uint16_t *)dY, lddy, (const uint16_t *)X, ldx, m, d, weight,
-                           mean, rstd, (uint16_t *)dX, lddx);
-        if (params)
-            hipLaunchKernelGGL((kq::norm::backward_params_any_kernel<uint16_t>), pgrid, dim3(kq::norm::kThreads), 0,
-                               (hipStream_t)stream, (const uint16_t *)dY, lddy, (const uint16_t *)X, ldx, m, d, mean,
-                               rstd, (int)parts, pw, pb);
-    } else {
-        hipLaunchKernelGGL((kq::norm::backward_dx_any_kernel<float>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
-                           (hipStream_t)stream, (const float *)dY, lddy, (const float *)X, ldx, m, d, weight, mean,
-                           rstd, (float *)dX, lddx);
-        if (params)
-            hipLaunchKernelGGL((kq::norm::backward_params_any_kernel<float>), pgrid, dim3(kq::norm::kThreads), 0,
-                               (hipStream_t)stream, (const float *)dY, lddy, (const float *)X, ldx, m, d, mean, rstd,
-                               (int)parts, pw, pb);
-    }
+    const bool vec = vector_rows(type, d, {dY, X, dX}, {lddy, ldx, lddx}, {weight, pw, pb});
+    const kq_status s =
+        type == KQ_BF16 ? launch_backward<uint16_t>(dY, lddy, X, ldx, m, d, weight, mean, rstd, dX, lddx, parts, pw,
+                                                    pb, params, vec, stream)
+                        : launch_backward<float>(dY, lddy, X, ldx, m, d, weight, mean, rstd, dX, lddx, parts, pw, pb,
+                                                 params, vec, stream);
+    if (s != KQ_OK) return s;
     if (params && parts > 1) return kqhost::reduce_parts(pw, pb, parts, d, dweight, dbias, stream);
-    return launched();
+    return KQ_OK;
 }
 
 kq_status kq_layernorm_quantize_mxfp4(const void *X, int type, int64_t m, int64_t d, int64_t ldx, const float *weight,
@@ -349,15 +866,11 @@ kq_status kq_layernorm_quantize_mxfp4(const void *X, int type, int64_t m, int64_
         !aligned(factors, 16) || !aligned(codes, 16) || !aligned(y_debug, 16) || !aligned(mean, 4) ||
         !aligned(rstd, 4))
         return KQ_ERR_ALIGN;
-    if (type == KQ_BF16)
-        hipLaunchKernelGGL((kq::norm::quantize_kernel<uint16_t>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
-                           (hipStream_t)stream, (const uint16_t *)X, m, d, ldx, weight, bias, eps, factors, codes,
-                           scales, packed, y_debug, mean, rstd);
-    else
-        hipLaunchKernelGGL((kq::norm::quantize_kernel<float>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
-                           (hipStream_t)stream, (const float *)X, m, d, ldx, weight, bias, eps, factors, codes, scales,
-                           packed, y_debug, mean, rstd);
-    return launched();
+    return type == KQ_BF16
+               ? launch_quantize<uint16_t>(X, m, d, ldx, weight, bias, eps, factors, codes, scales, packed, y_debug,
+                                           mean, rstd, stream)
+               : launch_quantize<float>(X, m, d, ldx, weight, bias, eps, factors, codes, scales, packed, y_debug, mean,
+                                        rstd, stream);
 }
 
 }  // extern "C"
