@@ -54,6 +54,7 @@
 #include <type_traits>
 
 #include "kq.h"
+#include "kq_act.hpp"
 #include "kq_cvt.hpp"
 #include "kq_device.hpp"
 #include "kq_host.hpp"
@@ -93,6 +94,15 @@ struct Geom {
     int rows16;   // O 16-byte aligned and ldo esz % 16 == 0: output rows staged through LDS
     int r;        // rank of the low-rank term (LR kernels)
     TileOrder order;  // which tile, or half tile, each workgroup computes
+};
+
+// The epilogue of kq_mxfp4_linear: z = sum + bias, O = act(z) + residual, z kept if asked.
+struct Epi {
+    const float *bias;       // or NULL
+    const void *residual;    // O's type, or NULL
+    void *Z;                 // O's type, or NULL
+    int64_t ldr, ldz;
+    int act;
 };
 
 __device__ __forceinline__ int swz8(int r) { return (r & 7) ^ ((r >> 3) & 1); }
@@ -169,14 +179,19 @@ typedef float floatx4_t __attribute__((ext_vector_type(4)));
 //
 // B16: O is written in bf16 (each fp32 sum rounded to nearest even) instead of fp32.
 //
+// EPI: the sums leave through the epilogue `ep`. With NS the last stage may then be part
+// of one (k % 128 == 0): chunks and scales past k are pushed past the record counts and
+// read zeros.
+//
 // One tile (run-order number u; half h of it when TN = 128) of one workgroup;
 // smem holds 2 stages of the full-width layout plus 1 KB.
-template <bool LR, int TN, bool B16, bool LRS = false, bool NS = false>
+template <bool LR, int TN, bool B16, bool LRS = false, bool NS = false, bool EPI = false>
 __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, const uint8_t *__restrict__ psa,
                                              const uint8_t *__restrict__ cw, const uint8_t *__restrict__ psw,
                                              const Geom g, const void *__restrict__ lr0,
                                              const void *__restrict__ lr1, const void *__restrict__ lr2,
-                                             void *__restrict__ O, int u, int h, uint8_t *smem) {
+                                             void *__restrict__ O, int u, int h, uint8_t *smem,
+                                             const Epi &ep = Epi()) {
     static_assert(TN == 256 || TN == 128, "tile width");
     using L = Lay<TN>;
     constexpr int NB = L::NB, LW = L::LW;
@@ -201,8 +216,10 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     // read stays inside the packed array: a padding row past m or n reads a
     // later stage's bytes (harmless: its codes are zero and its outputs are
     // never stored), or zero on the last stage
-    const i32x4_t dsa = sdesc(psa, (uint32_t)(g.stages * 8 * g.m));
-    const i32x4_t dsw = sdesc(psw, (uint32_t)(g.stages * 8 * g.n));
+    constexpr bool kTail = NS && EPI;
+    const int kblocks = kTail ? g.kbytes / 16 : 8 * g.stages;
+    const i32x4_t dsa = sdesc(psa, (uint32_t)(kblocks * g.m));
+    const i32x4_t dsw = sdesc(psw, (uint32_t)(kblocks * g.n));
     // (NS) scales in the MX layout [rows][k / 32]: row i's eight bytes of stage s at
     // (k / 32) i + 8 s, blocks in order; same record counts (k / 32 = 8 stages)
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
@@ -220,12 +237,17 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
         const int row = (TN / 4) * w + 8 * j + (lane >> 3);
         cvoffw[j] = (uint32_t)(row * g.kbytes) + 16u * (uint32_t)((lane & 7) ^ swz8(row & 15));
     }
+    // (kTail) the lane's chunk of an even and of an odd load (rows of a load start at
+    // multiples of 8, so row & 15 is 8 (j & 1) + lane / 8)
+    const int tail_chunk[2] = {(lane & 7) ^ swz8(lane >> 3), (lane & 7) ^ swz8(8 + (lane >> 3))};
     // loads of stage s: i in 0..7 A codes, 8..8 + LW - 1 W codes
     auto issue_code = [&](int s, int i) {
         const uint32_t st = lds0 + (uint32_t)((s & 1) * kStage);
         const uint32_t kb = 128u * (uint32_t)s;
-        if (i < 8) dma16(dca, st + (64 * w + 8 * i) * 128, cvoff[i], kb);
-        else dma16(dcw, st + L::kOffW + ((TN / 4) * w + 8 * (i - 8)) * 128, cvoffw[i - 8], kb);
+        uint32_t off = i < 8 ? cvoff[i & 7] : cvoffw[(i - 8) & (LW - 1)];
+        if (kTail) off = 128 * s + 16 * tail_chunk[i & 1] < g.kbytes ? off : 0x80000000u;
+        if (i < 8) dma16(dca, st + (64 * w + 8 * i) * 128, off, kb);
+        else dma16(dcw, st + L::kOffW + ((TN / 4) * w + 8 * (i - 8)) * 128, off, kb);
     };
     // scales of stage s, 1 KB per load: A rows 128 (w & 1) .. by waves 0 and 1, W rows
     // 128 (w & 1) .. by waves 2 and 3 (TN = 256) or all TN rows by wave 2 (TN = 128;
@@ -240,10 +262,11 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     // (NS) four loads of 256 bytes per wave and stage: load j, lane l: row
     // 128 (w & 1) + 32 j + l / 2 of the wave's operand, its dword l & 1 of the stage,
     // into the same [rows][8] bytes of LDS (blocks in order instead of even first)
-    const uint32_t ns_row = (uint32_t)(((sw_a ? m0 : n0) + 128 * (w & 1) + (lane >> 1)) * (int64_t)(8 * g.stages)) +
+    const uint32_t ns_row = (uint32_t)(((sw_a ? m0 : n0) + 128 * (w & 1) + (lane >> 1)) * (int64_t)kblocks) +
                             4u * (uint32_t)(lane & 1);
     auto issue_scl_ns = [&](int s, int j) {
-        const uint32_t voff = sw_none ? 0x80000000u : ns_row + (uint32_t)(32 * j * 8 * g.stages + 8 * s);
+        const bool past = kTail && 8 * s + 4 * (lane & 1) >= kblocks;
+        const uint32_t voff = sw_none || past ? 0x80000000u : ns_row + (uint32_t)(32 * j * kblocks + 8 * s);
         dma4(dss, lds0 + (uint32_t)((s & 1) * kStage) * !sw_none + s_lds + 256u * (uint32_t)j, voff);
     };
     auto issue_scl = [&](int s) {
@@ -590,6 +613,106 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     const bool whole = g.rows16 && n0 + TN <= g.n;
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     uint8_t *reg = smem + 32768 * w;
+    if constexpr (EPI) {
+        // Always staged in fp32, 64 columns a pass: a lane then holds EC neighbouring columns of a
+        // row, to which bias, activation and residual are applied where they leave in whole
+        // 128-byte (bf16) or 256-byte (fp32) runs.
+        typedef typename std::conditional<B16, uint16_t, float>::type T;
+        constexpr int EC = B16 ? 8 : 4, kLanes = 64 / EC, kRows = 64 / kLanes;
+        const int64_t tile_rows = rows_a - 1, tile_cols = g.n - n0;
+        auto tile_rsrc = [&](const void *p, int64_t ld) {
+            return __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<char *>(static_cast<const char *>(p) + (m0 * ld + n0) * esz), (short)0,
+                p ? (int)((tile_rows * ld + tile_cols) * esz) : 0, 0x00020000);
+        };
+        const __amdgpu_buffer_rsrc_t rr = tile_rsrc(ep.residual, ep.ldr), rzz = tile_rsrc(ep.Z, ep.ldz);
+        const int c = lane % kLanes;
+        auto put = [&](__amdgpu_buffer_rsrc_t r, int64_t ld, int orow, int col, const float (&v)[EC]) {
+            u32x4_t q;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (B16) {
+                    const bf16x2_t pr = {(__bf16)v[2 * e], (__bf16)v[2 * e + 1]};
+                    q[e] = __builtin_bit_cast(uint32_t, pr);
+                } else {
+                    q[e] = __float_as_uint(v[e]);
+                }
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(q, r, (uint32_t)((orow * ld + col) * esz), 0, kNonTemporal);
+        };
+        auto put1 = [&](T *p, float v) {
+            if constexpr (B16) *p = __builtin_bit_cast(uint16_t, (__bf16)v);
+            else *p = v;
+        };
+#pragma unroll
+        for (int pass = 0; pass < NB / 2; ++pass) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int bb = 0; bb < 2; ++bb)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int b = 2 * pass + bb, row = 32 * a + r, chunk = 8 * bb + 2 * q + hi;
+                        *reinterpret_cast<floatx4_t *>(reg + row * 256 + 16 * (chunk ^ (row & 15))) = floatx4_t{
+                            acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+                    }
+            const int col = wn + 64 * pass + EC * c;  // from n0
+            float bias[EC];
+#pragma unroll
+            for (int e = 0; e < EC; ++e) bias[e] = ep.bias && n0 + col + e < g.n ? ep.bias[n0 + col + e] : 0.f;
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 4
+            for (int i = 0; i < 128 / kRows; ++i) {
+                const int row = kRows * i + lane / kLanes, orow = wm + row;
+                float v[EC];
+#pragma unroll
+                for (int e4 = 0; e4 < EC / 4; ++e4) {
+                    const floatx4_t f = *reinterpret_cast<const floatx4_t *>(
+                        reg + row * 256 + 16 * (((EC / 4) * c + e4) ^ (row & 15)));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[4 * e4 + e] = f[e] + bias[4 * e4 + e];
+                }
+                if (whole) {
+                    u32x4_t q;
+                    if (ep.residual)
+                        q = __builtin_amdgcn_raw_buffer_load_b128(rr, (uint32_t)((orow * ep.ldr + col) * esz), 0, 0);
+                    if (ep.Z) put(rzz, ep.ldz, orow, col, v);
+                    activate(v, ep.act);
+                    if (ep.residual) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if constexpr (B16) {
+                                v[2 * e] += bf16_lo(q[e]);
+                                v[2 * e + 1] += bf16_hi(q[e]);
+                            } else {
+                                v[e] += __uint_as_float(q[e]);
+                            }
+                        }
+                    }
+                    put(ro, g.ldo, orow, col, v);
+                } else if (orow < rows_a) {
+                    const int64_t gi = m0 + orow;
+                    if (ep.Z) {
+#pragma unroll
+                        for (int e = 0; e < EC; ++e)
+                            if (n0 + col + e < g.n) put1(static_cast<T *>(ep.Z) + gi * ep.ldz + n0 + col + e, v[e]);
+                    }
+                    activate(v, ep.act);
+#pragma unroll
+                    for (int e = 0; e < EC; ++e)
+                        if (n0 + col + e < g.n) {
+                            if (ep.residual) {
+                                const T x = static_cast<const T *>(ep.residual)[gi * ep.ldr + n0 + col + e];
+                                if constexpr (B16) v[e] += __uint_as_float((uint32_t)x << 16);
+                                else v[e] += x;
+                            }
+                            put1(static_cast<T *>(O) + gi * g.ldo + n0 + col + e, v[e]);
+                        }
+                }
+            }
+        }
+        return;
+    }
     constexpr int kPasses = B16 ? 1 : NB / 2, kPerPass = NB / kPasses;
     // 16-byte chunks per staged row (bf16 at TN = 128: 8), rows per store
     constexpr int kCpr = B16 ? 4 * NB : 16, kRpi = 64 / kCpr;
@@ -663,6 +786,23 @@ __global__ __launch_bounds__(kThreads) void gemm256_kernel(const uint8_t *__rest
     const TileWork wk = tile_work((int)blockIdx.x, g.order);
     if (wk.half < 0) gemm256_tile<LR, 256, B16, LRS, NS>(ca, psa, cw, psw, g, lr0, lr1, lr2, O, wk.tile, 0, smem);
     else gemm256_tile<LR, 128, B16, LRS, NS>(ca, psa, cw, psw, g, lr0, lr1, lr2, O, wk.tile, wk.half, smem);
+}
+
+// The same with kq_mxfp4_linear's epilogue.
+template <bool B16, bool NS>
+__global__ __launch_bounds__(kThreads) void gemm256_epilogue_kernel(const uint8_t *__restrict__ ca,
+                                                                    const uint8_t *__restrict__ psa,
+                                                                    const uint8_t *__restrict__ cw,
+                                                                    const uint8_t *__restrict__ psw, Geom g, Epi ep,
+                                                                    void *__restrict__ O) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * Lay<256>::kStage + 1024];
+    const TileWork wk = tile_work((int)blockIdx.x, g.order);
+    if (wk.half < 0)
+        gemm256_tile<false, 256, B16, false, NS, true>(ca, psa, cw, psw, g, nullptr, nullptr, nullptr, O, wk.tile, 0,
+                                                       smem, ep);
+    else
+        gemm256_tile<false, 128, B16, false, NS, true>(ca, psa, cw, psw, g, nullptr, nullptr, nullptr, O, wk.tile,
+                                                       wk.half, smem, ep);
 }
 
 // Compute units of the current device (cached per device; 256 on MI355X).
@@ -820,6 +960,43 @@ kq_status gemm256_mx_lowrank(const uint8_t *codes_a, const uint8_t *scales_a, co
                              const uint8_t *codes_l, const uint8_t *scales_l, int64_t r, float *O, int64_t ldo,
                              kq_stream_t stream) {
     return gemm_lowrank<true>(codes_a, scales_a, codes_w, scales_w, m, n, k, Z, codes_l, scales_l, r, O, ldo, stream);
+}
+// kq_mxfp4_linear on these tiles; its arguments are checked by the caller. Packed scales
+// 16-byte aligned and k % 256 == 0, or MX-layout scales 4-byte aligned and k % 128 == 0.
+kq_status gemm256_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
+                         const uint8_t *scales_w, int packed, int64_t m, int64_t n, int64_t k, const float *bias,
+                         int act, int type, const void *residual, int64_t ldr, void *O, int64_t ldo, void *Z,
+                         int64_t ldz, kq_stream_t stream) {
+    const int64_t tiles_m = (m + 255) / 256, tiles_n = (n + 255) / 256;
+    if (tiles_m * tiles_n >= (int64_t)1 << 24) return KQ_ERR_UNSUPPORTED;  // work-items are counted in 32 bits
+    const int per16 = type == KQ_BF16 ? 8 : 4;
+    kq::g256::Geom g;
+    g.m = m;
+    g.n = n;
+    g.ldo = ldo;
+    g.kbytes = (int)(k / 2);
+    g.stages = (int)((k + 255) / 256);
+    g.tiles_m = (int)tiles_m;
+    g.tiles_n = (int)tiles_n;
+    g.nwg = (int)(tiles_m * tiles_n);
+    g.rows16 = aligned(O, 16) && ldo % per16 == 0 && aligned(residual, 16) && ldr % per16 == 0 && aligned(Z, 16) &&
+               ldz % per16 == 0;
+    g.r = 0;
+    g.order = kq::g256::make_tile_order(g.nwg, kq::g256::cu_count());
+    const kq::g256::Epi ep{bias, residual, Z, ldr, ldz, act};
+    const dim3 grid((unsigned)kq::g256::tile_order_groups(g.order)), block(kq::g256::kThreads);
+#define KQ_LINEAR(B16, NS)                                                                                      \
+    hipLaunchKernelGGL((kq::g256::gemm256_epilogue_kernel<B16, NS>), grid, block, 0, (hipStream_t)stream, codes_a, \
+                       scales_a, codes_w, scales_w, g, ep, O)
+    if (type == KQ_BF16) {
+        if (packed) KQ_LINEAR(true, false);
+        else KQ_LINEAR(true, true);
+    } else {
+        if (packed) KQ_LINEAR(false, false);
+        else KQ_LINEAR(false, true);
+    }
+#undef KQ_LINEAR
+    return launched();
 }
 }  // namespace kqhost
 

@@ -209,6 +209,13 @@ __global__ __launch_bounds__(256) void backward_any_kernel(const T *__restrict__
 // ===========================================================================
 // Host side
 // ===========================================================================
+namespace kqhost {
+kq_status gemm256_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
+                         const uint8_t *scales_w, int packed, int64_t m, int64_t n, int64_t k, const float *bias,
+                         int act, int type, const void *residual, int64_t ldr, void *O, int64_t ldo, void *Z,
+                         int64_t ldz, kq_stream_t stream);  // kq_gemm256.hip
+}
+
 namespace {
 
 using kqhost::aligned;
@@ -257,6 +264,11 @@ kq_status kq_mxfp4_linear(const uint8_t *codes_a, const uint8_t *scales_a, const
     if (256 * (k / 2) >= lim || m * (k / 32) >= lim || n * (k / 32) >= lim || (255 * ldo + n) * es >= lim ||
         (255 * ldr + n) * es >= lim || (255 * ldz + n) * es >= lim)
         return KQ_ERR_UNSUPPORTED;
+    const bool big = packed ? aligned(scales_a, 16) && aligned(scales_w, 16)
+                            : k % 128 == 0 && aligned(scales_a, 4) && aligned(scales_w, 4);
+    if (big && ((m + 255) / 256) * ((n + 255) / 256) >= 64)
+        return kqhost::gemm256_linear(codes_a, scales_a, codes_w, scales_w, packed, m, n, k, bias, act, type, residual,
+                                      ldr, O, ldo, Z, ldz, stream);
     kq::linear::Geom g;
     g.m = m;
     g.n = n;
