@@ -54,9 +54,10 @@
 #include <type_traits>
 
 #include "kq.h"
-#include "kq_act.hpp"
 #include "kq_cvt.hpp"
 #include "kq_device.hpp"
+#include "kq_dma.hpp"
+#include "kq_epilogue.hpp"
 #include "kq_host.hpp"
 #include "kq_tileorder.hpp"
 
@@ -81,8 +82,6 @@ struct Lay {
     static constexpr int LW = TN / 32;   // W code loads (8 rows each) per wave per stage
 };
 
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 typedef float floatx16_t __attribute__((ext_vector_type(16)));
 
@@ -95,60 +94,6 @@ struct Geom {
     int r;        // rank of the low-rank term (LR kernels)
     TileOrder order;  // which tile, or half tile, each workgroup computes
 };
-
-// The epilogue of kq_mxfp4_linear: z = sum + bias, O = act(z) + residual, z kept if asked.
-struct Epi {
-    const float *bias;       // or NULL
-    const void *residual;    // O's type, or NULL
-    void *Z;                 // O's type, or NULL
-    int64_t ldr, ldz;
-    int act;
-};
-
-__device__ __forceinline__ int swz8(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-
-// Raw buffer descriptor in SGPRs: base, 32-bit record count (bytes); loads at
-// or past the count return zero.
-__device__ __forceinline__ i32x4_t sdesc(const void *base, uint32_t bytes) {
-    const uint64_t a = reinterpret_cast<uint64_t>(base);
-    i32x4_t d;
-    d.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-    d.y = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xFFFFu));
-    d.z = __builtin_amdgcn_readfirstlane((int)bytes);
-    d.w = 0x00020000;
-    return d;
-}
-
-// 16 bytes per lane from the buffer straight into LDS: lane l's bytes land at
-// lds + 16 l. M0 carries the LDS address and is restored afterwards; the
-// compiler does not track these loads, so completion is waited for explicitly
-// (vmcnt) before a barrier.
-__device__ __forceinline__ void dma16(const i32x4_t &d, uint32_t lds, uint32_t voff, uint32_t soff) {
-    uint32_t keep;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %2, %3, %4 offen lds\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(keep)
-        : "s"(lds), "v"(voff), "s"(d), "s"(soff)
-        : "memory");
-}
-
-// 4 bytes per lane from the buffer straight into LDS: lane l's bytes land at lds + 4 l.
-__device__ __forceinline__ void dma4(const i32x4_t &d, uint32_t lds, uint32_t voff) {
-    uint32_t keep;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dword %2, %3, 0 offen lds\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(keep)
-        : "s"(lds), "v"(voff), "s"(d)
-        : "memory");
-}
 
 __device__ __forceinline__ void wait_loads_and_lds_then_barrier() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -619,31 +564,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
         // 128-byte (bf16) or 256-byte (fp32) runs.
         typedef typename std::conditional<B16, uint16_t, float>::type T;
         constexpr int EC = B16 ? 8 : 4, kLanes = 64 / EC, kRows = 64 / kLanes;
-        const int64_t tile_rows = rows_a - 1, tile_cols = g.n - n0;
-        auto tile_rsrc = [&](const void *p, int64_t ld) {
-            return __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<char *>(static_cast<const char *>(p) + (m0 * ld + n0) * esz), (short)0,
-                p ? (int)((tile_rows * ld + tile_cols) * esz) : 0, 0x00020000);
-        };
-        const __amdgpu_buffer_rsrc_t rr = tile_rsrc(ep.residual, ep.ldr), rzz = tile_rsrc(ep.Z, ep.ldz);
         const int c = lane % kLanes;
-        auto put = [&](__amdgpu_buffer_rsrc_t r, int64_t ld, int orow, int col, const float (&v)[EC]) {
-            u32x4_t q;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (B16) {
-                    const bf16x2_t pr = {(__bf16)v[2 * e], (__bf16)v[2 * e + 1]};
-                    q[e] = __builtin_bit_cast(uint32_t, pr);
-                } else {
-                    q[e] = __float_as_uint(v[e]);
-                }
-            }
-            __builtin_amdgcn_raw_buffer_store_b128(q, r, (uint32_t)((orow * ld + col) * esz), 0, kNonTemporal);
-        };
-        auto put1 = [&](T *p, float v) {
-            if constexpr (B16) *p = __builtin_bit_cast(uint16_t, (__bf16)v);
-            else *p = v;
-        };
 #pragma unroll
         for (int pass = 0; pass < NB / 2; ++pass) {
 #pragma unroll
@@ -658,8 +579,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
                     }
             const int col = wn + 64 * pass + EC * c;  // from n0
             float bias[EC];
-#pragma unroll
-            for (int e = 0; e < EC; ++e) bias[e] = ep.bias && n0 + col + e < g.n ? ep.bias[n0 + col + e] : 0.f;
+            load_bias(ep, n0 + col, bias);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 4
             for (int i = 0; i < 128 / kRows; ++i) {
@@ -672,43 +592,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[4 * e4 + e] = f[e] + bias[4 * e4 + e];
                 }
-                if (whole) {
-                    u32x4_t q;
-                    if (ep.residual)
-                        q = __builtin_amdgcn_raw_buffer_load_b128(rr, (uint32_t)((orow * ep.ldr + col) * esz), 0, 0);
-                    if (ep.Z) put(rzz, ep.ldz, orow, col, v);
-                    activate(v, ep.act);
-                    if (ep.residual) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if constexpr (B16) {
-                                v[2 * e] += bf16_lo(q[e]);
-                                v[2 * e + 1] += bf16_hi(q[e]);
-                            } else {
-                                v[e] += __uint_as_float(q[e]);
-                            }
-                        }
-                    }
-                    put(ro, g.ldo, orow, col, v);
-                } else if (orow < rows_a) {
-                    const int64_t gi = m0 + orow;
-                    if (ep.Z) {
-#pragma unroll
-                        for (int e = 0; e < EC; ++e)
-                            if (n0 + col + e < g.n) put1(static_cast<T *>(ep.Z) + gi * ep.ldz + n0 + col + e, v[e]);
-                    }
-                    activate(v, ep.act);
-#pragma unroll
-                    for (int e = 0; e < EC; ++e)
-                        if (n0 + col + e < g.n) {
-                            if (ep.residual) {
-                                const T x = static_cast<const T *>(ep.residual)[gi * ep.ldr + n0 + col + e];
-                                if constexpr (B16) v[e] += __uint_as_float((uint32_t)x << 16);
-                                else v[e] += x;
-                            }
-                            put1(static_cast<T *>(O) + gi * g.ldo + n0 + col + e, v[e]);
-                        }
-                }
+                if (orow < rows_a) finish<T>(v, ep, m0 + orow, n0 + col, whole);
             }
         }
         return;
@@ -793,15 +677,15 @@ template <bool B16, bool NS>
 __global__ __launch_bounds__(kThreads) void gemm256_epilogue_kernel(const uint8_t *__restrict__ ca,
                                                                     const uint8_t *__restrict__ psa,
                                                                     const uint8_t *__restrict__ cw,
-                                                                    const uint8_t *__restrict__ psw, Geom g, Epi ep,
-                                                                    void *__restrict__ O) {
+                                                                    const uint8_t *__restrict__ psw, Geom g,
+                                                                    Epi ep) {
     __shared__ __attribute__((aligned(16))) uint8_t smem[2 * Lay<256>::kStage + 1024];
     const TileWork wk = tile_work((int)blockIdx.x, g.order);
     if (wk.half < 0)
-        gemm256_tile<false, 256, B16, false, NS, true>(ca, psa, cw, psw, g, nullptr, nullptr, nullptr, O, wk.tile, 0,
-                                                       smem, ep);
+        gemm256_tile<false, 256, B16, false, NS, true>(ca, psa, cw, psw, g, nullptr, nullptr, nullptr, nullptr, wk.tile,
+                                                       0, smem, ep);
     else
-        gemm256_tile<false, 128, B16, false, NS, true>(ca, psa, cw, psw, g, nullptr, nullptr, nullptr, O, wk.tile,
+        gemm256_tile<false, 128, B16, false, NS, true>(ca, psa, cw, psw, g, nullptr, nullptr, nullptr, nullptr, wk.tile,
                                                        wk.half, smem, ep);
 }
 
@@ -964,30 +848,26 @@ kq_status gemm256_mx_lowrank(const uint8_t *codes_a, const uint8_t *scales_a, co
 // kq_mxfp4_linear on these tiles; its arguments are checked by the caller. Packed scales
 // 16-byte aligned and k % 256 == 0, or MX-layout scales 4-byte aligned and k % 128 == 0.
 kq_status gemm256_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
-                         const uint8_t *scales_w, int packed, int64_t m, int64_t n, int64_t k, const float *bias,
-                         int act, int type, const void *residual, int64_t ldr, void *O, int64_t ldo, void *Z,
-                         int64_t ldz, kq_stream_t stream) {
-    const int64_t tiles_m = (m + 255) / 256, tiles_n = (n + 255) / 256;
-    if (tiles_m * tiles_n >= (int64_t)1 << 24) return KQ_ERR_UNSUPPORTED;  // work-items are counted in 32 bits
-    const int per16 = type == KQ_BF16 ? 8 : 4;
+                         const uint8_t *scales_w, int packed, int64_t k, int type, const kq::Epi &ep,
+                         kq_stream_t stream) {
+    const int64_t tiles_m = (ep.m + 255) / 256, tiles_n = (ep.n + 255) / 256;
+    if (tiles_m * tiles_n >= (int64_t)1 << 23) return KQ_ERR_UNSUPPORTED;  // work-items are counted in 32 bits
     kq::g256::Geom g;
-    g.m = m;
-    g.n = n;
-    g.ldo = ldo;
+    g.m = ep.m;
+    g.n = ep.n;
+    g.ldo = ep.ldo;
     g.kbytes = (int)(k / 2);
     g.stages = (int)((k + 255) / 256);
     g.tiles_m = (int)tiles_m;
     g.tiles_n = (int)tiles_n;
     g.nwg = (int)(tiles_m * tiles_n);
-    g.rows16 = aligned(O, 16) && ldo % per16 == 0 && aligned(residual, 16) && ldr % per16 == 0 && aligned(Z, 16) &&
-               ldz % per16 == 0;
+    g.rows16 = ep.align >= 16;
     g.r = 0;
     g.order = kq::g256::make_tile_order(g.nwg, kq::g256::cu_count());
-    const kq::g256::Epi ep{bias, residual, Z, ldr, ldz, act};
     const dim3 grid((unsigned)kq::g256::tile_order_groups(g.order)), block(kq::g256::kThreads);
-#define KQ_LINEAR(B16, NS)                                                                                      \
+#define KQ_LINEAR(B16, NS)                                                                                         \
     hipLaunchKernelGGL((kq::g256::gemm256_epilogue_kernel<B16, NS>), grid, block, 0, (hipStream_t)stream, codes_a, \
-                       scales_a, codes_w, scales_w, g, ep, O)
+                       scales_a, codes_w, scales_w, g, ep)
     if (type == KQ_BF16) {
         if (packed) KQ_LINEAR(true, false);
         else KQ_LINEAR(true, true);

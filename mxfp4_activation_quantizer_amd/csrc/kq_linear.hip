@@ -3,109 +3,60 @@
 // (KroQuant, arXiv 2607.21446v1, Sec. 1 Eq. 2 for the product), and the
 // gradients of that epilogue.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kq.h"
-#include "kq_act.hpp"
 #include "kq_device.hpp"
+#include "kq_dma.hpp"
+#include "kq_epilogue.hpp"
 #include "kq_host.hpp"
+#include "kq_tileorder.hpp"
 
 namespace kq {
 namespace linear {
 
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float floatx16_t __attribute__((ext_vector_type(16)));
 
 struct Geom {
-    int64_t m, n, ldr, ldo, ldz;
     int kbytes, kblocks;  // k / 2, k / 32
     int stages;           // ceil(k / 256)
-    int tiles_n;
-    int act;
-    int vec;  // rows of O, Z and the residual in whole aligned groups of four
+    int tiles_n, tiles_m;
 };
 
-template <class T>
-__device__ __forceinline__ void load4(const T *p, float v[4]);
-template <>
-__device__ __forceinline__ void load4<float>(const float *p, float v[4]) {
-    const float4 q = *reinterpret_cast<const float4 *>(p);
-    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-}
-template <>
-__device__ __forceinline__ void load4<uint16_t>(const uint16_t *p, float v[4]) {
-    const uint2 q = *reinterpret_cast<const uint2 *>(p);
-    v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const bf16x2_t v = {(__bf16)a, (__bf16)b};
-    return __builtin_bit_cast(uint32_t, v);
-}
-__device__ __forceinline__ void store4(float *p, const float v[4]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void store4(uint16_t *p, const float v[4]) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-}
-__device__ __forceinline__ float load1(const float *p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
-__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
-
-// Four neighbouring elements of row i from column j: bias, activation, residual, stores.
-template <class T>
-__device__ __forceinline__ void finish4(float (&v)[4], const Geom &g, int64_t i, int64_t j, const float *bias,
-                                        const T *res, T *O, T *Z) {
-    if (g.vec) {
-        if (bias) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += bias[j + e];
-        }
-        if (Z) store4(Z + i * g.ldz + j, v);
-        activate(v, g.act);
-        if (res) {
-            float r[4];
-            load4(res + i * g.ldr + j, r);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += r[e];
-        }
-        store4(O + i * g.ldo + j, v);
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (bias && j + e < g.n) v[e] += bias[j + e];
-    if (Z) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (j + e < g.n) store1(Z + i * g.ldz + j + e, v[e]);
-    }
-    activate(v, g.act);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (j + e < g.n) store1(O + i * g.ldo + j + e, res ? v[e] + load1(res + i * g.ldr + j + e) : v[e]);
-}
+// How an operand's scales are read: byte by byte from the MX layout (any k % 32 == 0), or a
+// row's eight bytes of a 256-k stage at once, from the MX layout (k % 256 == 0, 8-byte
+// aligned) or the packed one.
+enum Scales { kBytes = 0, kRows8 = 1, kPacked8 = 2 };
 
 // A workgroup of WK waves computes 16 MF rows x 16 NF columns of O, each wave every
 // WK-th 256-k stage of the whole tile on v_mfma_scale_f32_16x16x128_f8f6f4, operands
 // straight from memory into registers (a stage of a row is 128 code bytes, one cache
-// line), and the waves' sums meet in LDS in wave order. The instruction's A operand is
-// a W fragment and its B operand an A fragment: lane l supplies row l % 16 of each and
-// k group l / 16 (one MX block: 16 code bytes, one scale byte), and receives O row
-// l % 16, columns 4 (l / 16) + 0..3 of the fragment. Rows past m or n and k groups
-// past k are past a record count (or pushed past it) and read zero codes.
-template <class T, bool PACKED, int MF, int NF, int WK>
+// line) D stages ahead, and the waves' sums meet in LDS in wave order. The
+// instruction's A operand is a W fragment and its B operand an A fragment: lane l
+// supplies row l % 16 of each and k group l / 16 (one MX block: 16 code bytes, one
+// scale byte), and receives O row l % 16, columns 4 (l / 16) + 0..3 of the fragment.
+// Rows past m or n and k groups past k are past a record count (or pushed past it) and
+// read zero codes.
+template <int F>
+struct Stage {
+    u32x4_t code[2][F];
+    uint32_t scl[2][F];
+};
+
+template <class T, int SC, int MF, int NF, int WK, int D>
 __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restrict__ ca,
                                                           const uint8_t *__restrict__ sa,
                                                           const uint8_t *__restrict__ cw,
-                                                          const uint8_t *__restrict__ sw, Geom g,
-                                                          const float *__restrict__ bias, const T *__restrict__ res,
-                                                          T *__restrict__ O, T *__restrict__ Z) {
+                                                          const uint8_t *__restrict__ sw, Geom g, Epi ep) {
     __shared__ float4 red[WK][MF * NF][64];
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int tn = (int)(blockIdx.x % (unsigned)g.tiles_n), tm = (int)(blockIdx.x / (unsigned)g.tiles_n);
     const int64_t m0 = (int64_t)tm * (16 * MF), n0 = (int64_t)tn * (16 * NF);
-    const int rows_a = (int)(g.m - m0 < 16 * MF ? g.m - m0 : 16 * MF);
-    const int rows_w = (int)(g.n - n0 < 16 * NF ? g.n - n0 : 16 * NF);
+    const int rows_a = (int)(ep.m - m0 < 16 * MF ? ep.m - m0 : 16 * MF);
+    const int rows_w = (int)(ep.n - n0 < 16 * NF ? ep.n - n0 : 16 * NF);
     const int row = lane & 15, grp = lane >> 4;
 
     auto rsrc = [](const uint8_t *p, int64_t bytes) {
@@ -115,10 +66,10 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
     const auto rcw = rsrc(cw + n0 * g.kbytes, (int64_t)rows_w * g.kbytes);
     // packed: a padding row reads a neighbour's or a later stage's byte, or zero past the
     // array; its codes are zero and its outputs are not stored
-    const auto rsa = PACKED ? rsrc(sa + 8 * m0, (int64_t)g.stages * 8 * g.m - 8 * m0)
-                            : rsrc(sa + m0 * g.kblocks, (int64_t)rows_a * g.kblocks);
-    const auto rsw = PACKED ? rsrc(sw + 8 * n0, (int64_t)g.stages * 8 * g.n - 8 * n0)
-                            : rsrc(sw + n0 * g.kblocks, (int64_t)rows_w * g.kblocks);
+    const auto rsa = SC == kPacked8 ? rsrc(sa + 8 * m0, (int64_t)g.stages * 8 * ep.m - 8 * m0)
+                                    : rsrc(sa + m0 * g.kblocks, (int64_t)rows_a * g.kblocks);
+    const auto rsw = SC == kPacked8 ? rsrc(sw + 8 * n0, (int64_t)g.stages * 8 * ep.n - 8 * n0)
+                                    : rsrc(sw + n0 * g.kblocks, (int64_t)rows_w * g.kblocks);
     constexpr uint32_t kNone = 0x80000000u;
 
     floatx4_t acc[NF][MF];
@@ -127,39 +78,71 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
 #pragma unroll
         for (int a = 0; a < MF; ++a) acc[b][a] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
-    auto codes = [&](__amdgpu_buffer_rsrc_t r, int f, int kb) {  // block kb of row 16 f + lane % 16
-        const uint32_t off = kb < g.kblocks ? (uint32_t)((16 * f + row) * g.kbytes + 16 * kb) : kNone;
-        const u32x4_t q = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
-        return i32x8_t{(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0};
-    };
-    auto scale = [&](__amdgpu_buffer_rsrc_t r, int64_t rows, int f, int kb) {
-        uint32_t off;
-        if (PACKED) off = (uint32_t)((kb >> 3) * 8 * rows) + 8 * (16 * f + row) + 4 * (kb & 1) + ((kb & 7) >> 1);
-        else off = (uint32_t)((16 * f + row) * g.kblocks + kb);
-        return (int)__builtin_amdgcn_raw_buffer_load_b8(r, kb < g.kblocks ? off : kNone, 0, 0);
-    };
-    for (int s = wave; s < g.stages; s += WK) {
+    // stage s of the F fragments of one operand of `rows` rows
+    auto fetch = [&](auto &S, __amdgpu_buffer_rsrc_t rc, __amdgpu_buffer_rsrc_t rs, int64_t rows, int s) {
+        constexpr int F = sizeof(S.code) / sizeof(u32x4_t) / 2;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int kb = 8 * s + 4 * h + grp;
-            i32x8_t fa[MF], fw[NF];
-            int xa[MF], xw[NF];
+        for (int f = 0; f < F; ++f) {
+            const int r = 16 * f + row;
 #pragma unroll
-            for (int a = 0; a < MF; ++a) {
-                fa[a] = codes(rca, a, kb);
-                xa[a] = scale(rsa, g.m, a, kb);
+            for (int h = 0; h < 2; ++h) {
+                const int kb = 8 * s + 4 * h + grp;
+                const bool in = kb < g.kblocks;
+                S.code[h][f] = __builtin_amdgcn_raw_buffer_load_b128(
+                    rc, in ? (uint32_t)(r * g.kbytes + 16 * kb) : kNone, 0, 0);
+                if (SC == kBytes)
+                    S.scl[h][f] = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? (uint32_t)(r * g.kblocks + kb) : kNone,
+                                                                     0, 0);
             }
-#pragma unroll
-            for (int b = 0; b < NF; ++b) {
-                fw[b] = codes(rcw, b, kb);
-                xw[b] = scale(rsw, g.n, b, kb);
+            if (SC != kBytes) {
+                const uint32_t off = SC == kPacked8 ? (uint32_t)(8 * rows * s) + 8 * r : (uint32_t)(r * g.kblocks + 8 * s);
+                const auto q = __builtin_amdgcn_raw_buffer_load_b64(rs, s < g.stages ? off : kNone, 0, 0);
+                S.scl[0][f] = q[0];
+                S.scl[1][f] = q[1];
             }
+        }
+    };
+    // the lane's scale of half h, in byte 0 (packed, half 1: in byte 2)
+    auto scale = [&](const auto &S, int h, int f) -> int {
+        if (SC == kBytes) return (int)S.scl[h][f];
+        if (SC == kRows8) return (int)(S.scl[h][f] >> (8 * grp));
+        return (int)((grp & 1 ? S.scl[1][f] : S.scl[0][f]) >> (8 * (grp >> 1)));
+    };
+    constexpr int kSel1 = SC == kPacked8 ? 2 : 0;
+
+    Stage<MF> A[D];
+    Stage<NF> B[D];
 #pragma unroll
-            for (int b = 0; b < NF; ++b)
+    for (int i = 0; i < D; ++i) {
+        fetch(A[i], rca, rsa, ep.m, wave + WK * i);
+        fetch(B[i], rcw, rsw, ep.n, wave + WK * i);
+    }
+    for (int s = wave; s < g.stages; s += WK * D) {
 #pragma unroll
-                for (int a = 0; a < MF; ++a)
-                    acc[b][a] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[b], fa[a], acc[b][a], 4, 4, 0,
-                                                                                  xw[b], 0, xa[a]);
+        for (int i = 0; i < D; ++i) {
+            if (s + WK * i < g.stages) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int b = 0; b < NF; ++b) {
+                        const u32x4_t w4 = B[i].code[h][b];
+                        const i32x8_t fw = {(int)w4[0], (int)w4[1], (int)w4[2], (int)w4[3], 0, 0, 0, 0};
+                        const int xw = scale(B[i], h, b);
+#pragma unroll
+                        for (int a = 0; a < MF; ++a) {
+                            const u32x4_t a4 = A[i].code[h][a];
+                            const i32x8_t fa = {(int)a4[0], (int)a4[1], (int)a4[2], (int)a4[3], 0, 0, 0, 0};
+                            if (h == 0)
+                                acc[b][a] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                    fw, fa, acc[b][a], 4, 4, 0, xw, 0, scale(A[i], h, a));
+                            else
+                                acc[b][a] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                    fw, fa, acc[b][a], 4, 4, kSel1, xw, kSel1, scale(A[i], h, a));
+                        }
+                    }
+            }
+            fetch(A[i], rca, rsa, ep.m, s + WK * (i + D));
+            fetch(B[i], rcw, rsw, ep.n, s + WK * (i + D));
         }
     }
 #pragma unroll
@@ -178,7 +161,256 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
             const float4 v = red[w][f][l];
             z[0] += v.x; z[1] += v.y; z[2] += v.z; z[3] += v.w;
         }
-        if (r < rows_a && 4 * c4 < rows_w) finish4<T>(z, g, m0 + r, n0 + 4 * c4, bias, res, O, Z);
+        if (r < rows_a && 4 * c4 < rows_w) {
+            float b[4];
+            load_bias(ep, n0 + 4 * c4, b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] += b[e];
+            finish<T>(z, ep, m0 + r, n0 + 4 * c4, ep.align >= 4 * (int)sizeof(T) && n0 + 4 * c4 + 4 <= ep.n);
+        }
+    }
+}
+
+// Between a few rows and many: 64 FA x 64 FB tiles through LDS. Four waves multiply, each
+// 32 FA x 32 FB on the 32 x 32 x 64 scaled instruction (layouts as the 256 x 256 kernel:
+// swapped operands, chunk c of staged row r at slot c ^ swz8(r)); they move the codes of
+// the 256-k stages straight into LDS, N - 1 stages ahead of the one multiplied, waiting only
+// for the oldest. A fifth wave brings the scales, whose layout (packed, or MX rows of any
+// length and alignment) needs them in registers on the way: eight bytes per row and stage,
+// even blocks first, zero past k. One barrier a stage.
+//
+// Why: the 256 x 256 kernel takes as long for one tile as for one on every compute unit
+// (22 us at k = 4096), so products of fewer tiles than that are faster in smaller ones.
+template <class T, int FA, int FB, int N>
+__global__ __launch_bounds__(320) void tile_kernel(const uint8_t *__restrict__ ca, const uint8_t *__restrict__ sa,
+                                                   const uint8_t *__restrict__ cw, const uint8_t *__restrict__ sw,
+                                                   int packed, Geom g, Epi ep) {
+    constexpr int TM = 64 * FA, TN = 64 * FB, kRowsAll = TM + TN;
+    constexpr int kOffScl = kRowsAll * 128, kStage = kRowsAll * 136;
+    constexpr int kLoads = kRowsAll / 32;  // code loads (8 rows each) per wave and stage
+    static_assert(kLoads * (N - 2) <= 63 && N >= 2, "the wait counts at most 63 loads");
+    static_assert(N * kStage >= TM * TN * 4, "the output is staged in the same LDS");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[N * kStage];
+    const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+    // an XCD's workgroups take a run of tiles, walked in bands of kBand rows of tiles (kq_tileorder.hpp)
+    constexpr int kBand = 4;
+    const int u = g256::tile_work((int)blockIdx.x, g256::TileOrder{g.tiles_m * g.tiles_n, 0, 0, 0}).tile;
+    const int band = u / (kBand * g.tiles_n), within = u % (kBand * g.tiles_n);
+    const int band_rows = g.tiles_m - band * kBand < kBand ? g.tiles_m - band * kBand : kBand;
+    const int tm = band * kBand + within % band_rows, tn = within / band_rows;
+    const int64_t m0 = (int64_t)tm * TM, n0 = (int64_t)tn * TN;
+    const int rows_a = (int)(ep.m - m0 < TM ? ep.m - m0 : TM), rows_w = (int)(ep.n - n0 < TN ? ep.n - n0 : TN);
+
+    if (w == 4) {
+        // Rows lane + 64 i of the tile: A's first, then W's. A padding row takes the last row's
+        // scales (its codes are zero and its outputs are not stored), so no load has a condition.
+        constexpr int R = FA + FB;
+        const uint8_t *at[R];
+        int64_t step[R];  // packed: bytes from a stage to the next
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const bool is_a = i < FA;
+            const int row = lane + 64 * (is_a ? i : i - FA), last = (is_a ? rows_a : rows_w) - 1;
+            const int64_t g_row = (is_a ? m0 : n0) + (row < last ? row : last);
+            at[i] = (is_a ? sa : sw) + g_row * (packed ? 8 : g.kblocks);
+            step[i] = 8 * (is_a ? ep.m : ep.n);
+        }
+        // this slot held stage s - N, whose reads ended before the barrier of stage s - N + 1
+        auto publish = [&](int slot, const uint2 (&v)[R]) {
+            uint8_t *to = smem + slot * kStage + kOffScl + 8 * lane;
+#pragma unroll
+            for (int i = 0; i < R; ++i) *reinterpret_cast<uint2 *>(to + 512 * i) = v[i];
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        };
+        if (packed) {
+            uint2 ring[4][R];
+            auto fetch = [&](uint2 (&v)[R], int s) {
+                const int sc = s < g.stages ? s : g.stages - 1;
+#pragma unroll
+                for (int i = 0; i < R; ++i) v[i] = *reinterpret_cast<const uint2 *>(at[i] + sc * step[i]);
+            };
+            if (g.stages > 0) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) fetch(ring[q], q);
+            }
+            for (int s0 = 0; s0 < g.stages; s0 += 4) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (s0 + q >= g.stages) break;
+                    publish(q % N, ring[q]);
+                    fetch(ring[q], s0 + q + 4);
+                }
+            }
+        } else {
+            // Four stages at a time: a row's 32 bytes of them lie in one cache line with nothing else that
+            // the tile needs now (fetched eight at a time, the scales cost as many lines as the codes and
+            // a product 1.5 x the time).
+            struct Group {
+                uint4 u[R][2];
+            };
+            Group now, next;
+            auto fetch = [&](Group &v, int s0) {
+                const int left = g.kblocks - 8 * s0;
+                if (left >= 32) {
+#pragma unroll
+                    for (int i = 0; i < R; ++i) __builtin_memcpy(v.u[i], at[i] + 8 * s0, 32);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        uint64_t x[4] = {0, 0, 0, 0};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (left >= 8 * q + 8) {
+                                __builtin_memcpy(&x[q], at[i] + 8 * (s0 + q), 8);
+                            } else {
+                                for (int b = 8 * q; b < left; ++b) x[q] |= (uint64_t)at[i][8 * s0 + b] << (8 * (b - 8 * q));
+                            }
+                        }
+                        __builtin_memcpy(v.u[i], x, 32);
+                    }
+                }
+            };
+            fetch(now, 0);
+            fetch(next, 4);
+            for (int s0 = 0; s0 < g.stages; s0 += 4) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (s0 + q >= g.stages) break;
+                    uint2 v[R];
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const uint4 u = now.u[i][q >> 1];
+                        const uint32_t x = q & 1 ? u.z : u.x, y = q & 1 ? u.w : u.y;
+                        v[i] = make_uint2(__builtin_amdgcn_perm(y, x, 0x06040200u),
+                                          __builtin_amdgcn_perm(y, x, 0x07050301u));
+                    }
+                    publish(q % N, v);
+                }
+                now = next;
+                fetch(next, s0 + 8);
+            }
+        }
+        static_assert(4 % N == 0, "a stage's slot is its place in a group of four, modulo N");
+        asm volatile("s_barrier" ::: "memory");  // the one in front of the output's staging
+        return;
+    }
+
+    const i32x4_t dca = sdesc(ca + m0 * g.kbytes, (uint32_t)(rows_a * g.kbytes));
+    const i32x4_t dcw = sdesc(cw + n0 * g.kbytes, (uint32_t)(rows_w * g.kbytes));
+    const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+    // load j of wave w: staged rows 8 (kLoads w + j) + lane / 8 (A's TM rows, then W's), slot lane % 8
+    const int chunk[2] = {(lane & 7) ^ swz8(lane >> 3), (lane & 7) ^ swz8(8 + (lane >> 3))};
+    uint32_t voff[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+        const int r0 = 8 * (kLoads * w + j), row = (r0 < TM ? r0 : r0 - TM) + (lane >> 3);
+        voff[j] = (uint32_t)(row * g.kbytes) + 16u * (uint32_t)chunk[j & 1];
+    }
+    auto issue = [&](int s, int slot) {  // past k (whole stages too): past the record count, zeros
+        const int kb = 128 * s;
+        const bool in[2] = {kb + 16 * chunk[0] < g.kbytes, kb + 16 * chunk[1] < g.kbytes};
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int r0 = 8 * (kLoads * w + j);
+            const uint32_t off = in[j & 1] ? voff[j] : 0x80000000u;
+            dma16(r0 < TM ? dca : dcw, lds0 + (uint32_t)(slot * kStage + r0 * 128), off, (uint32_t)kb);
+        }
+    };
+    const int r = lane & 31, hi = lane >> 5;
+    const int wm = (w >> 1) * (TM / 2), wn = (w & 1) * (TN / 2);
+    int rdo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rdo[j] = r * 128 + 16 * ((2 * j + hi) ^ swz8(r & 15));
+
+    floatx16_t acc[FA][FB];
+#pragma unroll
+    for (int a = 0; a < FA; ++a)
+#pragma unroll
+        for (int b = 0; b < FB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+
+#pragma unroll
+    for (int i = 0; i < N - 1; ++i) issue(i, i);
+    for (int s0 = 0; s0 < g.stages; s0 += N) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int s = s0 + i;
+            if (s >= g.stages) break;
+            // stage s has landed (the N - 2 younger ones may be in flight), and every wave is done
+            // with stage s - 1, whose slot takes stage s + N - 1
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads * (N - 2)) : "memory");
+            issue(s + N - 1, (i + N - 1) % N);
+            const uint8_t *st = smem + i * kStage;
+            uint32_t xa[FA], xw[FB];
+#pragma unroll
+            for (int a = 0; a < FA; ++a)
+                xa[a] = *reinterpret_cast<const uint32_t *>(st + kOffScl + 8 * (wm + 32 * a + r) + 4 * hi);
+#pragma unroll
+            for (int b = 0; b < FB; ++b)
+                xw[b] = *reinterpret_cast<const uint32_t *>(st + kOffScl + 8 * (TM + wn + 32 * b + r) + 4 * hi);
+            auto step = [&](auto jc) {
+                constexpr int j = decltype(jc)::value;
+                i32x8_t fa[FA], fw[FB];
+#pragma unroll
+                for (int a = 0; a < FA; ++a) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(st + (wm + 32 * a) * 128 + rdo[j]);
+                    fa[a] = i32x8_t{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
+                }
+#pragma unroll
+                for (int b = 0; b < FB; ++b) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(st + (TM + wn + 32 * b) * 128 + rdo[j]);
+                    fw[b] = i32x8_t{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
+                }
+#pragma unroll
+                for (int a = 0; a < FA; ++a)
+#pragma unroll
+                    for (int b = 0; b < FB; ++b)
+                        acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[b], fa[a], acc[a][b], 4, 4, j,
+                                                                                    (int)xw[b], j, (int)xa[a]);
+            };
+            step(std::integral_constant<int, 0>());
+            step(std::integral_constant<int, 1>());
+            step(std::integral_constant<int, 2>());
+            step(std::integral_constant<int, 3>());
+        }
+    }
+
+    // every load into LDS has landed (the ones past k too) and every wave is done with the stages
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    // Each wave stages its block in fp32 in its own region, rows of 32 FB columns with 16-byte chunk c
+    // at c ^ (row % CH), and reads it back as pieces of EC columns of a row.
+    constexpr int WM = TM / 2, WN = TN / 2, CH = WN / 4, EC = 16 / (int)sizeof(T), kLanes = WN / EC, kRows = 64 / kLanes;
+    uint8_t *reg = smem + w * (WM * WN * 4);
+#pragma unroll
+    for (int a = 0; a < FA; ++a)
+#pragma unroll
+        for (int b = 0; b < FB; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = 32 * a + r, c = 8 * b + 2 * q + hi;
+                *reinterpret_cast<floatx4_t *>(reg + row * (WN * 4) + 16 * (c ^ (row & (CH - 1)))) =
+                    floatx4_t{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+            }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int c = lane % kLanes;
+    const int64_t col = n0 + wn + EC * c;
+    const bool whole = ep.align >= 16 && col + EC <= ep.n;
+    if (col >= ep.n) return;
+    float bias[EC];
+    load_bias(ep, col, bias);
+#pragma unroll 4
+    for (int i = 0; i < WM / kRows; ++i) {
+        const int row = kRows * i + lane / kLanes;
+        float v[EC];
+#pragma unroll
+        for (int e4 = 0; e4 < EC / 4; ++e4) {
+            const floatx4_t f = *reinterpret_cast<const floatx4_t *>(
+                reg + row * (WN * 4) + 16 * (((EC / 4) * c + e4) ^ (row & (CH - 1))));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * e4 + e] = f[e] + bias[4 * e4 + e];
+        }
+        if (wm + row < rows_a) finish<T>(v, ep, m0 + wm + row, col, whole);
     }
 }
 
@@ -211,9 +443,8 @@ __global__ __launch_bounds__(256) void backward_any_kernel(const T *__restrict__
 // ===========================================================================
 namespace kqhost {
 kq_status gemm256_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
-                         const uint8_t *scales_w, int packed, int64_t m, int64_t n, int64_t k, const float *bias,
-                         int act, int type, const void *residual, int64_t ldr, void *O, int64_t ldo, void *Z,
-                         int64_t ldz, kq_stream_t stream);  // kq_gemm256.hip
+                         const uint8_t *scales_w, int packed, int64_t k, int type, const kq::Epi &ep,
+                         kq_stream_t stream);  // kq_gemm256.hip
 }
 
 namespace {
@@ -225,18 +456,94 @@ using kqhost::sizes_fit;
 bool good_type(int type) { return type == KQ_F32 || type == KQ_BF16; }
 bool good_act(int act) { return act >= KQ_ACT_NONE && act <= KQ_ACT_GELU_TANH; }
 
-template <class T, bool PACKED>
+// The launch's work-items are counted in 32 bits.
+bool groups_fit(int64_t groups, int threads) { return groups <= (int64_t)0xFFFFFFFF / threads; }
+
+template <class T, int SC, int MF, int NF, int WK, int D>
 kq_status launch_product(const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, const uint8_t *sw,
-                         kq::linear::Geom g, const float *bias, const void *res, void *O, void *Z,
-                         kq_stream_t stream) {
-    constexpr int MF = 2, NF = 2, WK = 4;
-    const int64_t tiles_m = (g.m + 16 * MF - 1) / (16 * MF), tiles_n = (g.n + 16 * NF - 1) / (16 * NF);
+                         kq::linear::Geom g, const kq::Epi &ep, kq_stream_t stream) {
+    const int64_t tiles_m = (ep.m + 16 * MF - 1) / (16 * MF), tiles_n = (ep.n + 16 * NF - 1) / (16 * NF);
     g.tiles_n = (int)tiles_n;
-    // the launch's work-items are counted in 32 bits
-    if (tiles_m * tiles_n > (int64_t)0xFFFFFFFF / (64 * WK)) return KQ_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((kq::linear::product_kernel<T, PACKED, MF, NF, WK>), dim3((unsigned)(tiles_m * tiles_n)),
-                       dim3(64 * WK), 0, (hipStream_t)stream, ca, sa, cw, sw, g, bias, (const T *)res, (T *)O, (T *)Z);
+    if (!groups_fit(tiles_m * tiles_n, 64 * WK)) return KQ_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((kq::linear::product_kernel<T, SC, MF, NF, WK, D>), dim3((unsigned)(tiles_m * tiles_n)),
+                       dim3(64 * WK), 0, (hipStream_t)stream, ca, sa, cw, sw, g, ep);
     return launched();
+}
+
+template <class T, int FA, int FB, int N>
+kq_status launch_tiles(const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, const uint8_t *sw, int packed,
+                       kq::linear::Geom g, const kq::Epi &ep, kq_stream_t stream) {
+    const int64_t tiles_m = (ep.m + 64 * FA - 1) / (64 * FA), tiles_n = (ep.n + 64 * FB - 1) / (64 * FB);
+    g.tiles_n = (int)tiles_n;
+    g.tiles_m = (int)tiles_m;
+    if (!groups_fit(tiles_m * tiles_n, 320)) return KQ_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((kq::linear::tile_kernel<T, FA, FB, N>), dim3((unsigned)(tiles_m * tiles_n)), dim3(320), 0,
+                       (hipStream_t)stream, ca, sa, cw, sw, packed, g, ep);
+    return launched();
+}
+
+// Which kernel a product of m x n outputs over `stages` 256-k stages runs on.
+//
+// Few rows or few tiles: product_kernel, whose waves share a tile's k. Its tile is the
+// smallest that needs at most one workgroup per compute unit (at k = 4096, us on MI355X:
+// 8 x 4096 4.9 with 16 x 16 tiles, 5.7 with 16 x 32; 64 x 1152 6.4 with 16 x 32, 7.8 with
+// 16 x 16; 64 x 4096 7.2 with 32 x 32, 8.1 with 64 x 64 tiles through LDS); up to 16 rows
+// take it at any n (1 x 16384 8.7 against 9.7 through LDS).
+//
+// Otherwise the least of four estimates, in us, fitted to 17 measured shapes from
+// 128 x 512 x 512 to 8192 x 4096 x 1024 (within about 15%): a launch, a stage's latency while
+// a compute unit has one tile, and each further tile's share. E.g. measured at k = 4096, for
+// 64 x 64 tiles 4 and 2 stages deep, 128 x 128 and 256 x 256:
+//   128 x 4096   8.2   10.8   16.2   23.1
+//   512 x 4096  14.7   12.1   16.5   24.0
+//   1024 x 4096 25.7   22.8   17.2   24.5
+//   4096 x 4096 89.2   76.0   53.2   42.7
+enum Kernel { kProduct11, kProduct12, kProduct22, kTile64Deep, kTile64, kTile128, kTile256 };
+
+Kernel choose_kernel(int64_t m, int64_t n, int stages, bool packed, bool can256) {
+    const int cus = kqhost::compute_units();
+    auto tiles = [&](int64_t tm, int64_t tn) { return (double)((m + tm - 1) / tm) * (double)((n + tn - 1) / tn); };
+    if (m <= 16) return tiles(16, 16) < 2 * cus ? kProduct11 : kProduct12;
+    if (tiles(32, 32) <= cus)
+        return tiles(16, 16) <= cus ? kProduct11 : tiles(16, 32) <= cus ? kProduct12 : kProduct22;
+    const double st = stages, t64 = tiles(64, 64) / cus, t128 = ceil(tiles(128, 128) / cus), t256 = tiles(256, 256);
+    const double deep = 3 + ceil(t64) * 0.33 * st;
+    const double shallow = fmax(2.8 + 0.5 * st, 1.2 + t64 * (0.325 * st + 0.7));
+    const double mid = 3 + 0.15 * st + t128 * (0.62 * st + 2.1);
+    Kernel k = kTile64Deep;
+    double best = deep;
+    if (shallow < best) k = kTile64, best = shallow;
+    if (mid < best) k = kTile128, best = mid;
+    if (can256) {
+        // whole rounds, and a last one of at most half the compute units in half tiles
+        const double full = 13.5 + (packed ? 1.8 : 2.05) * st, half = 7 + (packed ? 1.0 : 1.4) * st;
+        const double rem = fmod(t256, cus);
+        const double big = floor(t256 / cus) * full + (rem == 0 ? 0 : 2 * rem <= cus ? half : full);
+        if (big < best) k = kTile256;
+    }
+    return k;
+}
+
+template <class T, int MF, int NF, int WK>
+kq_status launch_any_product(const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, const uint8_t *sw, int packed,
+                             const kq::linear::Geom &g, const kq::Epi &ep, kq_stream_t stream) {
+    if (packed) return launch_product<T, kq::linear::kPacked8, MF, NF, WK, 1>(ca, sa, cw, sw, g, ep, stream);
+    if (g.kblocks % 8 == 0 && aligned(sa, 8) && aligned(sw, 8))
+        return launch_product<T, kq::linear::kRows8, MF, NF, WK, 1>(ca, sa, cw, sw, g, ep, stream);
+    return launch_product<T, kq::linear::kBytes, MF, NF, WK, 1>(ca, sa, cw, sw, g, ep, stream);
+}
+
+template <class T>
+kq_status launch_linear(Kernel k, const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, const uint8_t *sw,
+                        int packed, const kq::linear::Geom &g, const kq::Epi &ep, kq_stream_t stream) {
+    switch (k) {
+        case kProduct11: return launch_any_product<T, 1, 1, 8>(ca, sa, cw, sw, packed, g, ep, stream);
+        case kProduct12: return launch_any_product<T, 1, 2, 4>(ca, sa, cw, sw, packed, g, ep, stream);
+        case kProduct22: return launch_any_product<T, 2, 2, 4>(ca, sa, cw, sw, packed, g, ep, stream);
+        case kTile64Deep: return launch_tiles<T, 1, 1, 4>(ca, sa, cw, sw, packed, g, ep, stream);
+        case kTile64: return launch_tiles<T, 1, 1, 2>(ca, sa, cw, sw, packed, g, ep, stream);
+        default: return launch_tiles<T, 2, 2, 2>(ca, sa, cw, sw, packed, g, ep, stream);
+    }
 }
 
 }  // namespace
@@ -264,31 +571,19 @@ kq_status kq_mxfp4_linear(const uint8_t *codes_a, const uint8_t *scales_a, const
     if (256 * (k / 2) >= lim || m * (k / 32) >= lim || n * (k / 32) >= lim || (255 * ldo + n) * es >= lim ||
         (255 * ldr + n) * es >= lim || (255 * ldz + n) * es >= lim)
         return KQ_ERR_UNSUPPORTED;
+    kq::Epi ep{bias, residual, O, Z, m, n, ldr, ldo, ldz, act, 16};
+    while (ep.align > es && (!aligned(O, ep.align) || !aligned(residual, ep.align) || !aligned(Z, ep.align) ||
+                             ((ldo | ldr | ldz) * es) % ep.align != 0))
+        ep.align /= 2;
+    const kq::linear::Geom g{(int)(k / 2), (int)(k / 32), (int)((k + 255) / 256), 0, 0};
     const bool big = packed ? aligned(scales_a, 16) && aligned(scales_w, 16)
                             : k % 128 == 0 && aligned(scales_a, 4) && aligned(scales_w, 4);
-    if (big && ((m + 255) / 256) * ((n + 255) / 256) >= 64)
-        return kqhost::gemm256_linear(codes_a, scales_a, codes_w, scales_w, packed, m, n, k, bias, act, type, residual,
-                                      ldr, O, ldo, Z, ldz, stream);
-    kq::linear::Geom g;
-    g.m = m;
-    g.n = n;
-    g.ldr = ldr;
-    g.ldo = ldo;
-    g.ldz = ldz;
-    g.kbytes = (int)(k / 2);
-    g.kblocks = (int)(k / 32);
-    g.stages = (int)((k + 255) / 256);
-    g.act = act;
-    g.vec = n % 4 == 0 && ldo % 4 == 0 && ldr % 4 == 0 && ldz % 4 == 0 && aligned(O, 4 * es) &&
-            aligned(residual, 4 * es) && aligned(Z, 4 * es);
-    if (type == KQ_BF16)
-        return packed ? launch_product<uint16_t, true>(codes_a, scales_a, codes_w, scales_w, g, bias, residual, O, Z,
-                                                       stream)
-                      : launch_product<uint16_t, false>(codes_a, scales_a, codes_w, scales_w, g, bias, residual, O, Z,
-                                                        stream);
-    return packed
-               ? launch_product<float, true>(codes_a, scales_a, codes_w, scales_w, g, bias, residual, O, Z, stream)
-               : launch_product<float, false>(codes_a, scales_a, codes_w, scales_w, g, bias, residual, O, Z, stream);
+    const Kernel kernel = choose_kernel(m, n, g.stages, packed != 0, big);
+    if (kernel == kTile256)
+        return kqhost::gemm256_linear(codes_a, scales_a, codes_w, scales_w, packed, k, type, ep, stream);
+    return type == KQ_BF16
+               ? launch_linear<uint16_t>(kernel, codes_a, scales_a, codes_w, scales_w, packed, g, ep, stream)
+               : launch_linear<float>(kernel, codes_a, scales_a, codes_w, scales_w, packed, g, ep, stream);
 }
 
 kq_status kq_mxfp4_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t *bytes) {
