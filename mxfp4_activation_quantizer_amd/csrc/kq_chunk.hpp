@@ -1,0 +1,66 @@
+// Elements of bf16 (as bit patterns) or fp32 rows, one by one and in chunks of
+// eight neighbours, for the kernels that take either type.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kq_device.hpp"
+
+namespace kq {
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const bf16x2_t v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+// Buffer over `bytes` bytes: loads past them read zeros, stores are dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void *p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
+}
+
+// Eight neighbouring channels as they are loaded.
+template <class T>
+struct Chunk;
+template <>
+struct Chunk<uint16_t> {
+    u32x4_t q;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
+        q = __builtin_amdgcn_raw_buffer_load_b128(r, 2 * ch, 0, 0);
+    }
+    __device__ __forceinline__ void widen(float x[8]) const { widen8(make_uint4(q[0], q[1], q[2], q[3]), x); }
+};
+template <>
+struct Chunk<float> {
+    u32x4_t a, b;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
+        a = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * ch, 0, 0);
+        b = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * ch + 16, 0, 0);
+    }
+    __device__ __forceinline__ void widen(float x[8]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[e] = __uint_as_float(a[e]);
+            x[4 + e] = __uint_as_float(b[e]);
+        }
+    }
+};
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const uint16_t *) {
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                   pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])},
+                                           r, 2 * ch, 0, 0);
+}
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const float *) {
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{__float_as_uint(y[0]), __float_as_uint(y[1]),
+                                                   __float_as_uint(y[2]), __float_as_uint(y[3])},
+                                           r, 4 * ch, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{__float_as_uint(y[4]), __float_as_uint(y[5]),
+                                                   __float_as_uint(y[6]), __float_as_uint(y[7])},
+                                           r, 4 * ch + 16, 0, 0);
+}
+
+}  // namespace kq

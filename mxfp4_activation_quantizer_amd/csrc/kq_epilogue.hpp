@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "kq_act.hpp"
+#include "kq_chunk.hpp"
 #include "kq_device.hpp"
 
 namespace kq {
@@ -21,15 +22,6 @@ struct Epi {
     int act;
     int align;  // every row of O, Z and the residual starts at a multiple of this many bytes (16, 8 or less)
 };
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const bf16x2_t v = {(__bf16)a, (__bf16)b};
-    return __builtin_bit_cast(uint32_t, v);
-}
-__device__ __forceinline__ float load1(const float *p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
-__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
 // N neighbouring elements in one piece. Non-temporal stores: outputs are not read again
 // here, so they should not push the operand lines that other workgroups still read.
@@ -75,34 +67,99 @@ __device__ __forceinline__ void load_bias(const Epi &ep, int64_t j, float (&b)[N
     for (int e = 0; e < N; ++e) b[e] = ep.bias && j + e < ep.n ? ep.bias[j + e] : 0.f;
 }
 
-// Row i (< m), columns j .. j + N - 1 (from z, the bias added). `whole`: all of them inside
-// n and in one aligned piece.
+// The residual of row i, columns j .. j + N - 1 (0 without one); they are inside n, in one
+// aligned piece. Apart from finish(), so that a lane has its rows' loads in flight together:
+// behind a store the compiler would keep each in its place.
 template <class T, int N>
-__device__ __forceinline__ void finish(float (&v)[N], const Epi &ep, int64_t i, int64_t j, bool whole) {
-    T *o = static_cast<T *>(ep.O) + i * ep.ldo + j;
-    T *z = static_cast<T *>(ep.Z) + i * ep.ldz + j;
-    const T *r = static_cast<const T *>(ep.residual) + i * ep.ldr + j;
-    if (whole) {
-        float add[N];
-        if (ep.residual) load_piece(r, add);
-        if (ep.Z) store_piece(z, v);
-        activate(v, ep.act);
-        if (ep.residual) {
+__device__ __forceinline__ void load_residual(const Epi &ep, int64_t i, int64_t j, float (&v)[N]) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[e] += add[e];
+    for (int e = 0; e < N; ++e) v[e] = 0.f;
+    if (ep.residual) load_piece(static_cast<const T *>(ep.residual) + i * ep.ldr + j, v);
+}
+
+// Those columns from z (the bias added) and the residual.
+template <class T, int N>
+__device__ __forceinline__ void finish(float (&v)[N], const float (&add)[N], const Epi &ep, int64_t i, int64_t j) {
+    if (ep.Z) store_piece(static_cast<T *>(ep.Z) + i * ep.ldz + j, v);
+    activate(v, ep.act);
+    if (ep.residual) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] += add[e];
+    }
+    store_piece(static_cast<T *>(ep.O) + i * ep.ldo + j, v);
+}
+
+// The same for one element: rows without alignment, and the columns of a last partial tile.
+template <class T>
+__device__ __forceinline__ float load_residual1(const Epi &ep, int64_t i, int64_t j) {
+    return ep.residual ? load1(static_cast<const T *>(ep.residual) + i * ep.ldr + j) : 0.f;
+}
+template <class T>
+__device__ __forceinline__ void finish1(float z, float add, const Epi &ep, int64_t i, int64_t j) {
+    float v[1] = {z};
+    if (ep.Z) store1(static_cast<T *>(ep.Z) + i * ep.ldz + j, z);
+    activate(v, ep.act);
+    store1(static_cast<T *>(ep.O) + i * ep.ldo + j, ep.residual ? v[0] + add : v[0]);
+}
+
+// Rows [0, ROWS) x columns [0, COLS) of a wave's fp32 sums, staged in LDS at reg in rows of COLS
+// with 16-byte chunk c at c ^ (row % (COLS / 4)), to O's rows i0 .. (those < rows) and columns
+// j0 ..: a lane takes 16 bytes of a row of O, or, where those are not aligned or not all inside
+// n, the wave takes a row's elements side by side.
+template <class T, int ROWS, int COLS>
+__device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep, int64_t i0, int rows, int64_t j0) {
+    constexpr int CH = COLS / 4;
+    const int lane = threadIdx.x & 63;
+    auto at = [&](int row, int chunk) { return reg + row * (COLS * 4) + 16 * (chunk ^ (row & (CH - 1))); };
+    if (rows <= 0) return;
+    if (ep.align >= 16 && j0 + COLS <= ep.n) {
+        constexpr int EC = 16 / (int)sizeof(T), kLanes = COLS / EC, kRows = 64 / kLanes, N = ROWS / kRows;
+        constexpr int U = N < 4 ? N : 4;
+        const int c = lane % kLanes, r0 = lane / kLanes;
+        const int64_t j = j0 + EC * c;
+        float bias[EC];
+        load_bias(ep, j, bias);
+        for (int i = 0; i < N; i += U) {
+            float add[U][EC];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int row = kRows * (i + u) + r0;
+                load_residual<T>(ep, i0 + (row < rows ? row : 0), j, add[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int row = kRows * (i + u) + r0;
+                float v[EC];
+#pragma unroll
+                for (int e4 = 0; e4 < EC / 4; ++e4) {
+                    const floatx4_t f = *reinterpret_cast<const floatx4_t *>(at(row, (EC / 4) * c + e4));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[4 * e4 + e] = f[e] + bias[4 * e4 + e];
+                }
+                if (row < rows) finish<T>(v, add[u], ep, i0 + row, j);
+            }
         }
-        store_piece(o, v);
         return;
     }
-    if (ep.Z) {
+    constexpr int kRows = 64 / COLS, N = ROWS / kRows, U = 8;  // kRows rows side by side
+    const int c = lane % COLS, r0 = lane / COLS;
+    const int64_t j = j0 + c;
+    if (j >= ep.n) return;
+    const float bias = ep.bias ? ep.bias[j] : 0.f;
+    for (int i = 0; i < N; i += U) {
+        float add[U];
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (j + e < ep.n) store1(z + e, v[e]);
+        for (int u = 0; u < U; ++u) {
+            const int row = kRows * (i + u) + r0;
+            add[u] = load_residual1<T>(ep, i0 + (row < rows ? row : 0), j);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = kRows * (i + u) + r0;
+            const float z = *reinterpret_cast<const float *>(at(row, c >> 2) + 4 * (c & 3)) + bias;
+            if (row < rows) finish1<T>(z, add[u], ep, i0 + row, j);
+        }
     }
-    activate(v, ep.act);
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-        if (j + e < ep.n) store1(o + e, ep.residual ? v[e] + load1(r + e) : v[e]);
 }
 
 }  // namespace kq

@@ -559,12 +559,9 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     uint8_t *reg = smem + 32768 * w;
     if constexpr (EPI) {
-        // Always staged in fp32, 64 columns a pass: a lane then holds EC neighbouring columns of a
-        // row, to which bias, activation and residual are applied where they leave in whole
-        // 128-byte (bf16) or 256-byte (fp32) runs.
+        // Always staged in fp32, 64 columns a pass: bias, activation and residual are applied where
+        // whole 128-byte (bf16) or 256-byte (fp32) runs of a row leave.
         typedef typename std::conditional<B16, uint16_t, float>::type T;
-        constexpr int EC = B16 ? 8 : 4, kLanes = 64 / EC, kRows = 64 / kLanes;
-        const int c = lane % kLanes;
 #pragma unroll
         for (int pass = 0; pass < NB / 2; ++pass) {
 #pragma unroll
@@ -577,23 +574,8 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
                         *reinterpret_cast<floatx4_t *>(reg + row * 256 + 16 * (chunk ^ (row & 15))) = floatx4_t{
                             acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
                     }
-            const int col = wn + 64 * pass + EC * c;  // from n0
-            float bias[EC];
-            load_bias(ep, n0 + col, bias);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll 4
-            for (int i = 0; i < 128 / kRows; ++i) {
-                const int row = kRows * i + lane / kLanes, orow = wm + row;
-                float v[EC];
-#pragma unroll
-                for (int e4 = 0; e4 < EC / 4; ++e4) {
-                    const floatx4_t f = *reinterpret_cast<const floatx4_t *>(
-                        reg + row * 256 + 16 * (((EC / 4) * c + e4) ^ (row & 15)));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[4 * e4 + e] = f[e] + bias[4 * e4 + e];
-                }
-                if (orow < rows_a) finish<T>(v, ep, m0 + orow, n0 + col, whole);
-            }
+            finish_staged<T, 128, 64>(reg, ep, m0 + wm, rows_a - wm, n0 + wn + 64 * pass);
         }
         return;
     }

@@ -162,11 +162,20 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
             z[0] += v.x; z[1] += v.y; z[2] += v.z; z[3] += v.w;
         }
         if (r < rows_a && 4 * c4 < rows_w) {
+            const int64_t i = m0 + r, j = n0 + 4 * c4;
             float b[4];
-            load_bias(ep, n0 + 4 * c4, b);
+            load_bias(ep, j, b);
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[e] += b[e];
-            finish<T>(z, ep, m0 + r, n0 + 4 * c4, ep.align >= 4 * (int)sizeof(T) && n0 + 4 * c4 + 4 <= ep.n);
+            if (ep.align >= 4 * (int)sizeof(T) && j + 4 <= ep.n) {
+                float add[4];
+                load_residual<T>(ep, i, j, add);
+                finish<T>(z, add, ep, i, j);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < ep.n) finish1<T>(z[e], load_residual1<T>(ep, i, j + e), ep, i, j + e);
+            }
         }
     }
 }
@@ -379,8 +388,8 @@ __global__ __launch_bounds__(320) void tile_kernel(const uint8_t *__restrict__ c
     // every load into LDS has landed (the ones past k too) and every wave is done with the stages
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     // Each wave stages its block in fp32 in its own region, rows of 32 FB columns with 16-byte chunk c
-    // at c ^ (row % CH), and reads it back as pieces of EC columns of a row.
-    constexpr int WM = TM / 2, WN = TN / 2, CH = WN / 4, EC = 16 / (int)sizeof(T), kLanes = WN / EC, kRows = 64 / kLanes;
+    // at c ^ (row % CH), and reads it back row by row.
+    constexpr int WM = TM / 2, WN = TN / 2, CH = WN / 4;
     uint8_t *reg = smem + w * (WM * WN * 4);
 #pragma unroll
     for (int a = 0; a < FA; ++a)
@@ -393,46 +402,98 @@ __global__ __launch_bounds__(320) void tile_kernel(const uint8_t *__restrict__ c
                     floatx4_t{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
             }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    const int c = lane % kLanes;
-    const int64_t col = n0 + wn + EC * c;
-    const bool whole = ep.align >= 16 && col + EC <= ep.n;
-    if (col >= ep.n) return;
-    float bias[EC];
-    load_bias(ep, col, bias);
-#pragma unroll 4
-    for (int i = 0; i < WM / kRows; ++i) {
-        const int row = kRows * i + lane / kLanes;
-        float v[EC];
-#pragma unroll
-        for (int e4 = 0; e4 < EC / 4; ++e4) {
-            const floatx4_t f = *reinterpret_cast<const floatx4_t *>(
-                reg + row * (WN * 4) + 16 * (((EC / 4) * c + e4) ^ (row & (CH - 1))));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * e4 + e] = f[e] + bias[4 * e4 + e];
-        }
-        if (wm + row < rows_a) finish<T>(v, ep, m0 + wm + row, col, whole);
-    }
+    finish_staged<T, WM, WN>(reg, ep, m0 + wm, rows_a - wm, n0 + wn);
 }
 
 // Backward of the epilogue, any layout: workgroup (x, p) takes 256 columns of the rows
-// p, p + parts, ...
+// p, p + parts, ..., four of them at a time.
 template <class T>
 __global__ __launch_bounds__(256) void backward_any_kernel(const T *__restrict__ dO, int64_t lddo,
                                                            const T *__restrict__ Z, int64_t ldz, int64_t m, int64_t n,
                                                            int act, T *__restrict__ dZ, int64_t lddz, int parts,
                                                            float *__restrict__ part) {
+    constexpr int U = 4;
     const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= n) return;
     const int p = (int)blockIdx.y;
     float s = 0.f;
-    for (int64_t i = p; i < m; i += parts) {
-        float d[1] = {load1(dO + i * lddo + c)}, z[1] = {0.f};
-        if (act != KQ_ACT_NONE) z[0] = load1(Z + i * ldz + c);
+    for (int64_t i = p; i < m; i += (int64_t)U * parts) {
+        float d[U], z[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = i + (int64_t)u * parts;
+            d[u] = row < m ? load1(dO + row * lddo + c) : 0.f;
+            z[u] = act != KQ_ACT_NONE && row < m ? load1(Z + row * ldz + c) : 0.f;
+        }
         activate_grad(d, z, act);
-        if (dZ) store1(dZ + i * lddz + c, d[0]);
-        s += d[0];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = i + (int64_t)u * parts;
+            if (row >= m) break;
+            if (dZ) store1(dZ + row * lddz + c, d[u]);
+            s += d[u];
+        }
     }
     if (part) part[p * n + c] = s;
+}
+
+// Backward of the epilogue, rows of whole 16-byte pieces: wave w of workgroup (x, p) takes 512
+// columns (8 per lane: 1 KB of a bf16 row) of the rows p + parts (4 j + w), U of them in
+// flight; the waves' column sums meet in LDS in wave order. Bound by HBM: two reads and a
+// write per element against about 25 vector operations of 39 T/s for gelu_tanh.
+template <class T>
+__global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO, int64_t lddo,
+                                                       const T *__restrict__ Z, int64_t ldz, int64_t m, int64_t n,
+                                                       int act, T *__restrict__ dZ, int64_t lddz, int parts,
+                                                       float *__restrict__ part) {
+    constexpr int U = 4;
+    __shared__ float4 join[4][2][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t c0 = (int64_t)blockIdx.x * 512, left = n - c0 < 512 ? n - c0 : 512;
+    const int64_t bytes = left * (int)sizeof(T);
+    const uint32_t ch = 8u * lane;
+    const int p = (int)blockIdx.y;
+    const bool reads_z = act != KQ_ACT_NONE;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int64_t step = 4 * (int64_t)parts;
+    for (int64_t i = p + (int64_t)parts * wave; i < m; i += U * step) {
+        Chunk<T> d[U], z[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = i + u * step;
+            const bool in = row < m;
+            d[u].load(row_rsrc(dO + (in ? row : i) * lddo + c0, in ? bytes : 0), ch);
+            if (reads_z) z[u].load(row_rsrc(Z + (in ? row : i) * ldz + c0, in ? bytes : 0), ch);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = i + u * step;
+            if (row >= m) break;
+            float v[8], x[8];
+            d[u].widen(v);
+            if (reads_z) {
+                z[u].widen(x);
+                activate_grad(v, x, act);
+            }
+            if (dZ) store8(row_rsrc(dZ + row * lddz + c0, bytes), ch, v, dZ);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += v[e];
+        }
+    }
+    if (!part) return;
+    join[wave][0][lane] = make_float4(s[0], s[1], s[2], s[3]);
+    join[wave][1][lane] = make_float4(s[4], s[5], s[6], s[7]);
+    __syncthreads();
+    if (wave < 2) {
+        float4 a = join[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+            const float4 o = join[w][wave][lane];
+            a.x += o.x; a.y += o.y; a.z += o.z; a.w += o.w;
+        }
+        const int64_t c = c0 + ch + 4 * wave;
+        if (c < n) *reinterpret_cast<float4 *>(part + p * n + c) = a;
+    }
 }
 
 }  // namespace linear
@@ -455,6 +516,26 @@ using kqhost::sizes_fit;
 
 bool good_type(int type) { return type == KQ_F32 || type == KQ_BF16; }
 bool good_act(int act) { return act >= KQ_ACT_NONE && act <= KQ_ACT_GELU_TANH; }
+
+// Parts of the bias gradient's sum: those of m rows, at most as many as give 4096 workgroups of
+// 512 columns (more only make the partial sums larger: 512 parts of 16384 columns are 34 MB).
+int64_t column_parts(int64_t m, int64_t n) {
+    const int64_t strips = (n + 511) / 512, most = 4096 / (strips < 64 ? strips : 64), p = kqhost::row_parts(m);
+    return p < most ? p : most;
+}
+
+template <class T>
+void launch_backward(const void *dO, int64_t lddo, const void *Z, int64_t ldz, int64_t m, int64_t n, int act, void *dZ,
+                     int64_t lddz, int64_t parts, float *part, bool vec, kq_stream_t stream) {
+    const int64_t columns = vec ? 512 : 256;
+    const dim3 grid((unsigned)((n + columns - 1) / columns), (unsigned)parts);
+    if (vec)
+        hipLaunchKernelGGL((kq::linear::backward_kernel<T>), grid, dim3(256), 0, (hipStream_t)stream, (const T *)dO,
+                           lddo, (const T *)Z, ldz, m, n, act, (T *)dZ, lddz, (int)parts, part);
+    else
+        hipLaunchKernelGGL((kq::linear::backward_any_kernel<T>), grid, dim3(256), 0, (hipStream_t)stream,
+                           (const T *)dO, lddo, (const T *)Z, ldz, m, n, act, (T *)dZ, lddz, (int)parts, part);
+}
 
 // The launch's work-items are counted in 32 bits.
 bool groups_fit(int64_t groups, int threads) { return groups <= (int64_t)0xFFFFFFFF / threads; }
@@ -482,46 +563,44 @@ kq_status launch_tiles(const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, 
     return launched();
 }
 
-// Which kernel a product of m x n outputs over `stages` 256-k stages runs on.
-//
-// Few rows or few tiles: product_kernel, whose waves share a tile's k. Its tile is the
-// smallest that needs at most one workgroup per compute unit (at k = 4096, us on MI355X:
-// 8 x 4096 4.9 with 16 x 16 tiles, 5.7 with 16 x 32; 64 x 1152 6.4 with 16 x 32, 7.8 with
-// 16 x 16; 64 x 4096 7.2 with 32 x 32, 8.1 with 64 x 64 tiles through LDS); up to 16 rows
-// take it at any n (1 x 16384 8.7 against 9.7 through LDS).
-//
-// Otherwise the least of four estimates, in us, fitted to 17 measured shapes from
-// 128 x 512 x 512 to 8192 x 4096 x 1024 (within about 15%): a launch, a stage's latency while
-// a compute unit has one tile, and each further tile's share. E.g. measured at k = 4096, for
-// 64 x 64 tiles 4 and 2 stages deep, 128 x 128 and 256 x 256:
-//   128 x 4096   8.2   10.8   16.2   23.1
-//   512 x 4096  14.7   12.1   16.5   24.0
-//   1024 x 4096 25.7   22.8   17.2   24.5
-//   4096 x 4096 89.2   76.0   53.2   42.7
+// Which kernel a product of m x n outputs over `stages` 256-k stages runs on: the least of
+// seven estimates, in us, fitted to 30 measured shapes from 1 x 1152 x 4608 to 8192 x 4096 x 1024
+// (most within 15%): a launch and what a stage takes while a compute unit has one tile, and
+// each further round of tiles. Up to 16 rows only the kernel that splits k is considered (1 x
+// 16384 x 8192 17.4 us, 20.9 with 64 x 64 tiles). Measured at k = 4096, in the order of the list:
+//      8 x 4096   4.9   5.7
+//     64 x 4096  12.7   9.4   7.2   8.2  10.8
+//    128 x 4096  21.7  15.8  11.6   8.2  10.8  16.2  23.1
+//    512 x 4096        54.4  37.8  14.7  12.1  16.5  24.0
+//   1024 x 4096              72.3  25.7  22.8  17.2  24.5
+//   4096 x 4096             281    89.2  76.0  53.2  42.7
 enum Kernel { kProduct11, kProduct12, kProduct22, kTile64Deep, kTile64, kTile128, kTile256 };
 
 Kernel choose_kernel(int64_t m, int64_t n, int stages, bool packed, bool can256) {
     const int cus = kqhost::compute_units();
-    auto tiles = [&](int64_t tm, int64_t tn) { return (double)((m + tm - 1) / tm) * (double)((n + tn - 1) / tn); };
-    if (m <= 16) return tiles(16, 16) < 2 * cus ? kProduct11 : kProduct12;
-    if (tiles(32, 32) <= cus)
-        return tiles(16, 16) <= cus ? kProduct11 : tiles(16, 32) <= cus ? kProduct12 : kProduct22;
-    const double st = stages, t64 = tiles(64, 64) / cus, t128 = ceil(tiles(128, 128) / cus), t256 = tiles(256, 256);
-    const double deep = 3 + ceil(t64) * 0.33 * st;
-    const double shallow = fmax(2.8 + 0.5 * st, 1.2 + t64 * (0.325 * st + 0.7));
-    const double mid = 3 + 0.15 * st + t128 * (0.62 * st + 2.1);
-    Kernel k = kTile64Deep;
-    double best = deep;
-    if (shallow < best) k = kTile64, best = shallow;
-    if (mid < best) k = kTile128, best = mid;
+    const double st = stages;
+    auto tiles = [&](int64_t tm, int64_t tn) {  // per compute unit
+        return (double)((m + tm - 1) / tm) * (double)((n + tn - 1) / tn) / cus;
+    };
+    Kernel best = kProduct11;
+    double least = 2.0 + ceil(tiles(16, 16)) * 0.16 * st;
+    auto consider = [&](Kernel k, double us) {
+        if (us < least) best = k, least = us;
+    };
+    consider(kProduct12, 2.0 + ceil(tiles(16, 32)) * 0.22 * st);
+    if (m <= 16) return best;
+    consider(kProduct22, 2.3 + ceil(tiles(32, 32)) * 0.29 * st);
+    const double t64 = tiles(64, 64);
+    consider(kTile64Deep, 3.0 + ceil(t64) * 0.33 * st);
+    consider(kTile64, fmax(2.8 + 0.5 * st, 1.2 + t64 * (0.325 * st + 0.7)));
+    consider(kTile128, 3.0 + 0.15 * st + ceil(tiles(128, 128)) * (0.62 * st + 2.1));
     if (can256) {
         // whole rounds, and a last one of at most half the compute units in half tiles
         const double full = 13.5 + (packed ? 1.8 : 2.05) * st, half = 7 + (packed ? 1.0 : 1.4) * st;
-        const double rem = fmod(t256, cus);
-        const double big = floor(t256 / cus) * full + (rem == 0 ? 0 : 2 * rem <= cus ? half : full);
-        if (big < best) k = kTile256;
+        const double t256 = tiles(256, 256), rem = t256 - floor(t256);
+        consider(kTile256, floor(t256) * full + (rem == 0 ? 0 : rem <= 0.5 ? half : full));
     }
-    return k;
+    return best;
 }
 
 template <class T, int MF, int NF, int WK>
@@ -591,7 +670,7 @@ kq_status kq_mxfp4_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t
     *bytes = 0;
     if (m < 0 || n < 0) return KQ_ERR_SHAPE;
     if (!sizes_fit({m, n})) return KQ_ERR_UNSUPPORTED;
-    const int64_t parts = kqhost::row_parts(m);
+    const int64_t parts = column_parts(m, n);
     if (parts > 1) *bytes = parts * n * 4;
     return KQ_OK;
 }
@@ -610,7 +689,7 @@ kq_status kq_mxfp4_linear_backward(const void *dO, int64_t lddo, const void *Z, 
     if (!dO || (reads_z && !Z) || (!dZ && !dbias)) return KQ_ERR_NULL;
     const uintptr_t es = type == KQ_BF16 ? 2 : 4;
     if (!aligned(dO, es) || (reads_z && !aligned(Z, es)) || !aligned(dZ, es)) return KQ_ERR_ALIGN;
-    const int64_t parts = kqhost::row_parts(m);
+    const int64_t parts = column_parts(m, n);
     float *part = dbias;
     if (dbias && parts > 1) {
         if (!workspace) return KQ_ERR_NULL;
@@ -618,17 +697,15 @@ kq_status kq_mxfp4_linear_backward(const void *dO, int64_t lddo, const void *Z, 
         if (workspace_bytes < parts * n * 4) return KQ_ERR_SHAPE;
         part = static_cast<float *>(workspace);
     }
-    const dim3 grid((unsigned)((n + 255) / 256), (unsigned)parts);
-    if (type == KQ_BF16)
-        hipLaunchKernelGGL((kq::linear::backward_any_kernel<uint16_t>), grid, dim3(256), 0, (hipStream_t)stream,
-                           (const uint16_t *)dO, lddo, (const uint16_t *)Z, ldz, m, n, act, (uint16_t *)dZ, lddz,
-                           (int)parts, part);
-    else
-        hipLaunchKernelGGL((kq::linear::backward_any_kernel<float>), grid, dim3(256), 0, (hipStream_t)stream,
-                           (const float *)dO, lddo, (const float *)Z, ldz, m, n, act, (float *)dZ, lddz, (int)parts,
-                           part);
+    const int64_t per16 = 16 / es;
+    const bool vec = n % 8 == 0 && aligned(dO, 16) && lddo % per16 == 0 && (!reads_z || (aligned(Z, 16) && ldz % per16 == 0)) &&
+                     aligned(dZ, 16) && lddz % per16 == 0 && aligned(part, 16);
+    if (type == KQ_BF16) launch_backward<uint16_t>(dO, lddo, Z, ldz, m, n, act, dZ, lddz, parts, part, vec, stream);
+    else launch_backward<float>(dO, lddo, Z, ldz, m, n, act, dZ, lddz, parts, part, vec, stream);
+    const kq_status s = launched();
+    if (s != KQ_OK) return s;
     if (dbias && parts > 1) return kqhost::reduce_parts(part, nullptr, parts, n, dbias, nullptr, stream);
-    return launched();
+    return KQ_OK;
 }
 
 }  // extern "C"

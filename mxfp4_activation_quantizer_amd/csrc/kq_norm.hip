@@ -8,18 +8,21 @@
 //   y = (x - mean) rstd w + b.
 // The mean is summed in 64 bits: a mean near zero is what is left of values
 // that cancel, and 32 bits would leave it with the rounding of the largest. It
-// is kept as c + off (c its fp32 rounding, off the rest), and values are
-// centred as (x - c) - off, so that the rounding of the mean itself (2^-24
-// |mean|, 1000 times the rest for a mean of 3000 beside a deviation of 1) never
-// enters y. The squares are summed around it, with nothing large to cancel.
+// is kept as c + off (c its fp32 rounding, off the rest), so that the rounding
+// of the mean itself (2^-24 |mean|, 1000 times the rest for a mean of 3000
+// beside a deviation of 1) never enters y: with v = x - c,
+//   sum (x - mean)^2 = sum v^2 - d off^2,  (x - mean) rstd = v rstd - off rstd,
+// one subtraction and two multiply-adds per element.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <initializer_list>
 #include <type_traits>
+#include <utility>
 
 #include "kq.h"
+#include "kq_chunk.hpp"
 #include "kq_device.hpp"
 #include "kq_host.hpp"
 
@@ -27,11 +30,6 @@ namespace kq {
 namespace norm {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ float load1(const float *p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
-__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
 // The value of v in the lane that differs: DPP patterns within 16 lanes.
 template <int CTRL>
@@ -86,15 +84,17 @@ __device__ __forceinline__ V block_sum(V v) {
 
 // A row's statistics.
 struct Stats {
-    float c, off, rstd;
-    __device__ __forceinline__ float centred(float x) const { return (x - c) - off; }
+    float c, off, rstd, shift;
+    __device__ __forceinline__ float normed(float x) const { return fmaf(x - c, rstd, shift); }
     __device__ __forceinline__ void set_mean(double sum, double inv) {
         const double mean = sum * inv;
         c = (float)mean;
         off = (float)(mean - c);
     }
-    __device__ __forceinline__ void set_rstd(float squares, double inv, float eps) {
-        rstd = __builtin_amdgcn_rsqf(fmaf(squares, (float)inv, eps));  // 1 ulp
+    __device__ __forceinline__ void set_rstd(float squares, double inv, float eps) {  // sum (x - c)^2
+        const float var = fmaxf(fmaf(squares, (float)inv, -off * off), 0.f);
+        rstd = __builtin_amdgcn_rsqf(var + eps);  // 1 ulp
+        shift = -off * rstd;
     }
 };
 
@@ -108,7 +108,7 @@ __device__ __forceinline__ Stats row_stats(const T *x, int64_t d, float eps) {
     st.set_mean(block_sum(s), inv);
     float q = 0.f;
     for (int64_t c = threadIdx.x; c < d; c += kThreads) {
-        const float v = st.centred(load1(x + c));
+        const float v = load1(x + c) - st.c;
         q = fmaf(v, v, q);
     }
     st.set_rstd(block_sum(q), inv, eps);
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void forward_any_kernel(const T *__restri
         const T *x = X + i * ldx;
         const Stats st = row_stats(x, d, eps);
         for (int64_t c = threadIdx.x; c < d; c += kThreads) {
-            const float h = st.centred(load1(x + c)) * st.rstd;
+            const float h = st.normed(load1(x + c));
             store1(Y + i * ldy + c, fmaf(h, w ? w[c] : 1.0f, b ? b[c] : 0.0f));
         }
         if (threadIdx.x == 0) {
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(kThreads) void quantize_wide_kernel(const T *__rest
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = st.centred(load1(x + c + e)) * st.rstd;
+                const float h = st.normed(load1(x + c + e));
                 y[e] = fmaf(h, w ? w[c + e] : 1.0f, b ? b[c + e] : 0.0f);
             }
             if (factors) {
@@ -274,54 +274,6 @@ __global__ __launch_bounds__(kThreads) void quantize_wide_kernel(const T *__rest
 // are in flight while a row is summed. With W = 1 a workgroup's 4 waves walk
 // rows of their own and there is no barrier in the loop.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void *p, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
-}
-
-// Eight neighbouring channels as they are loaded.
-template <class T>
-struct Chunk;
-template <>
-struct Chunk<uint16_t> {
-    u32x4_t q;
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
-        q = __builtin_amdgcn_raw_buffer_load_b128(r, 2 * ch, 0, 0);
-    }
-    __device__ __forceinline__ void widen(float x[8]) const { widen8(make_uint4(q[0], q[1], q[2], q[3]), x); }
-};
-template <>
-struct Chunk<float> {
-    u32x4_t a, b;
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
-        a = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * ch, 0, 0);
-        b = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * ch + 16, 0, 0);
-    }
-    __device__ __forceinline__ void widen(float x[8]) const {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[e] = __uint_as_float(a[e]);
-            x[4 + e] = __uint_as_float(b[e]);
-        }
-    }
-};
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const bf16x2_t v = {(__bf16)a, (__bf16)b};
-    return __builtin_bit_cast(uint32_t, v);
-}
-__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const uint16_t *) {
-    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
-                                                   pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])},
-                                           r, 2 * ch, 0, 0);
-}
-__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const float *) {
-    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{__float_as_uint(y[0]), __float_as_uint(y[1]),
-                                                   __float_as_uint(y[2]), __float_as_uint(y[3])},
-                                           r, 4 * ch, 0, 0);
-    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{__float_as_uint(y[4]), __float_as_uint(y[5]),
-                                                   __float_as_uint(y[6]), __float_as_uint(y[7])},
-                                           r, 4 * ch + 16, 0, 0);
-}
-
 // Parameters of a lane's chunk (fp32; `none` where there are none or past d).
 __device__ __forceinline__ void load_params(const float *p, int64_t ch, int64_t d, float none, float v[8]) {
 #pragma unroll
@@ -376,7 +328,7 @@ __device__ __forceinline__ Stats chunk_stats(const Chunk<T> (&raw)[C], bool last
         raw[c].widen(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float v = st.centred(x[e]);
+            const float v = x[e] - st.c;
             qc = fmaf(v, v, qc);
         }
         q += c < C - 1 || last ? qc : 0.f;
@@ -428,7 +380,7 @@ __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__re
             float x[8];
             raw[c].widen(x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = fmaf(st.centred(x[e]) * st.rstd, pw[c][e], pb[c][e]);
+            for (int e = 0; e < 8; ++e) x[e] = fmaf(st.normed(x[e]), pw[c][e], pb[c][e]);
             store8(out, ch[c], x, Y);
         }
         if (lane == 0 && wr == 0) {
@@ -587,7 +539,7 @@ __global__ __launch_bounds__(kGroupThreads<W>) void quantize_kernel(
     const int64_t step = (int64_t)gridDim.x * R;
     int64_t row = (int64_t)blockIdx.x * R + (W == 1 ? wave : 0);
     if (row >= m) return;
-    uint32_t ch[C];
+    uint32_t ch[C], scale_at[C];
     float pw[C][8], pb[C][8], coef[C][16];
     bool shear[C];
     const double inv = 1.0 / (double)d;
@@ -603,6 +555,12 @@ __global__ __launch_bounds__(kGroupThreads<W>) void quantize_kernel(
     for (int c = 0; c < C; ++c) {
         load_params(w, ch[c], d, 1.0f, pw[c]);
         load_params(b, ch[c], d, 0.0f, pb[c]);
+        // the block's scale byte from its row's first, stored by the quad's first lane; the others and
+        // the blocks past d are past every record count
+        const uint32_t j = ch[c] / 32;
+        scale_at[c] = sub || ch[c] >= d ? 0xFFFFFFF0u
+                      : packed          ? (uint32_t)((j >> 3) * m * 8) + 4 * (j & 1) + ((j & 7) >> 1)
+                                        : j;
         shear[c] = true;
 #pragma unroll
         for (int i = 0; i < 16; ++i) coef[c][i] = 0.f;
@@ -630,12 +588,13 @@ __global__ __launch_bounds__(kGroupThreads<W>) void quantize_kernel(
         for (int c = 0; c < C; ++c) next[c].load(ahead, ch[c]);
         const Stats st = chunk_stats<T, W, C>(raw, last, d, inv, eps, red_sum, red_sq, wr);
         const auto rc = row_rsrc(codes + row * (d / 2), d / 2);
+        const auto rs = packed ? row_rsrc(scales + 8 * row, m * (d / 32) - 8 * row) : row_rsrc(scales + row * (d / 32), d / 32);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float y[8];
             raw[c].widen(y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = fmaf(st.centred(y[e]) * st.rstd, pw[c][e], pb[c][e]);
+            for (int e = 0; e < 8; ++e) y[e] = fmaf(st.normed(y[e]), pw[c][e], pb[c][e]);
             if (factors) {
                 if (shear[c]) apply_coefs<true>(y, coef[c]);
                 else apply_coefs<false>(y, coef[c]);
@@ -643,11 +602,7 @@ __global__ __launch_bounds__(kGroupThreads<W>) void quantize_kernel(
             uint32_t sbyte;
             const uint32_t q = quantize_quad_f32(y, sbyte);
             __builtin_amdgcn_raw_buffer_store_b32(q, rc, ch[c] / 2, 0, 0);
-            if (sub == 0 && ch[c] < d) {
-                const int64_t j = ch[c] / 32;
-                scales[packed ? ((j >> 3) * m + row) * 8 + 4 * (j & 1) + ((j & 7) >> 1) : row * (d / 32) + j] =
-                    (uint8_t)sbyte;
-            }
+            __builtin_amdgcn_raw_buffer_store_b8((uint8_t)sbyte, rs, scale_at[c], 0, 0);
             if (y_debug) store8(row_rsrc(y_debug + row * d, 4 * d), ch[c], y, y_debug);
         }
         if (lane == 0 && wr == 0) {
@@ -689,33 +644,34 @@ bool vector_rows(int type, int64_t d, std::initializer_list<const void *> ptrs, 
     return true;
 }
 
-// Waves per row and chunks per lane. Many rows: the fewest waves that hold the row at `most`
-// chunks per lane, so that a wave has work between its sums. Rows too few to give every
-// compute unit one: one chunk per lane where 16 waves reach, so that a row's time is one
-// memory latency.
-struct RowShape {
-    int waves, chunks;
-};
-RowShape row_shape(int64_t m, int64_t d, int most) {
-    const int64_t pieces = (d + 511) / 512;  // wave-wide chunks of the row
-    const bool few = m < kqhost::compute_units();
-    RowShape s{1, 0};
-    while (s.waves < (few ? 16 : 8) && pieces > s.waves * (few ? 1 : most)) s.waves *= 2;
-    s.chunks = (int)((pieces + s.waves - 1) / s.waves);
-    return s;
-}
-
-// Calls f(W, C) (integral constants) with the shape; false if it is not built.
+// Waves per row and chunks of 8 channels per lane for a row of `pieces` 512-channel pieces: the
+// first entry W, C of a kernel's list that holds it, f(W, C); false if none does.
 template <class F>
-bool with_shape(RowShape s, F f) {
-    using std::integral_constant;
-#define KQ_SHAPE(W, C) \
-    if (s.waves == W && s.chunks == C) return f(integral_constant<int, W>(), integral_constant<int, C>()), true;
-    KQ_SHAPE(1, 1) KQ_SHAPE(1, 2) KQ_SHAPE(2, 1) KQ_SHAPE(2, 2) KQ_SHAPE(4, 1) KQ_SHAPE(4, 2)
-    KQ_SHAPE(8, 1) KQ_SHAPE(8, 2) KQ_SHAPE(8, 3) KQ_SHAPE(8, 4) KQ_SHAPE(16, 1) KQ_SHAPE(16, 2)
-#undef KQ_SHAPE
+bool first_shape(int64_t, std::integer_sequence<int>, F) {
     return false;
 }
+template <int W, int C, int... Rest, class F>
+bool first_shape(int64_t pieces, std::integer_sequence<int, W, C, Rest...>, F f) {
+    if (pieces > W * C) return first_shape(pieces, std::integer_sequence<int, Rest...>(), f);
+    f(std::integral_constant<int, W>(), std::integral_constant<int, C>());
+    return true;
+}
+
+// Many rows: few waves per row, so that a wave has work between its sums, with as few empty
+// places as the lists allow (us at 8192 x 1152: norm 8.5 with 1 x 3, 10.2 with 2 x 2, 11.0 with
+// 4 x 1; norm and quantizer 12.5, 14.6, 14.8).
+// Above three waves, multiples of four: a workgroup's waves are dealt to the four SIMDs from
+// the first on, so 5 waves take a second place on one of them in every workgroup. 3 x 3 is for
+// rows of 9 pieces (norm and quantizer 8192 x 4608: 28.7 us, 32.5 with 4 x 3, 41 with 8 x 2).
+using Many = std::integer_sequence<int, 1, 1, 1, 2, 1, 3, 2, 2, 4, 2, 3, 3, 4, 3, 8, 2, 8, 3, 8, 4>;
+// Fewer rows than compute units: one chunk per lane where 16 waves reach, so that a row's time
+// is one memory latency.
+using Few = std::integer_sequence<int, 1, 1, 2, 1, 4, 1, 8, 1, 16, 1, 16, 2>;
+// Backward: at most one workgroup per compute unit (the parts of the parameters' sums), so
+// as many waves as the row has pieces, from 2048 channels on.
+using Backward = std::integer_sequence<int, 1, 1, 1, 2, 1, 3, 4, 1, 8, 1, 8, 2, 8, 3, 16, 2>;
+
+int64_t pieces_of(int64_t d) { return (d + 511) / 512; }
 
 // Workgroups of `waves` waves (4 rows at a time when waves == 1) that keep `per_cu` waves on
 // every compute unit, or one per row where there are fewer.
@@ -728,12 +684,13 @@ unsigned persistent_grid(int64_t m, int waves, int per_cu) {
 template <class T>
 kq_status launch_forward(const void *X, int64_t m, int64_t d, int64_t ldx, const float *weight, const float *bias,
                          float eps, void *Y, int64_t ldy, float *mean, float *rstd, bool vec, kq_stream_t stream) {
-    const RowShape s = row_shape(m, d, 2);
-    if (!vec || !with_shape(s, [&](auto W, auto C) {
-            hipLaunchKernelGGL((kq::norm::forward_kernel<T, W(), C()>), dim3(persistent_grid(m, s.waves, 16)),
-                               dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx,
-                               weight, bias, eps, (T *)Y, ldy, mean, rstd);
-        }))
+    auto go = [&](auto W, auto C) {
+        hipLaunchKernelGGL((kq::norm::forward_kernel<T, W(), C()>), dim3(persistent_grid(m, W(), W() == 3 ? 12 : 16)),
+                           dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx, weight,
+                           bias, eps, (T *)Y, ldy, mean, rstd);
+    };
+    if (!vec || !(m < kqhost::compute_units() ? first_shape(pieces_of(d), Few(), go)
+                                              : first_shape(pieces_of(d), Many(), go)))
         hipLaunchKernelGGL((kq::norm::forward_any_kernel<T>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
                            (hipStream_t)stream, (const T *)X, m, d, ldx, weight, bias, eps, (T *)Y, ldy, mean, rstd);
     return launched();
@@ -743,12 +700,12 @@ template <class T>
 kq_status launch_backward(const void *dY, int64_t lddy, const void *X, int64_t ldx, int64_t m, int64_t d,
                           const float *weight, const float *mean, const float *rstd, void *dX, int64_t lddx,
                           int64_t parts, float *pw, float *pb, bool params, bool vec, kq_stream_t stream) {
-    if (vec && with_shape(row_shape(parts, d, 2), [&](auto W, auto C) {
-            hipLaunchKernelGGL((kq::norm::backward_kernel<T, W(), C()>), dim3((unsigned)parts),
-                               dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)dY, lddy,
-                               (const T *)X, ldx, m, d, weight, mean, rstd, (T *)dX, lddx, (int)parts, pw, pb);
-        }))
-        return launched();
+    auto go = [&](auto W, auto C) {
+        hipLaunchKernelGGL((kq::norm::backward_kernel<T, W(), C()>), dim3((unsigned)parts),
+                           dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)dY, lddy,
+                           (const T *)X, ldx, m, d, weight, mean, rstd, (T *)dX, lddx, (int)parts, pw, pb);
+    };
+    if (vec && first_shape(pieces_of(d), Backward(), go)) return launched();
     hipLaunchKernelGGL((kq::norm::backward_dx_any_kernel<T>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
                        (hipStream_t)stream, (const T *)dY, lddy, (const T *)X, ldx, m, d, weight, mean, rstd, (T *)dX,
                        lddx);
@@ -763,12 +720,15 @@ template <class T>
 kq_status launch_quantize(const void *X, int64_t m, int64_t d, int64_t ldx, const float *weight, const float *bias,
                           float eps, const float *factors, uint8_t *codes, uint8_t *scales, int packed, float *y_debug,
                           float *mean, float *rstd, kq_stream_t stream) {
-    const RowShape s = row_shape(m, d, 2);
-    if (d > 16384 || !with_shape(s, [&](auto W, auto C) {
-            hipLaunchKernelGGL((kq::norm::quantize_kernel<T, W(), C()>), dim3(persistent_grid(m, s.waves, 16)),
-                               dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx,
-                               weight, bias, eps, factors, codes, scales, packed, y_debug, mean, rstd);
-        }))
+    auto go = [&](auto W, auto C) {
+        // with one wave per row the coefficients' setup weighs more: 8 waves per compute unit (12.5 us
+        // at 8192 x 1152, 15.1 with 16)
+        hipLaunchKernelGGL((kq::norm::quantize_kernel<T, W(), C()>), dim3(persistent_grid(m, W(), W() == 1 ? 8 : W() == 3 ? 12 : 16)),
+                           dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx, weight,
+                           bias, eps, factors, codes, scales, packed, y_debug, mean, rstd);
+    };
+    if (d > 16384 || !(m < kqhost::compute_units() ? first_shape(pieces_of(d), Few(), go)
+                                                   : first_shape(pieces_of(d), Many(), go)))
         hipLaunchKernelGGL((kq::norm::quantize_wide_kernel<T>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
                            (hipStream_t)stream, (const T *)X, m, d, ldx, weight, bias, eps, factors, codes, scales,
                            packed, y_debug, mean, rstd);
