@@ -145,9 +145,9 @@ def _torch():
 
 
 def _stream_ptr(stream):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return ctypes.c_void_p(_current_stream(_torch().cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _dev(t, name, dtypes):
@@ -777,65 +777,94 @@ def calib_step_noalloc(A, W, theta, adam_m, adam_v, t, lambdas, losses, grad=Non
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # kq_act
 
 
-def _elsewhere(t, stream):
-    """The context a call on ``t`` has to run in when it was given a stream or t's device is not
-    the current one (its allocations then belong to that stream too), else None."""
+def _activation(t, name):
+    """(bf16?, device index) of the bf16 or fp32 GPU tensor t."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if t.dtype is torch.bfloat16:
+        return True, t.get_device()
+    if t.dtype is torch.float32:
+        return False, t.get_device()
+    raise TypeError("%s has dtype %s, expected torch.bfloat16 or torch.float32" % (name, t.dtype))
+
+
+def _elsewhere(index, stream):
+    """The context a call on device ``index`` has to run in when it was given a stream or that is
+    not the current device (its allocations then belong to that stream too), else None."""
     torch = _torch()
     if stream is not None:
-        if stream.device != t.device:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
+        if stream.device.index != index:
+            raise ValueError("the stream is on %s, the tensors on device %d" % (stream.device, index))
         return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
+    if index != torch.cuda.current_device():
+        return torch.cuda.device(index)
     return None
 
 
-def _matrix(t, name, dtype, device, shape=None):
-    """t's row stride: t must be a [rows][columns] tensor of dtype on device with unit column
-    stride (of that shape). A single row's stride does not matter."""
-    if t.dtype != dtype:
+def _current_stream(index):
+    """The current stream of device ``index`` (the current device) as a number. torch.cuda's own
+    stream object costs 2.7 us to make, a third of a small call."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _matrix(t, name, dtype, index, rows=None, cols=None):
+    """t's row stride: t must be a [rows][cols] tensor of dtype on device ``index`` with unit column
+    stride. A single row's stride does not matter."""
+    if t.dtype is not dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape),
-                                                            "[rows][columns]" if shape is None else tuple(shape)))
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected device %d" % (name, t.device, index))
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and (shape[0] != rows or shape[1] != cols)):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(shape),
+                                                            "[rows][columns]" if rows is None else (rows, cols)))
+    stride = t.stride()
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError("%s must have unit column stride" % name)
-    return t.stride(0) if rows > 1 else cols
+    return stride[0] if shape[0] > 1 else shape[1]
 
 
-def _vector(t, name, d, device):
+def _vector(t, name, d, index):
     """Pointer of the fp32 vector t of length d (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != _torch().float32:
+    if t.dtype is not _torch().float32:
         raise TypeError("%s has dtype %s, expected torch.float32" % (name, t.dtype))
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected device %d" % (name, t.device, index))
     if t.numel() != d or not t.is_contiguous():
         raise ValueError("%s must be a contiguous fp32 vector of length %d" % (name, d))
     return t.data_ptr()
 
 
-def _packed_scales(t, name, rows, k, device, packed):
+def _bytes(t, name, rows, cols, index):
+    """Pointer of the contiguous uint8 tensor t of rows * cols bytes on device ``index``."""
     torch = _torch()
-    if t.dtype != torch.uint8 or t.device != device:
-        raise TypeError("%s must be a uint8 tensor on %s" % (name, device))
-    if not t.is_contiguous() or (t.numel() != rows * (k // 32) if packed else tuple(t.shape) != (rows, k // 32)):
-        raise ValueError("%s must be contiguous, %s" % (name, "rows * k/32 bytes" if packed else "[rows][k/32]"))
+    if t.dtype is not torch.uint8 or t.get_device() != index:
+        raise TypeError("%s must be a uint8 tensor on device %d" % (name, index))
+    if t.numel() != rows * cols or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with %d x %d bytes" % (name, rows, cols))
     return t.data_ptr()
 
 
-def _workspace(name, rows, cols, workspace, device):
-    """(tensor, its bytes) for a call that sums over rows: the caller's, or one of this call's own."""
+def _packed_scales(t, name, rows, k, index, packed):
+    if not packed and tuple(t.shape) != (rows, k // 32):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (rows, k // 32)))
+    return _bytes(t, name, rows, k // 32, index)
+
+
+def _workspace(name, rows, cols, workspace, like):
+    """(tensor, its bytes) for a call that sums over rows: the caller's, or one of this call's own on
+    the device of ``like``."""
     n = ctypes.c_int64(0)
     _check(name, getattr(lib(), name)(rows, cols, ctypes.byref(n)))
     if workspace is None:
-        workspace = _torch().empty(n.value, dtype=_torch().uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+        workspace = like.new_empty(n.value, dtype=_torch().uint8)
+    elif workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -846,28 +875,28 @@ def layernorm(x, weight=None, bias=None, eps=1e-5, out=None, stats=False, mean=N
     into) returns (y, mean, rstd), what layernorm_backward takes.
     """
     torch = _torch()
-    _dev(x, "x", (torch.bfloat16, torch.float32))
-    here = _elsewhere(x, stream)
+    bf16, index = _activation(x, "x")
+    here = _elsewhere(index, stream)
     if here is not None:
         with here:
             return layernorm(x, weight, bias, eps, out, stats, mean, rstd)
-    dtype, dev = x.dtype, x.device
-    ldx = _matrix(x, "x", dtype, dev)
+    ldx = _matrix(x, "x", x.dtype, index)
     m, d = x.shape
     if out is None:
-        out = torch.empty((m, d), dtype=dtype, device=dev)
-    ldy = _matrix(out, "out", dtype, dev, x.shape)
+        out, ldy = x.new_empty((m, d)), d
+    else:
+        ldy = _matrix(out, "out", x.dtype, index, m, d)
     stats = stats or mean is not None or rstd is not None
     if stats:
         if mean is None:
-            mean = torch.empty(m, dtype=torch.float32, device=dev)
+            mean = x.new_empty(m, dtype=torch.float32)
         if rstd is None:
-            rstd = torch.empty(m, dtype=torch.float32, device=dev)
+            rstd = x.new_empty(m, dtype=torch.float32)
     _check("kq_layernorm",
-           lib().kq_layernorm(x.data_ptr(), 1 if dtype == torch.bfloat16 else 0, m, d, ldx,
-                              _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), eps, out.data_ptr(),
-                              ldy, _vector(mean, "mean", m, dev), _vector(rstd, "rstd", m, dev),
-                              torch.cuda.current_stream().cuda_stream))
+           lib().kq_layernorm(x.data_ptr(), int(bf16), m, d, ldx, _vector(weight, "weight", d, index),
+                              _vector(bias, "bias", d, index), eps, out.data_ptr(), ldy,
+                              _vector(mean, "mean", m, index), _vector(rstd, "rstd", m, index),
+                              _current_stream(index)))
     return (out, mean, rstd) if stats else out
 
 
@@ -880,37 +909,37 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, db
     bytes, or None (allocated for this call).
     """
     torch = _torch()
-    _dev(x, "x", (torch.bfloat16, torch.float32))
-    _dev(dy, "dy", (x.dtype,))
-    here = _elsewhere(x, stream)
+    bf16, index = _activation(x, "x")
+    _activation(dy, "dy")
+    here = _elsewhere(index, stream)
     if here is not None:
         with here:
             return layernorm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, params, workspace)
-    dtype, dev = x.dtype, x.device
-    ldx = _matrix(x, "x", dtype, dev)
-    lddy = _matrix(dy, "dy", dtype, dev, x.shape)
+    ldx = _matrix(x, "x", x.dtype, index)
     m, d = x.shape
+    lddy = _matrix(dy, "dy", x.dtype, index, m, d)
     if dx is None:
-        dx = torch.empty((m, d), dtype=dtype, device=dev)
-    lddx = _matrix(dx, "dx", dtype, dev, x.shape)
+        dx, lddx = x.new_empty((m, d)), d
+    else:
+        lddx = _matrix(dx, "dx", x.dtype, index, m, d)
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward pass are required")
     ws, ws_bytes = None, 0
     if params:
         if dweight is None:
-            dweight = torch.empty(d, dtype=torch.float32, device=dev)
+            dweight = x.new_empty(d, dtype=torch.float32)
         if dbias is None:
-            dbias = torch.empty(d, dtype=torch.float32, device=dev)
-        ws, ws_bytes = _workspace("kq_layernorm_backward_workspace_bytes", m, d, workspace, dev)
+            dbias = x.new_empty(d, dtype=torch.float32)
+        ws, ws_bytes = _workspace("kq_layernorm_backward_workspace_bytes", m, d, workspace, x)
     elif dweight is not None or dbias is not None:
         raise ValueError("params=False computes neither dweight nor dbias")
     _check("kq_layernorm_backward",
-           lib().kq_layernorm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, 1 if dtype == torch.bfloat16 else 0,
-                                       m, d, _vector(weight, "weight", d, dev), _vector(mean, "mean", m, dev),
-                                       _vector(rstd, "rstd", m, dev), dx.data_ptr(), lddx,
-                                       _vector(dweight, "dweight", d, dev), _vector(dbias, "dbias", d, dev),
+           lib().kq_layernorm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, int(bf16), m, d,
+                                       _vector(weight, "weight", d, index), _vector(mean, "mean", m, index),
+                                       _vector(rstd, "rstd", m, index), dx.data_ptr(), lddx,
+                                       _vector(dweight, "dweight", d, index), _vector(dbias, "dbias", d, index),
                                        ws.data_ptr() if ws is not None else None, ws_bytes,
-                                       torch.cuda.current_stream().cuda_stream))
+                                       _current_stream(index)))
     return dx, dweight, dbias
 
 
@@ -924,40 +953,39 @@ def layernorm_quantize_mxfp4(x, weight=None, bias=None, factors=None, eps=1e-5, 
     ``stats=True`` (or mean, rstd given) returns (codes, scales, mean, rstd).
     """
     torch = _torch()
-    _dev(x, "x", (torch.bfloat16, torch.float32))
-    here = _elsewhere(x, stream)
+    bf16, index = _activation(x, "x")
+    here = _elsewhere(index, stream)
     if here is not None:
         with here:
             return layernorm_quantize_mxfp4(x, weight, bias, factors, eps, packed, codes, scales, y_debug, stats,
                                             mean, rstd)
-    dtype, dev = x.dtype, x.device
-    ldx = _matrix(x, "x", dtype, dev)
+    ldx = _matrix(x, "x", x.dtype, index)
     m, d = x.shape
     if codes is None:
-        codes = torch.empty((m, d // 2), dtype=torch.uint8, device=dev)
-    if codes.dtype != torch.uint8 or codes.device != dev or tuple(codes.shape) != (m, d // 2) or \
-            not codes.is_contiguous():
-        raise ValueError("codes must be a contiguous [m][d/2] uint8 tensor on %s" % dev)
+        codes = x.new_empty((m, d // 2), dtype=torch.uint8)
+    elif tuple(codes.shape) != (m, d // 2):
+        raise ValueError("codes has shape %s, expected %s" % (tuple(codes.shape), (m, d // 2)))
+    cp = _bytes(codes, "codes", m, d // 2, index)
     if scales is None:
-        scales = torch.empty((d // 256, m, 8) if packed and d % 256 == 0 else (m, d // 32), dtype=torch.uint8,
-                             device=dev)
-    sp = _packed_scales(scales, "scales", m, d, dev, packed)
+        scales = x.new_empty((d // 256, m, 8) if packed and d % 256 == 0 else (m, d // 32), dtype=torch.uint8)
+    sp = _packed_scales(scales, "scales", m, d, index, packed)
+    yp = None
     if y_debug is not None:
-        _dev(y_debug, "y_debug", (torch.float32,))
-        if y_debug.device != dev or tuple(y_debug.shape) != (m, d) or not y_debug.is_contiguous():
-            raise ValueError("y_debug must be a contiguous fp32 [m][d] tensor on %s" % dev)
+        if tuple(y_debug.shape) != (m, d):
+            raise ValueError("y_debug has shape %s, expected %s" % (tuple(y_debug.shape), (m, d)))
+        yp = _vector(y_debug, "y_debug", m * d, index)
     stats = stats or mean is not None or rstd is not None
     if stats:
         if mean is None:
-            mean = torch.empty(m, dtype=torch.float32, device=dev)
+            mean = x.new_empty(m, dtype=torch.float32)
         if rstd is None:
-            rstd = torch.empty(m, dtype=torch.float32, device=dev)
+            rstd = x.new_empty(m, dtype=torch.float32)
     _check("kq_layernorm_quantize_mxfp4",
-           lib().kq_layernorm_quantize_mxfp4(x.data_ptr(), 1 if dtype == torch.bfloat16 else 0, m, d, ldx,
-                                             _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), eps,
-                                             _vector(factors, "factors", (d // 32) * 20, dev), codes.data_ptr(), sp,
-                                             1 if packed else 0, _p(y_debug), _vector(mean, "mean", m, dev),
-                                             _vector(rstd, "rstd", m, dev), torch.cuda.current_stream().cuda_stream))
+           lib().kq_layernorm_quantize_mxfp4(x.data_ptr(), int(bf16), m, d, ldx, _vector(weight, "weight", d, index),
+                                             _vector(bias, "bias", d, index), eps,
+                                             _vector(factors, "factors", (d // 32) * 20, index), cp, sp,
+                                             1 if packed else 0, yp, _vector(mean, "mean", m, index),
+                                             _vector(rstd, "rstd", m, index), _current_stream(index)))
     return (codes, scales, mean, rstd) if stats else (codes, scales)
 
 
@@ -971,42 +999,44 @@ def mxfp4_linear(codes_a, scales_a, codes_w, scales_w, bias=None, act="none", re
     the activation, (out, pre), what mxfp4_linear_backward takes.
     """
     torch = _torch()
-    _dev(codes_a, "codes_a", (torch.uint8,))
-    here = _elsewhere(codes_a, stream)
+    if not isinstance(codes_a, torch.Tensor) or not codes_a.is_cuda or codes_a.dtype is not torch.uint8:
+        raise TypeError("codes_a must be a uint8 CUDA (HIP) tensor")
+    index = codes_a.get_device()
+    here = _elsewhere(index, stream)
     if here is not None:
         with here:
             return mxfp4_linear(codes_a, scales_a, codes_w, scales_w, bias, act, residual, out, pre, bf16, packed,
                                 want_pre)
-    dev = codes_a.device
     if act not in ACTS:
         raise ValueError("act must be one of %s" % ", ".join(ACTS))
-    if codes_w.dtype != torch.uint8 or codes_w.device != dev:
-        raise TypeError("codes_w must be a uint8 tensor on %s" % dev)
-    if codes_a.dim() != 2 or codes_w.dim() != 2 or codes_a.shape[1] != codes_w.shape[1] or \
-            not codes_a.is_contiguous() or not codes_w.is_contiguous():
-        raise ValueError("codes_a [m][k/2] and codes_w [n][k/2] must be contiguous")
-    m, kb = codes_a.shape
-    n, k = codes_w.shape[0], 2 * kb
-    sa = _packed_scales(scales_a, "scales_a", m, k, dev, packed)
-    sw = _packed_scales(scales_w, "scales_w", n, k, dev, packed)
+    sa, sw = codes_a.shape, codes_w.shape
+    if len(sa) != 2 or len(sw) != 2 or sa[1] != sw[1]:
+        raise ValueError("codes_a must be [m][k/2] and codes_w [n][k/2], got %s and %s" % (tuple(sa), tuple(sw)))
+    m, kb = sa
+    n, k = sw[0], 2 * kb
     dtype = torch.bfloat16 if bf16 else torch.float32
-    shape = (m, n)
+    rp = zp = None
     ldr = ldz = 0
     if residual is not None:
-        ldr = _matrix(residual, "residual", dtype, dev, shape)
+        ldr = _matrix(residual, "residual", dtype, index, m, n)
+        rp = residual.data_ptr()
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    ldo = _matrix(out, "out", dtype, dev, shape)
-    if pre is None and want_pre:
-        pre = torch.empty(shape, dtype=dtype, device=dev)
+        out, ldo = codes_a.new_empty((m, n), dtype=dtype), n
+    else:
+        ldo = _matrix(out, "out", dtype, index, m, n)
     if pre is not None:
-        ldz = _matrix(pre, "pre", dtype, dev, shape)
+        ldz = _matrix(pre, "pre", dtype, index, m, n)
+        zp = pre.data_ptr()
+    elif want_pre:
+        pre, ldz = codes_a.new_empty((m, n), dtype=dtype), n
+        zp = pre.data_ptr()
     _check("kq_mxfp4_linear",
-           lib().kq_mxfp4_linear(codes_a.data_ptr(), sa, codes_w.data_ptr(), sw, 1 if packed else 0, m, n, k,
-                                 _vector(bias, "bias", n, dev), ACTS[act], 1 if bf16 else 0,
-                                 None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldo,
-                                 None if pre is None else pre.data_ptr(), ldz,
-                                 torch.cuda.current_stream().cuda_stream))
+           lib().kq_mxfp4_linear(_bytes(codes_a, "codes_a", m, kb, index),
+                                 _packed_scales(scales_a, "scales_a", m, k, index, packed),
+                                 _bytes(codes_w, "codes_w", n, kb, index),
+                                 _packed_scales(scales_w, "scales_w", n, k, index, packed), 1 if packed else 0, m, n,
+                                 k, _vector(bias, "bias", n, index), ACTS[act], 1 if bf16 else 0, rp, ldr,
+                                 out.data_ptr(), ldo, zp, ldz, _current_stream(index)))
     return out if pre is None else (out, pre)
 
 
@@ -1018,32 +1048,32 @@ def mxfp4_linear_backward(dout, z=None, act="none", dz=None, dbias=None, workspa
     residual's gradient is dout; the operands' are dz deq(W) and dz^T deq(A).
     """
     torch = _torch()
-    _dev(dout, "dout", (torch.bfloat16, torch.float32))
-    here = _elsewhere(dout, stream)
+    bf16, index = _activation(dout, "dout")
+    here = _elsewhere(index, stream)
     if here is not None:
         with here:
             return mxfp4_linear_backward(dout, z, act, dz, dbias, workspace)
-    dtype, dev = dout.dtype, dout.device
+    dtype = dout.dtype
     if act not in ACTS:
         raise ValueError("act must be one of %s" % ", ".join(ACTS))
-    lddo = _matrix(dout, "dout", dtype, dev)
+    lddo = _matrix(dout, "dout", dtype, index)
     m, n = dout.shape
     ldz = 0
     if z is not None:
-        ldz = _matrix(z, "z", dtype, dev, dout.shape)
+        ldz = _matrix(z, "z", dtype, index, m, n)
     elif act != "none":
         raise ValueError("z is required with act %r" % act)
     if dz is None:
-        dz = torch.empty((m, n), dtype=dtype, device=dev)
-    lddz = _matrix(dz, "dz", dtype, dev, dout.shape)
+        dz, lddz = dout.new_empty((m, n)), n
+    else:
+        lddz = _matrix(dz, "dz", dtype, index, m, n)
     if dbias is None:
-        dbias = torch.empty(n, dtype=torch.float32, device=dev)
-    ws, ws_bytes = _workspace("kq_mxfp4_linear_backward_workspace_bytes", m, n, workspace, dev)
+        dbias = dout.new_empty(n, dtype=torch.float32)
+    ws, ws_bytes = _workspace("kq_mxfp4_linear_backward_workspace_bytes", m, n, workspace, dout)
     _check("kq_mxfp4_linear_backward",
-           lib().kq_mxfp4_linear_backward(dout.data_ptr(), lddo, None if z is None else z.data_ptr(), ldz,
-                                          1 if dtype == torch.bfloat16 else 0, m, n, ACTS[act], dz.data_ptr(), lddz,
-                                          _vector(dbias, "dbias", n, dev), ws.data_ptr(), ws_bytes,
-                                          torch.cuda.current_stream().cuda_stream))
+           lib().kq_mxfp4_linear_backward(dout.data_ptr(), lddo, None if z is None else z.data_ptr(), ldz, int(bf16),
+                                          m, n, ACTS[act], dz.data_ptr(), lddz, _vector(dbias, "dbias", n, index),
+                                          ws.data_ptr(), ws_bytes, _current_stream(index)))
     return dz, dbias
 
 
