@@ -23,23 +23,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void *p, int64_
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
 }
 
-// Eight neighbouring channels as they are loaded.
+// Eight neighbouring channels as they are loaded; NT: non-temporal (streamed_once below).
 template <class T>
 struct Chunk;
 template <>
 struct Chunk<uint16_t> {
     u32x4_t q;
+    template <bool NT = false>
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
-        q = __builtin_amdgcn_raw_buffer_load_b128(r, 2 * ch, 0, 0);
+        q = __builtin_amdgcn_raw_buffer_load_b128(r, 2 * ch, 0, NT ? 2 : 0);
     }
     __device__ __forceinline__ void widen(float x[8]) const { widen8(make_uint4(q[0], q[1], q[2], q[3]), x); }
 };
 template <>
 struct Chunk<float> {
     u32x4_t a, b;
+    template <bool NT = false>
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
-        a = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * ch, 0, 0);
-        b = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * ch + 16, 0, 0);
+        a = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * ch, 0, NT ? 2 : 0);
+        b = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * ch + 16, 0, NT ? 2 : 0);
     }
     __device__ __forceinline__ void widen(float x[8]) const {
 #pragma unroll
@@ -49,18 +51,27 @@ struct Chunk<float> {
         }
     }
 };
+template <bool NT = false>
 __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const uint16_t *) {
     __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
                                                    pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])},
-                                           r, 2 * ch, 0, 0);
+                                           r, 2 * ch, 0, NT ? 2 : 0);
 }
+template <bool NT = false>
 __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const float *) {
     __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{__float_as_uint(y[0]), __float_as_uint(y[1]),
                                                    __float_as_uint(y[2]), __float_as_uint(y[3])},
-                                           r, 4 * ch, 0, 0);
+                                           r, 4 * ch, 0, NT ? 2 : 0);
     __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{__float_as_uint(y[4]), __float_as_uint(y[5]),
                                                    __float_as_uint(y[6]), __float_as_uint(y[7])},
-                                           r, 4 * ch + 16, 0, 0);
+                                           r, 4 * ch + 16, 0, NT ? 2 : 0);
 }
+
+// Whether a call that moves `bytes` marks its accesses non-temporal: from half of the 256 MiB
+// Infinity Cache on. What it reads is then not there from before (us: norm 16384 x 8192 bf16
+// 92.6 -> 87.2, 8192 x 4608 30.5 -> 27.1; its gradients 16384 x 8192 152 -> 133 with the loads
+// marked, 138 with the stores too; linear's gradient 8192 x 16384 158 -> 131; below, input that the
+// cache holds is lost: norm 8192 x 1152 8.4 -> 9.9, 2048 x 4096 7.8 -> 8.7).
+inline bool streamed_once(int64_t bytes) { return bytes >= (int64_t)128 << 20; }
 
 }  // namespace kq

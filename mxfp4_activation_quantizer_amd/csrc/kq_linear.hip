@@ -438,15 +438,16 @@ __global__ __launch_bounds__(256) void backward_any_kernel(const T *__restrict__
 }
 
 // Backward of the epilogue, rows of whole 16-byte pieces: wave w of workgroup (x, p) takes 512
-// columns (8 per lane: 1 KB of a bf16 row) of the rows p + parts (4 j + w), U of them in
-// flight; the waves' column sums meet in LDS in wave order. Bound by HBM: two reads and a
-// write per element against about 25 vector operations of 39 T/s for gelu_tanh.
-template <class T>
+// columns (8 per lane: 1 KB of a bf16 row) of every fourth of the p-th `group_rows` rows, U of
+// them in flight; the waves' column sums meet in LDS in wave order. Bound by HBM: two reads and a
+// write per element against about 25 vector operations of 39 T/s for gelu_tanh (131 us without
+// an activation too at 8192 x 16384 bf16: 6.1 TB/s; with every parts-th row instead 140).
+template <class T, bool NT>
 __global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO, int64_t lddo,
                                                        const T *__restrict__ Z, int64_t ldz, int64_t m, int64_t n,
-                                                       int act, T *__restrict__ dZ, int64_t lddz, int parts,
+                                                       int act, T *__restrict__ dZ, int64_t lddz, int64_t group_rows,
                                                        float *__restrict__ part) {
-    constexpr int U = 4;
+    constexpr int U = 8;
     __shared__ float4 join[4][2][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t c0 = (int64_t)blockIdx.x * 512, left = n - c0 < 512 ? n - c0 : 512;
@@ -455,27 +456,27 @@ __global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO,
     const int p = (int)blockIdx.y;
     const bool reads_z = act != KQ_ACT_NONE;
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const int64_t step = 4 * (int64_t)parts;
-    for (int64_t i = p + (int64_t)parts * wave; i < m; i += U * step) {
+    const int64_t end = m - p * group_rows < group_rows ? m : (p + 1) * group_rows;
+    for (int64_t i = p * group_rows + wave; i < end; i += 4 * U) {
         Chunk<T> d[U], z[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t row = i + u * step;
-            const bool in = row < m;
-            d[u].load(row_rsrc(dO + (in ? row : i) * lddo + c0, in ? bytes : 0), ch);
-            if (reads_z) z[u].load(row_rsrc(Z + (in ? row : i) * ldz + c0, in ? bytes : 0), ch);
+            const int64_t row = i + 4 * u;
+            const bool in = row < end;
+            d[u].template load<NT>(row_rsrc(dO + (in ? row : i) * lddo + c0, in ? bytes : 0), ch);
+            if (reads_z) z[u].template load<NT>(row_rsrc(Z + (in ? row : i) * ldz + c0, in ? bytes : 0), ch);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t row = i + u * step;
-            if (row >= m) break;
+            const int64_t row = i + 4 * u;
+            if (row >= end) break;
             float v[8], x[8];
             d[u].widen(v);
             if (reads_z) {
                 z[u].widen(x);
                 activate_grad(v, x, act);
             }
-            if (dZ) store8(row_rsrc(dZ + row * lddz + c0, bytes), ch, v, dZ);
+            if (dZ) store8<NT>(row_rsrc(dZ + row * lddz + c0, bytes), ch, v, dZ);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] += v[e];
         }
@@ -517,21 +518,24 @@ using kqhost::sizes_fit;
 bool good_type(int type) { return type == KQ_F32 || type == KQ_BF16; }
 bool good_act(int act) { return act >= KQ_ACT_NONE && act <= KQ_ACT_GELU_TANH; }
 
-// Parts of the bias gradient's sum: those of m rows, at most as many as give 4096 workgroups of
-// 512 columns (more only make the partial sums larger: 512 parts of 16384 columns are 34 MB).
+// Parts of the bias gradient's sum: those of m rows, at most as many as give 8192 workgroups of
+// 512 columns.
 int64_t column_parts(int64_t m, int64_t n) {
-    const int64_t strips = (n + 511) / 512, most = 4096 / (strips < 64 ? strips : 64), p = kqhost::row_parts(m);
+    const int64_t strips = (n + 511) / 512, most = 8192 / (strips < 128 ? strips : 128), p = kqhost::row_parts(m);
     return p < most ? p : most;
 }
 
 template <class T>
 void launch_backward(const void *dO, int64_t lddo, const void *Z, int64_t ldz, int64_t m, int64_t n, int act, void *dZ,
                      int64_t lddz, int64_t parts, float *part, bool vec, kq_stream_t stream) {
-    const int64_t columns = vec ? 512 : 256;
+    const int64_t columns = vec ? 512 : 256, rows = (m + parts - 1) / parts;
     const dim3 grid((unsigned)((n + columns - 1) / columns), (unsigned)parts);
-    if (vec)
-        hipLaunchKernelGGL((kq::linear::backward_kernel<T>), grid, dim3(256), 0, (hipStream_t)stream, (const T *)dO,
-                           lddo, (const T *)Z, ldz, m, n, act, (T *)dZ, lddz, (int)parts, part);
+    if (vec && kq::streamed_once(3 * m * n * (int)sizeof(T)))
+        hipLaunchKernelGGL((kq::linear::backward_kernel<T, true>), grid, dim3(256), 0, (hipStream_t)stream,
+                           (const T *)dO, lddo, (const T *)Z, ldz, m, n, act, (T *)dZ, lddz, rows, part);
+    else if (vec)
+        hipLaunchKernelGGL((kq::linear::backward_kernel<T, false>), grid, dim3(256), 0, (hipStream_t)stream,
+                           (const T *)dO, lddo, (const T *)Z, ldz, m, n, act, (T *)dZ, lddz, rows, part);
     else
         hipLaunchKernelGGL((kq::linear::backward_any_kernel<T>), grid, dim3(256), 0, (hipStream_t)stream,
                            (const T *)dO, lddo, (const T *)Z, ldz, m, n, act, (T *)dZ, lddz, (int)parts, part);

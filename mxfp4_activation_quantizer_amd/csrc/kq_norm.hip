@@ -183,33 +183,39 @@ __global__ __launch_bounds__(kThreads) void backward_params_any_kernel(
     if (pb) pb[p * d + c] = sb;
 }
 
-// out[c] = sum over p of part[p][c]: 64 columns per workgroup, wave w adds the parts w,
-// w + 16, ... in turn, then the 16 sums in wave order; y = 0 for the first output, 1 for
-// the second.
-constexpr int kChains = 16;
-__global__ __launch_bounds__(64 * kChains) void reduce_parts_kernel(const float *__restrict__ part0,
-                                                                    const float *__restrict__ part1, int parts,
-                                                                    int64_t d, float *__restrict__ out0,
-                                                                    float *__restrict__ out1) {
-    __shared__ float red[kChains][64];
+// out[c] = sum over p of part[p][c]: 32 columns per workgroup (one cache line of a part), half
+// wave w adds the parts w, w + 32, ... in turn, then four of them the 32 sums in order and the
+// first those four; y = 0 for the first output, 1 for the second. Few columns make few
+// workgroups, so the parts are spread as wide as one has threads (256 parts of 2 x 1152
+// columns: 2.4 us).
+constexpr int kColumns = 32, kChains = 32;
+__global__ __launch_bounds__(kColumns *kChains) void reduce_parts_kernel(const float *__restrict__ part0,
+                                                                         const float *__restrict__ part1, int parts,
+                                                                         int64_t d, float *__restrict__ out0,
+                                                                         float *__restrict__ out1) {
+    __shared__ float red[kChains][kColumns + 1];
     const float *part = blockIdx.y ? part1 : part0;
     float *out = blockIdx.y ? out1 : out0;
     if (!out) return;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < d; c0 += (int64_t)gridDim.x * 64) {
-        const int64_t c = c0 + lane;
+    const int col = threadIdx.x % kColumns, w = threadIdx.x / kColumns;
+    for (int64_t c0 = (int64_t)blockIdx.x * kColumns; c0 < d; c0 += (int64_t)gridDim.x * kColumns) {
+        const int64_t c = c0 + col;
         float s = 0.f;
         if (c < d) {
 #pragma unroll 8
             for (int p = w; p < parts; p += kChains) s += part[p * d + c];
         }
-        red[w][lane] = s;
+        red[w][col] = s;
         __syncthreads();
-        if (w == 0 && c < d) {
+        if (w < 4) {
+            s = red[8 * w][col];
 #pragma unroll
-            for (int i = 1; i < kChains; ++i) s += red[i][lane];
-            out[c] = s;
+            for (int i = 1; i < 8; ++i) s += red[8 * w + i][col];
         }
+        __syncthreads();
+        if (w < 4) red[w][col] = s;
+        __syncthreads();
+        if (w == 0 && c < d) out[c] = (red[0][col] + red[1][col]) + (red[2][col] + red[3][col]);
         __syncthreads();
     }
 }
@@ -337,7 +343,7 @@ __device__ __forceinline__ Stats chunk_stats(const Chunk<T> (&raw)[C], bool last
     return st;
 }
 
-template <class T, int W, int C>
+template <class T, int W, int C, bool NT>
 __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__restrict__ X, int64_t m, int64_t d,
                                                                    int64_t ldx, const float *__restrict__ w,
                                                                    const float *__restrict__ b, float eps,
@@ -365,14 +371,14 @@ __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__re
     const int64_t bytes = d * (int)sizeof(T);
     Chunk<T> raw[C], next[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) next[c].load(row_rsrc(X + row * ldx, bytes), ch[c]);
+    for (int c = 0; c < C; ++c) next[c].template load<NT>(row_rsrc(X + row * ldx, bytes), ch[c]);
     for (; row < m; row += step) {
 #pragma unroll
         for (int c = 0; c < C; ++c) raw[c] = next[c];
         // past the last row: no records, so no access
         const auto ahead = row_rsrc(X + (row + step < m ? row + step : row) * ldx, row + step < m ? bytes : 0);
 #pragma unroll
-        for (int c = 0; c < C; ++c) next[c].load(ahead, ch[c]);
+        for (int c = 0; c < C; ++c) next[c].template load<NT>(ahead, ch[c]);
         const Stats st = chunk_stats<T, W, C>(raw, last, d, inv, eps, red_sum, red_sq, wr);
         const auto out = row_rsrc(Y + row * ldy, bytes);
 #pragma unroll
@@ -381,7 +387,7 @@ __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__re
             raw[c].widen(x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = fmaf(st.normed(x[e]), pw[c][e], pb[c][e]);
-            store8(out, ch[c], x, Y);
+            store8<NT>(out, ch[c], x, Y);
         }
         if (lane == 0 && wr == 0) {
             if (mean) mean[row] = st.c;
@@ -390,10 +396,12 @@ __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__re
     }
 }
 
-// Workgroup p of the backward pass walks the rows p, p + parts, ... (with W = 1, every fourth
-// of them per wave), writes their dx and keeps its lanes' columns of dweight and dbias in
+// Workgroup p of `parts` in the backward pass walks the p-th run of rows, or, where the rows
+// stream from memory (NT), the rows p, p + parts, ..., so that all workgroups together read one
+// stretch of it (16384 x 8192 bf16 152 us, 167 with runs; from the caches, runs are faster: 1024 x
+// 4096 12.4 us, 13.1 without). With W = 1, each wave takes every fourth of them. It writes their dx and keeps its lanes' columns of dweight and dbias in
 // registers; row p of the partial sums gets them at the end.
-template <class T, int W, int C>
+template <class T, int W, int C, bool NT>
 __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__restrict__ dY, int64_t lddy,
                                                                     const T *__restrict__ X, int64_t ldx, int64_t m,
                                                                     int64_t d, const float *__restrict__ w,
@@ -406,8 +414,10 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wr = W == 1 ? 0 : wave;
     constexpr int R = W == 1 ? 4 : 1;
-    const int64_t p = blockIdx.x, step = (int64_t)parts * R;
-    int64_t row = p + (W == 1 ? (int64_t)parts * wave : 0);
+    const int64_t p = blockIdx.x, run = (m + parts - 1) / parts;
+    const int64_t apart = NT ? parts : 1, step = R * apart;
+    const int64_t end = NT || m - p * run < run ? m : (p + 1) * run;
+    int64_t row = (NT ? p : p * run) + (W == 1 ? apart * wave : 0);
     uint32_t ch[C];
     float wv[C][8], aw[C][8], ab[C][8];
 #pragma unroll
@@ -422,19 +432,19 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
     Chunk<T> x[C], dy[C], nx[C], ndy[C];
     float mu = 0.f, rs = 0.f, nmu = 0.f, nrs = 0.f;
     auto fetch = [&](int64_t r) {
-        const bool in = r < m;
+        const bool in = r < end;
         const int64_t rr = in ? r : 0;
         const auto rx = row_rsrc(X + rr * ldx, in ? bytes : 0), rd = row_rsrc(dY + rr * lddy, in ? bytes : 0);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            nx[c].load(rx, ch[c]);
-            ndy[c].load(rd, ch[c]);
+            nx[c].template load<NT>(rx, ch[c]);
+            ndy[c].template load<NT>(rd, ch[c]);
         }
         nmu = mean[rr];
         nrs = rstd[rr];
     };
     fetch(row);
-    for (int par = 0; row < m; row += step, par ^= 1) {
+    for (int par = 0; row < end; row += step, par ^= 1) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             x[c] = nx[c];
@@ -684,13 +694,17 @@ unsigned persistent_grid(int64_t m, int waves, int per_cu) {
 template <class T>
 kq_status launch_forward(const void *X, int64_t m, int64_t d, int64_t ldx, const float *weight, const float *bias,
                          float eps, void *Y, int64_t ldy, float *mean, float *rstd, bool vec, kq_stream_t stream) {
-    auto go = [&](auto W, auto C) {
-        hipLaunchKernelGGL((kq::norm::forward_kernel<T, W(), C()>), dim3(persistent_grid(m, W(), W() == 3 ? 12 : 16)),
+    const bool few = m < kqhost::compute_units();
+    auto go = [&](auto W, auto C, auto NT) {
+        hipLaunchKernelGGL((kq::norm::forward_kernel<T, W(), C(), NT()>), dim3(persistent_grid(m, W(), W() == 3 ? 12 : 16)),
                            dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx, weight,
                            bias, eps, (T *)Y, ldy, mean, rstd);
     };
-    if (!vec || !(m < kqhost::compute_units() ? first_shape(pieces_of(d), Few(), go)
-                                              : first_shape(pieces_of(d), Many(), go)))
+    auto go_plain = [&](auto W, auto C) { go(W, C, std::false_type()); };
+    auto go_nt = [&](auto W, auto C) { go(W, C, std::true_type()); };
+    if (!vec || !(few ? first_shape(pieces_of(d), Few(), go_plain)
+                  : kq::streamed_once(2 * m * d * (int)sizeof(T)) ? first_shape(pieces_of(d), Many(), go_nt)
+                                                                  : first_shape(pieces_of(d), Many(), go_plain)))
         hipLaunchKernelGGL((kq::norm::forward_any_kernel<T>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
                            (hipStream_t)stream, (const T *)X, m, d, ldx, weight, bias, eps, (T *)Y, ldy, mean, rstd);
     return launched();
@@ -700,12 +714,16 @@ template <class T>
 kq_status launch_backward(const void *dY, int64_t lddy, const void *X, int64_t ldx, int64_t m, int64_t d,
                           const float *weight, const float *mean, const float *rstd, void *dX, int64_t lddx,
                           int64_t parts, float *pw, float *pb, bool params, bool vec, kq_stream_t stream) {
-    auto go = [&](auto W, auto C) {
-        hipLaunchKernelGGL((kq::norm::backward_kernel<T, W(), C()>), dim3((unsigned)parts),
+    auto go = [&](auto W, auto C, auto NT) {
+        hipLaunchKernelGGL((kq::norm::backward_kernel<T, W(), C(), NT()>), dim3((unsigned)parts),
                            dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)dY, lddy,
                            (const T *)X, ldx, m, d, weight, mean, rstd, (T *)dX, lddx, (int)parts, pw, pb);
     };
-    if (vec && first_shape(pieces_of(d), Backward(), go)) return launched();
+    auto go_plain = [&](auto W, auto C) { go(W, C, std::false_type()); };
+    auto go_nt = [&](auto W, auto C) { go(W, C, std::true_type()); };
+    if (vec && (kq::streamed_once(3 * m * d * (int)sizeof(T)) ? first_shape(pieces_of(d), Backward(), go_nt)
+                                                              : first_shape(pieces_of(d), Backward(), go_plain)))
+        return launched();
     hipLaunchKernelGGL((kq::norm::backward_dx_any_kernel<T>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
                        (hipStream_t)stream, (const T *)dY, lddy, (const T *)X, ldx, m, d, weight, mean, rstd, (T *)dX,
                        lddx);
@@ -741,9 +759,9 @@ namespace kqhost {
 
 kq_status reduce_parts(const float *part0, const float *part1, int64_t parts, int64_t d, float *out0, float *out1,
                        kq_stream_t stream) {
-    const int64_t groups = (d + 63) / 64;
+    const int64_t groups = (d + kq::norm::kColumns - 1) / kq::norm::kColumns;
     hipLaunchKernelGGL(kq::norm::reduce_parts_kernel, dim3((unsigned)(groups < 65536 ? groups : 65536), out1 ? 2 : 1),
-                       dim3(64 * kq::norm::kChains), 0, (hipStream_t)stream, part0, part1, (int)parts, d, out0, out1);
+                       dim3(kq::norm::kColumns * kq::norm::kChains), 0, (hipStream_t)stream, part0, part1, (int)parts, d, out0, out1);
     return launched();
 }
 
