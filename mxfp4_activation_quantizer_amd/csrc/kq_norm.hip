@@ -535,8 +535,10 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
 // Layer norm, transform and quantizer (vector path). A quad of lanes holds a 32-channel block and a wave's
 // chunk 16 of them (the segments of the fused transform kernels), for which every lane keeps
 // its block's 16 coefficients and its channels' parameters over all rows of the workgroup.
+// (bf16 with 3 chunks: held to the 168 registers of three waves per SIMD; at 170, two, 8192 x
+// 4608 takes 37 us instead of 28.5.)
 template <class T, int W, int C>
-__global__ __launch_bounds__(kGroupThreads<W>) void quantize_kernel(
+__global__ __launch_bounds__(kGroupThreads<W>, sizeof(T) == 2 && C == 3 ? 3 : 1) void quantize_kernel(
     const T *__restrict__ X, int64_t m, int64_t d, int64_t ldx, const float *__restrict__ w,
     const float *__restrict__ b, float eps, const float *__restrict__ factors, uint8_t *__restrict__ codes,
     uint8_t *__restrict__ scales, int packed, float *__restrict__ y_debug, float *__restrict__ mean,
@@ -739,9 +741,9 @@ kq_status launch_quantize(const void *X, int64_t m, int64_t d, int64_t ldx, cons
                           float eps, const float *factors, uint8_t *codes, uint8_t *scales, int packed, float *y_debug,
                           float *mean, float *rstd, kq_stream_t stream) {
     auto go = [&](auto W, auto C) {
-        // with one wave per row the coefficients' setup weighs more: 8 waves per compute unit (12.5 us
-        // at 8192 x 1152, 15.1 with 16)
-        hipLaunchKernelGGL((kq::norm::quantize_kernel<T, W(), C()>), dim3(persistent_grid(m, W(), W() == 1 ? 8 : W() == 3 ? 12 : 16)),
+        // one resident round; with one wave per row the coefficients' setup weighs more and 8 waves per
+        // compute unit are faster (8192 x 512 5.9 us, 6.0 with 16)
+        hipLaunchKernelGGL((kq::norm::quantize_kernel<T, W(), C()>), dim3(persistent_grid(m, W(), C() == 3 ? 12 : W() == 1 ? 8 : 16)),
                            dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx, weight,
                            bias, eps, factors, codes, scales, packed, y_debug, mean, rstd);
     };
