@@ -568,10 +568,11 @@ kq_status launch_tiles(const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, 
 }
 
 // Which kernel a product of m x n outputs over `stages` 256-k stages runs on: the least of
-// seven estimates, in us, fitted to 30 measured shapes from 1 x 1152 x 4608 to 8192 x 4096 x 1024
-// (most within 15%): a launch and what a stage takes while a compute unit has one tile, and
-// each further round of tiles. Up to 16 rows only the kernel that splits k is considered (1 x
-// 16384 x 8192 17.4 us, 20.9 with 64 x 64 tiles). Measured at k = 4096, in the order of the list:
+// seven estimates, in us, fitted to 427 measured products (m = 1 .. 8192, n = 512 .. 11008, k = 256
+// .. 8192; the choice is 1.8% slower than the fastest on average, 33% at worst): a launch, and per
+// round of tiles a tile's own time and that of its stages. Up to 16 rows only the kernel that
+// splits k is considered (1 x 16384 x 8192, W from HBM: 17.4 us, 20.9 with 64 x 64 tiles).
+// Measured at k = 4096, in the order of the list:
 //      8 x 4096   4.9   5.7
 //     64 x 4096  12.7   9.4   7.2   8.2  10.8
 //    128 x 4096  21.7  15.8  11.6   8.2  10.8  16.2  23.1
@@ -587,22 +588,22 @@ Kernel choose_kernel(int64_t m, int64_t n, int stages, bool packed, bool can256)
         return (double)((m + tm - 1) / tm) * (double)((n + tn - 1) / tn) / cus;
     };
     Kernel best = kProduct11;
-    double least = 2.0 + ceil(tiles(16, 16)) * 0.16 * st;
+    double least = 2.8 + ceil(tiles(16, 16)) * (0.148 * st + 0.14);
     auto consider = [&](Kernel k, double us) {
         if (us < least) best = k, least = us;
     };
-    consider(kProduct12, 2.0 + ceil(tiles(16, 32)) * 0.22 * st);
+    consider(kProduct12, 2.6 + ceil(tiles(16, 32)) * (0.21 * st + 0.13));
     if (m <= 16) return best;
-    consider(kProduct22, 2.3 + ceil(tiles(32, 32)) * 0.29 * st);
-    const double t64 = tiles(64, 64);
-    consider(kTile64Deep, 3.0 + ceil(t64) * 0.33 * st);
-    consider(kTile64, fmax(2.8 + 0.5 * st, 1.2 + t64 * (0.325 * st + 0.7)));
-    consider(kTile128, 3.0 + 0.15 * st + ceil(tiles(128, 128)) * (0.62 * st + 2.1));
+    consider(kProduct22, 2.6 + ceil(tiles(32, 32)) * (0.277 * st + 0.27));
+    consider(kTile64Deep, 2.5 + ceil(tiles(64, 64)) * (0.296 * st + 1.6));
+    // four at a time per compute unit, a stage's latency each while there are fewer
+    consider(kTile64, 2.8 + fmax(0.5 * st, 0.25 * st + tiles(64, 64) * (0.2 * st + 0.84)));
+    consider(kTile128, 2.9 + ceil(tiles(128, 128)) * (0.65 * st + 2.55));
     if (can256) {
         // whole rounds, and a last one of at most half the compute units in half tiles
-        const double full = 13.5 + (packed ? 1.8 : 2.05) * st, half = 7 + (packed ? 1.0 : 1.4) * st;
+        const double full = packed ? 14.2 + 1.52 * st : 13.6 + 1.83 * st, half = packed ? 6.8 + 0.88 * st : 6.4 + 1.15 * st;
         const double t256 = tiles(256, 256), rem = t256 - floor(t256);
-        consider(kTile256, floor(t256) * full + (rem == 0 ? 0 : rem <= 0.5 ? half : full));
+        consider(kTile256, 1.65 + floor(t256) * full + (rem == 0 ? 0 : rem <= 0.5 ? half : full));
     }
     return best;
 }

@@ -93,6 +93,42 @@ def test_many_rows(torch, kq, m, n, k, dt):
         check(torch, kq, m, n, k, ACTS[(m + k // 32) % 5], dt, packed, seed=m, pad=8 * packed)
 
 
+# one ragged product or more for every kernel the choice knows on 256 compute units (16 x 16, 16 x 32 and
+# 32 x 32 tiles with split k; 64 x 64 four and two stages deep, 128 x 128, 256 x 256 through LDS), each with a
+# k of whole stages (either layout), of a half stage and of single blocks as far as it takes them
+EVERY = [(250, 129, 4608), (20, 4095, 512), (64, 4001, 1184), (60, 3901, 2304), (100, 4100, 2080), (130, 4093, 4096),
+         (200, 4093, 1152), (600, 4099, 1024), (300, 3000, 96), (2050, 1154, 2304), (2050, 1155, 2336), (4100, 5000, 544),
+         (3000, 4000, 1920), (1500, 3333, 4096), (1500, 3336, 3968), (2048, 4096, 1152)]
+
+
+@pytest.mark.parametrize("m,n,k", EVERY)
+def test_every_kernel(torch, kq, m, n, k):
+    for i, packed in enumerate([False, True] if k % 256 == 0 else [False]):
+        dt = ("bfloat16", "float32")[(m + k // 32 + i) % 2]
+        check(torch, kq, m, n, k, ACTS[(n + i) % 5], dt, packed, seed=k, pad=(0, 8, 5)[m % 3])
+
+
+@pytest.mark.parametrize("m,n,k", [(9, 300, 512), (60, 3901, 2304), (600, 4099, 1024), (2050, 1154, 2304)])
+def test_scales_at_any_address(torch, kq, m, n, k):
+    """MX-layout scales need no alignment: at odd addresses, the same output (bytes 1 and 3 into a
+    buffer), whichever kernel runs."""
+    ca, sa = operand(torch, kq, m, k, 1)
+    cw, sw = operand(torch, kq, n, k, 2, k ** -0.5)
+    want = kq.mxfp4_linear(ca, sa, cw, sw, act="relu", bf16=False)
+
+    def moved(s, by):
+        buf = torch.empty(s.numel() + by, dtype=torch.uint8, device="cuda")
+        v = buf[by:].view(s.shape)
+        v.copy_(s)
+        return v
+
+    o, z, o_tol, z_tol = ref.linear(ca, sa, cw, sw, None, "relu", None)
+    for by_a, by_w in ((1, 3), (0, 1), (2, 0)):
+        got = kq.mxfp4_linear(ca, moved(sa, by_a), cw, moved(sw, by_w), act="relu", bf16=False)
+        ref.assert_near(got, o, o_tol)
+    ref.assert_near(want, o, o_tol)
+
+
 @pytest.mark.parametrize("name", ACTS)
 @pytest.mark.parametrize("dt", ["bfloat16", "float32"])
 def test_activations(torch, kq, name, dt):
