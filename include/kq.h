@@ -541,11 +541,11 @@ typedef enum {
  * all in fp32 (the squares are summed around the mean), y rounded once to its
  * type (nearest, ties to even).
  *   X, Y          device, `type` (a kq_type) [m][ldx] and [m][ldy], ldx, ldy >= d;
- *                 aligned to their elements. Both 16-byte aligned with rows of a
- *                 multiple of 16 bytes (and weight, bias 16-byte aligned) run
- *                 the vector path; d > 65536 bytes of a row and all other
- *                 layouts the general one. Elements past d of a row are neither
- *                 read nor written.
+ *                 aligned to their elements. With d % 8 == 0, d <= 16384, both 16-byte
+ *                 aligned with rows of a multiple of 16 bytes, and weight, bias
+ *                 16-byte aligned, rows are read once (the vector path); all
+ *                 other layouts take a slower general path. Elements past d of
+ *                 a row are neither read nor written.
  *   weight, bias  device, fp32 [d], or NULL (1 and 0)
  *   eps           >= 0 and finite (KQ_ERR_SHAPE)
  *   mean, rstd    device, fp32 [m], or NULL (not written); what
@@ -614,7 +614,8 @@ kq_status kq_layernorm_quantize_mxfp4(const void *X, int type, int64_t m, int64_
  *   bias                  device, fp32 [n], or NULL (0)
  *   act                   a kq_act value (any other: KQ_ERR_UNSUPPORTED)
  *   type                  type of residual, O and Z (a kq_type)
- *   residual              device, `type` [m][ldr], ldr >= n, or NULL (0); element aligned
+ *   residual              device, `type` [m][ldr], ldr >= n, or NULL (0); element aligned;
+ *                         may be O itself (with ldr == ldo): O = act(z) + O
  *   O                     device, `type` [m][ldo], ldo >= n; element aligned, written
  *   Z                     device, `type` [m][ldz], ldz >= n, or NULL: receives z (what
  *                         kq_mxfp4_linear_backward reads)

@@ -995,7 +995,7 @@ def mxfp4_linear(codes_a, scales_a, codes_w, scales_w, bias=None, act="none", re
 
     Operands as mxfp4_gemm (scales [rows][k/32]; any k % 32 == 0) or, with ``packed``, as
     mxfp4_gemm_packed (k % 256 == 0). bias: fp32 [n]; act: one of ACTS; residual, out, pre: [m][n]
-    of the output's type. ``want_pre=True`` (or pre given) also returns the values in front of
+    of the output's type (residual may be out itself). ``want_pre=True`` (or pre given) also returns the values in front of
     the activation, (out, pre), what mxfp4_linear_backward takes.
     """
     torch = _torch()

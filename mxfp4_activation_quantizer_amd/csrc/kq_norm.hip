@@ -669,6 +669,8 @@ bool first_shape(int64_t pieces, std::integer_sequence<int, W, C, Rest...>, F f)
     return true;
 }
 
+// In each list, an entry is reached only by rows of more than W (C - 1) pieces, so that no chunk but
+// the last has places past the row's end.
 // Many rows: few waves per row, so that a wave has work between its sums, with as few empty
 // places as the lists allow (us at 8192 x 1152: norm 8.5 with 1 x 3, 10.2 with 2 x 2, 11.0 with
 // 4 x 1; norm and quantizer 12.5, 14.6, 14.8).

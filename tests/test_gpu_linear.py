@@ -203,6 +203,50 @@ def test_backward(torch, kq, m, n, dt, name):
         assert torch.equal(alone[0], got[0]) and torch.equal(alone[1], got[1])
 
 
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_backward_streamed(torch, kq, dt):
+    """128 MiB and more (non-temporal accesses), an odd number of rows and of strips."""
+    dtype = getattr(torch, dt)
+    m, n = 8311, 2728
+    dout = torch.randn(m, n, generator=gen(torch, 1), device="cuda").to(dtype)
+    z = torch.randn(m, n, generator=gen(torch, 2), device="cuda").to(dtype)
+    got = kq.mxfp4_linear_backward(dout, z, act="gelu_tanh")
+    want, tol = ref.linear_grad(dout, z, "gelu_tanh")
+    for g, v, t in zip(got, want, tol):
+        ref.assert_near(g, v, t)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 512, 256), (64, 4001, 1184), (100, 4100, 2080), (2050, 1155, 2336), (1500, 3336, 3968)])
+def test_residual_in_place(torch, kq, m, n, k):
+    """O = act(z) + O on every family of kernels, aligned rows and ragged ones."""
+    ca, sa = operand(torch, kq, m, k, 1)
+    cw, sw = operand(torch, kq, n, k, 2, k ** -0.5)
+    for bf16 in (True, False):
+        x = torch.randn(m, n, generator=gen(torch, 4), device="cuda").to(torch.bfloat16 if bf16 else torch.float32)
+        want = kq.mxfp4_linear(ca, sa, cw, sw, act="silu", residual=x, bf16=bf16)
+        got = kq.mxfp4_linear(ca, sa, cw, sw, act="silu", residual=x, out=x, bf16=bf16)
+        assert got is x and torch.equal(x, want)
+
+
+def test_outputs_past_32_bits(torch, kq):
+    """Rows of the outputs, the residual and the gradients 2^20 elements apart: offsets past 2^31."""
+    ld, m, n, k = 1 << 20, 2300, 136, 256
+    buf = torch.empty(m * ld, dtype=torch.bfloat16, device="cuda").view(m, ld)
+    ca, sa = operand(torch, kq, m, k, 1)
+    cw, sw = operand(torch, kq, n, k, 2, k ** -0.5)
+    res, out, pre = buf[:, 0:n], buf[:, 4096:4096 + n], buf[:, 8192:8192 + n]
+    res.copy_(torch.randn(m, n, generator=gen(torch, 3), device="cuda"))
+    kq.mxfp4_linear(ca, sa, cw, sw, act="silu", residual=res, out=out, pre=pre)
+    o, z, o_tol, z_tol = ref.linear(ca, sa, cw, sw, None, "silu", res)
+    ref.assert_near(pre, z, z_tol, "z")
+    ref.assert_near(out, o, o_tol, "out")
+    for lo in (16384, 16385):  # the vector path and the general one
+        dz, dbias = kq.mxfp4_linear_backward(res, pre, act="silu", dz=buf[:, lo:lo + n])
+        want, tol = ref.linear_grad(res, pre, "silu")
+        ref.assert_near(dz, want[0], tol[0])
+        ref.assert_near(dbias, want[1], tol[1])
+
+
 @pytest.mark.parametrize("extra,offset", [(8, 0), (3, 0), (0, 1)])
 def test_backward_strides_and_alignment(torch, kq, extra, offset):
     m, n = 50, 712

@@ -111,6 +111,59 @@ def test_backward(torch, kq, m, d, dt):
     assert torch.equal(dx, got[0]) and none is None and nothing is None
 
 
+# widths for every number of waves and chunks that many rows take (whole rows and a partial last piece), and, at the
+# end, calls of 128 MiB and more, whose accesses are non-temporal
+MANY = [(260, 512), (300, 1000), (700, 1152), (260, 2048), (257, 2056), (512, 4096), (300, 4608), (290, 6144), (260, 8192),
+        (258, 12288), (256, 16384), (33000, 1032), (8300, 4104), (5000, 8200), (2100, 16384)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,d", MANY)
+def test_many_rows(torch, kq, m, d, dt):
+    dtype = getattr(torch, dt)
+    case("norm, norm_grad %dx%d %s" % (m, d, dt))
+    x = rand(torch, m, d, seed=m, scale=2.0, shift=0.5, dtype=dtype)
+    dy = rand(torch, m, d, seed=d, dtype=dtype)
+    w, b = rand(torch, d, seed=1, shift=1.0), rand(torch, d, seed=2)
+    y, mean, rstd = kq.layernorm(x, w, b, eps=EPS, stats=True)
+    y0, mu, rs, y_tol, mu_tol, rs_tol = ref.norm(x, w, b, EPS)
+    ref.assert_near(y, y0, y_tol, "y")
+    ref.assert_near(mean, mu, mu_tol, "mean")
+    ref.assert_near(rstd, rs, rs * rs_tol, "rstd")
+    del y, y0, y_tol
+    got = kq.layernorm_backward(dy, x, mean, rstd, w)
+    want, tol = ref.norm_grad(dy, x, mean, rstd, w)
+    for g, v, t, what in zip(got, want, tol, ("dx", "dw", "db")):
+        ref.assert_near(g, v, t, what)
+    again = kq.layernorm_backward(dy, x, mean, rstd, w)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_parameters_at_any_address(torch, kq):
+    """weight, bias and their gradients 4-byte aligned only: the same values by the general path; the
+    quantizing norm refuses them."""
+    m, d = 40, 1024
+    x = rand(torch, m, d, seed=1, dtype=torch.bfloat16)
+    dy = rand(torch, m, d, seed=2, dtype=torch.bfloat16)
+    buf = rand(torch, 4 * d + 8, seed=3, shift=1.0)
+    w, b = buf[1:1 + d], buf[d + 2:2 * d + 2]
+    y, mean, rstd = kq.layernorm(x, w, b, eps=EPS, stats=True)
+    y0, mu, rs, y_tol, _, _ = ref.norm(x, w, b, EPS)
+    ref.assert_near(y, y0, y_tol, "y")
+    keep = buf.clone()
+    dw, db = buf[2 * d + 3:3 * d + 3], buf[3 * d + 5:4 * d + 5]
+    for rows in (m, 3):
+        want, tol = ref.norm_grad(dy[:rows], x[:rows], mean[:rows], rstd[:rows], w)
+        got = kq.layernorm_backward(dy[:rows], x[:rows], mean[:rows], rstd[:rows], w, dweight=dw, dbias=db)
+        for g, v, t, what in zip(got, want, tol, ("dx", "dw", "db")):
+            ref.assert_near(g, v, t, what)
+    buf[2 * d + 3:3 * d + 3] = keep[2 * d + 3:3 * d + 3]
+    buf[3 * d + 5:4 * d + 5] = keep[3 * d + 5:4 * d + 5]
+    assert torch.equal(buf, keep)  # nothing beside them was written
+    with pytest.raises(kq.KQError):
+        kq.layernorm_quantize_mxfp4(x, w)
+
+
 def test_large_offset_and_equal_rows(torch, kq):
     """A mean far from zero cancels without loss; a row of equal values gives the bias (x - mean is
     0 up to 2 u of the first mean's rounding, times rstd = 1 / sqrt(eps))."""
@@ -176,7 +229,8 @@ def test_offsets_past_32_bits(torch, kq):
 
 # one block, widths that fill no wave, whole and partial segments of 512 channels, one to many waves
 QSHAPES = [(1, 32), (3, 96), (70, 160), (5, 512), (33, 544), (19, 1152), (1, 4096), (40, 4608), (6, 8224), (3, 16384),
-           (2, 32768)]
+           (2, 32768), (300, 512), (257, 1056), (600, 1152), (260, 2048), (300, 4096), (258, 4608), (260, 5120), (256, 8192),
+           (256, 12288), (257, 16384)]
 
 
 @pytest.mark.parametrize("dt", ["bfloat16", "float32"])
