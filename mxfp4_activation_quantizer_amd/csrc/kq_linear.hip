@@ -660,8 +660,11 @@ kq_status kq_mxfp4_linear(const uint8_t *codes_a, const uint8_t *scales_a, const
                              ((ldo | ldr | ldz) * es) % ep.align != 0))
         ep.align /= 2;
     const kq::linear::Geom g{(int)(k / 2), (int)(k / 32), (int)((k + 255) / 256), 0, 0};
-    const bool big = packed ? aligned(scales_a, 16) && aligned(scales_w, 16)
-                            : k % 128 == 0 && aligned(scales_a, 4) && aligned(scales_w, 4);
+    // without scales their layout does not matter, and the packed record counts (stages 8 m - 8 m0) would
+    // be below zero, so past every guard, for all tiles but the first
+    if (k == 0) packed = 0;
+    const bool big = k > 0 && (packed ? aligned(scales_a, 16) && aligned(scales_w, 16)
+                                      : k % 128 == 0 && aligned(scales_a, 4) && aligned(scales_w, 4));
     const Kernel kernel = choose_kernel(m, n, g.stages, packed != 0, big);
     if (kernel == kTile256)
         return kqhost::gemm256_linear(codes_a, scales_a, codes_w, scales_w, packed, k, type, ep, stream);

@@ -154,6 +154,19 @@ def test_no_inner_dimension_and_empty(torch, kq):
         assert kq.mxfp4_linear(ca, sa, cw, sw).shape == (m, n)
 
 
+@pytest.mark.parametrize("m,n", [(5, 40), (40, 72), (200, 4100), (1030, 4000)])
+def test_no_inner_dimension_packed(torch, kq, m, n):
+    """k = 0 is a multiple of 256 too: O = act(bias) + residual whatever the scales' layout, in every tile."""
+    case("k = 0 packed %dx%d" % (m, n))
+    none = lambda rows: torch.empty((rows, 0), dtype=torch.uint8, device="cuda")
+    b = torch.randn(n, generator=gen(torch, 1), device="cuda")
+    res = torch.randn(m, n, generator=gen(torch, 2), device="cuda")
+    args = (none(m), none(m), none(n), none(n))
+    out, pre = kq.mxfp4_linear(*args, bias=b, act="relu", residual=res, bf16=False, packed=True, want_pre=True)
+    assert torch.equal(pre, b.expand(m, n)) and torch.equal(out, b.clamp(min=0) + res)
+    assert torch.equal(out, kq.mxfp4_linear(*args, bias=b, act="relu", residual=res, bf16=False))
+
+
 def test_matches_plain_product(torch, kq):
     """Without bias, activation and residual: the product's own fp32 sums, rounded once for bf16."""
     ca, sa = operand(torch, kq, 1024, 768, 1)
