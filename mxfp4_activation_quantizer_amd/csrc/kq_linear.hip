@@ -315,9 +315,11 @@ __global__ __launch_bounds__(320) void tile_kernel(const uint8_t *__restrict__ c
         const int r0 = 8 * (kLoads * w + j), row = (r0 < TM ? r0 : r0 - TM) + (lane >> 3);
         voff[j] = (uint32_t)(row * g.kbytes) + 16u * (uint32_t)chunk[j & 1];
     }
-    auto issue = [&](int s, int slot) {  // past k (whole stages too): past the record count, zeros
-        const int kb = 128 * s;
-        const bool in[2] = {kb + 16 * chunk[0] < g.kbytes, kb + 16 * chunk[1] < g.kbytes};
+    // Past k (whole stages too): past the record count, zeros. The count is compared with the scalar
+    // offset taken off it, so that must not exceed it: 0 for the stages past the last.
+    auto issue = [&](int s, int slot) {
+        const bool in[2] = {128 * s + 16 * chunk[0] < g.kbytes, 128 * s + 16 * chunk[1] < g.kbytes};
+        const int kb = s < g.stages ? 128 * s : 0;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int r0 = 8 * (kLoads * w + j);

@@ -108,6 +108,13 @@ def test_every_kernel(torch, kq, m, n, k):
         check(torch, kq, m, n, k, ACTS[(n + i) % 5], dt, packed, seed=k, pad=(0, 8, 5)[m % 3])
 
 
+# last tiles of one row and one column, whose code buffers are shorter than the stages that are loaded ahead
+@pytest.mark.parametrize("m,n,k", [(65, 4033, 32), (65, 4033, 256), (129, 4033, 1056), (257, 4033, 288), (1537, 2561, 96),
+                                   (1537, 2561, 1280)])
+def test_one_row_in_the_last_tile(torch, kq, m, n, k):
+    check(torch, kq, m, n, k, "silu", "bfloat16", False, seed=m)
+
+
 @pytest.mark.parametrize("m,n,k", [(9, 300, 512), (60, 3901, 2304), (600, 4099, 1024), (2050, 1154, 2304)])
 def test_scales_at_any_address(torch, kq, m, n, k):
     """MX-layout scales need no alignment: at odd addresses, the same output (bytes 1 and 3 into a
