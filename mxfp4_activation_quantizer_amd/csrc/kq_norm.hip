@@ -92,8 +92,8 @@ struct Stats {
         off = (float)(mean - c);
     }
     __device__ __forceinline__ void set_rstd(float squares, double inv, float eps) {  // sum (x - c)^2
-        const float var = fmaxf(fmaf(squares, (float)inv, -off * off), 0.f);
-        rstd = __builtin_amdgcn_rsqf(var + eps);  // 1 ulp
+        const float var = fmaf(squares, (float)inv, -off * off);
+        rstd = __builtin_amdgcn_rsqf((var < 0.f ? 0.f : var) + eps);  // 1 ulp; NaN stays NaN
         shift = -off * rstd;
     }
 };

@@ -194,6 +194,20 @@ def test_nan_and_infinity_stay_in_their_rows(torch, kq):
         assert torch.equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("d", [40, 1030, 4096])
+def test_statistics_of_rows_with_nan_and_infinity(torch, kq, d):
+    """rstd is NaN too, so that the gradients of such a row are NaN and do not pass for numbers."""
+    x = rand(torch, 8, d, seed=d)
+    x[1, 3], x[4, d - 1], x[6, 0] = float("nan"), float("inf"), float("-inf")
+    y, mean, rstd = kq.layernorm(x, eps=EPS, stats=True)
+    bad = torch.zeros(8, dtype=torch.bool, device="cuda")
+    bad[[1, 4, 6]] = True
+    assert torch.equal(rstd.isnan(), bad) and torch.equal(mean.isfinite(), ~bad)
+    assert torch.equal(y.isnan().all(1), bad) and torch.equal(y.isnan().any(1), bad)
+    dx, _, _ = kq.layernorm_backward(rand(torch, 8, d, seed=2), x, mean, rstd)
+    assert torch.equal(dx.isnan().all(1), bad) and torch.equal(dx.isnan().any(1), bad)
+
+
 def test_no_rows(torch, kq):
     x = torch.empty(0, 48, device="cuda")
     w = torch.ones(48, device="cuda")
