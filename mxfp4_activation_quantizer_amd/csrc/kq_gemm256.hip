@@ -189,10 +189,11 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     auto issue_code = [&](int s, int i) {
         const uint32_t st = lds0 + (uint32_t)((s & 1) * kStage);
         const uint32_t kb = 128u * (uint32_t)s;
-        uint32_t off = i < 8 ? cvoff[i & 7] : cvoffw[(i - 8) & (LW - 1)];
-        if (kTail) off = 128 * s + 16 * tail_chunk[i & 1] < g.kbytes ? off : 0x80000000u;
-        if (i < 8) dma16(dca, st + (64 * w + 8 * i) * 128, off, kb);
-        else dma16(dcw, st + L::kOffW + ((TN / 4) * w + 8 * (i - 8)) * 128, off, kb);
+        auto in = [&](uint32_t off) {
+            return !kTail || 128 * s + 16 * tail_chunk[i & 1] < g.kbytes ? off : 0x80000000u;
+        };
+        if (i < 8) dma16(dca, st + (64 * w + 8 * i) * 128, in(cvoff[i]), kb);
+        else dma16(dcw, st + L::kOffW + ((TN / 4) * w + 8 * (i - 8)) * 128, in(cvoffw[i - 8]), kb);
     };
     // scales of stage s, 1 KB per load: A rows 128 (w & 1) .. by waves 0 and 1, W rows
     // 128 (w & 1) .. by waves 2 and 3 (TN = 256) or all TN rows by wave 2 (TN = 128;
