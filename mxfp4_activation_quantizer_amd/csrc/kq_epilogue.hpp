@@ -120,24 +120,36 @@ __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep,
         float bias[EC];
         load_bias(ep, j, bias);
         for (int i = 0; i < N; i += U) {
-            float add[U][EC];
+            // rows past the last take row 0's residual and are not stored
+            auto row_of = [&](int u) { return kRows * (i + u) + r0; };
+            float add[U][EC], v[U * EC];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int row = kRows * (i + u) + r0;
-                load_residual<T>(ep, i0 + (row < rows ? row : 0), j, add[u]);
-            }
+            for (int u = 0; u < U; ++u)
+                load_residual<T>(ep, i0 + (row_of(u) < rows ? row_of(u) : 0), j, add[u]);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int row = kRows * (i + u) + r0;
-                float v[EC];
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int e4 = 0; e4 < EC / 4; ++e4) {
-                    const floatx4_t f = *reinterpret_cast<const floatx4_t *>(at(row, (EC / 4) * c + e4));
+                    const floatx4_t f = *reinterpret_cast<const floatx4_t *>(at(row_of(u), (EC / 4) * c + e4));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[4 * e4 + e] = f[e] + bias[4 * e4 + e];
+                    for (int e = 0; e < 4; ++e) v[EC * u + 4 * e4 + e] = f[e] + bias[4 * e4 + e];
                 }
-                if (row < rows) finish<T>(v, add[u], ep, i0 + row, j);
+            auto store = [&](void *to, int64_t ld) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float x[EC];
+#pragma unroll
+                    for (int e = 0; e < EC; ++e) x[e] = v[EC * u + e];
+                    if (row_of(u) < rows) store_piece(static_cast<T *>(to) + (i0 + row_of(u)) * ld + j, x);
+                }
+            };
+            if (ep.Z) store(ep.Z, ep.ldz);
+            activate(v, ep.act);
+            if (ep.residual) {
+#pragma unroll
+                for (int e = 0; e < U * EC; ++e) v[e] += add[e / EC][e % EC];
             }
+            store(ep.O, ep.ldo);
         }
         return;
     }
