@@ -102,30 +102,71 @@ __device__ __forceinline__ void finish1(float z, float add, const Epi &ep, int64
     store1(static_cast<T *>(ep.O) + i * ep.ldo + j, ep.residual ? v[0] + add : v[0]);
 }
 
+// How a wave takes a staged block of ROWS x COLS sums where a lane moves whole 16-byte pieces of
+// O's rows: lane l has columns EC (l % kLanes) .. of the rows l / kLanes + kRows i, i < N, U of
+// them at a time.
+template <class T, int ROWS, int COLS>
+struct Staged {
+    static constexpr int EC = 16 / (int)sizeof(T), kLanes = COLS / EC, kRows = 64 / kLanes, N = ROWS / kRows;
+    static constexpr int U = N < 4 ? N : N < 16 ? 4 : 8;
+};
+
+// The residual's pieces of the rows i .. i + U - 1 of that block, as they are in memory; rows past
+// the last take row 0's, and without a residual nothing is read.
+template <class T, int ROWS, int COLS>
+struct Residual {
+    typedef Staged<T, ROWS, COLS> S;
+    u32x4_t q[S::U];
+    __device__ __forceinline__ void load(const Epi &ep, int64_t i0, int rows, int64_t j0, int i) {
+        if (!ep.residual || ep.align < 16 || j0 + COLS > ep.n || rows <= 0 || i >= S::N) return;
+        const int lane = threadIdx.x & 63, r0 = lane / S::kLanes;
+        const int64_t j = j0 + S::EC * (lane % S::kLanes);
+#pragma unroll
+        for (int u = 0; u < S::U; ++u) {
+            const int row = S::kRows * (i + u) + r0;
+            q[u] = *reinterpret_cast<const u32x4_t *>(static_cast<const T *>(ep.residual) +
+                                                      (i0 + (row < rows ? row : 0)) * ep.ldr + j);
+        }
+    }
+    __device__ __forceinline__ void add_to(float (&v)[S::U * S::EC]) const {
+#pragma unroll
+        for (int u = 0; u < S::U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (sizeof(T) == 2) {
+                    v[S::EC * u + 2 * e] += bf16_lo(q[u][e]);
+                    v[S::EC * u + 2 * e + 1] += bf16_hi(q[u][e]);
+                } else {
+                    v[S::EC * u + e] += __uint_as_float(q[u][e]);
+                }
+            }
+    }
+};
+
 // Rows [0, ROWS) x columns [0, COLS) of a wave's fp32 sums, staged in LDS at reg in rows of COLS
 // with 16-byte chunk c at c ^ (row % (COLS / 4)), to O's rows i0 .. (those < rows) and columns
 // j0 ..: a lane takes 16 bytes of a row of O, or, where those are not aligned or not all inside
-// n, the wave takes a row's elements side by side.
+// n, the wave takes a row's elements side by side. `first` holds the first rows' residual
+// (asked for before the sums were staged); each next batch's is in flight while one is finished.
 template <class T, int ROWS, int COLS>
-__device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep, int64_t i0, int rows, int64_t j0) {
+__device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep, int64_t i0, int rows, int64_t j0,
+                                              const Residual<T, ROWS, COLS> &first) {
     constexpr int CH = COLS / 4;
     const int lane = threadIdx.x & 63;
     auto at = [&](int row, int chunk) { return reg + row * (COLS * 4) + 16 * (chunk ^ (row & (CH - 1))); };
     if (rows <= 0) return;
     if (ep.align >= 16 && j0 + COLS <= ep.n) {
-        constexpr int EC = 16 / (int)sizeof(T), kLanes = COLS / EC, kRows = 64 / kLanes, N = ROWS / kRows;
-        constexpr int U = N < 4 ? N : 4;
-        const int c = lane % kLanes, r0 = lane / kLanes;
+        typedef Staged<T, ROWS, COLS> S;
+        constexpr int EC = S::EC, U = S::U;
+        const int c = lane % S::kLanes, r0 = lane / S::kLanes;
         const int64_t j = j0 + EC * c;
         float bias[EC];
         load_bias(ep, j, bias);
-        for (int i = 0; i < N; i += U) {
-            // rows past the last take row 0's residual and are not stored
-            auto row_of = [&](int u) { return kRows * (i + u) + r0; };
-            float add[U][EC], v[U * EC];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                load_residual<T>(ep, i0 + (row_of(u) < rows ? row_of(u) : 0), j, add[u]);
+        Residual<T, ROWS, COLS> now = first, next;
+        for (int i = 0; i < S::N; i += U) {
+            auto row_of = [&](int u) { return S::kRows * (i + u) + r0; };
+            next.load(ep, i0, rows, j0, i + U);
+            float v[U * EC];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -145,11 +186,9 @@ __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep,
             };
             if (ep.Z) store(ep.Z, ep.ldz);
             activate(v, ep.act);
-            if (ep.residual) {
-#pragma unroll
-                for (int e = 0; e < U * EC; ++e) v[e] += add[e / EC][e % EC];
-            }
+            if (ep.residual) now.add_to(v);
             store(ep.O, ep.ldo);
+            now = next;
         }
         return;
     }

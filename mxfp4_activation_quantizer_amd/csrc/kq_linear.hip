@@ -387,11 +387,13 @@ __global__ __launch_bounds__(320) void tile_kernel(const uint8_t *__restrict__ c
         }
     }
 
+    constexpr int WM = TM / 2, WN = TN / 2, CH = WN / 4;
+    Residual<T, WM, WN> add;
+    add.load(ep, m0 + wm, rows_a - wm, n0 + wn, 0);
     // every load into LDS has landed (the ones past k too) and every wave is done with the stages
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     // Each wave stages its block in fp32 in its own region, rows of 32 FB columns with 16-byte chunk c
     // at c ^ (row % CH), and reads it back row by row.
-    constexpr int WM = TM / 2, WN = TN / 2, CH = WN / 4;
     uint8_t *reg = smem + w * (WM * WN * 4);
 #pragma unroll
     for (int a = 0; a < FA; ++a)
@@ -404,7 +406,7 @@ __global__ __launch_bounds__(320) void tile_kernel(const uint8_t *__restrict__ c
                     floatx4_t{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
             }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    finish_staged<T, WM, WN>(reg, ep, m0 + wm, rows_a - wm, n0 + wn);
+    finish_staged<T, WM, WN>(reg, ep, m0 + wm, rows_a - wm, n0 + wn, add);
 }
 
 // Backward of the epilogue, any layout: workgroup (x, p) takes 256 columns of the rows
