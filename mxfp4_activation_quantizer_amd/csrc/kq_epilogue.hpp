@@ -21,6 +21,9 @@ struct Epi {
     int64_t m, n, ldr, ldo, ldz;
     int act;
     int align;  // every row of O, Z and the residual starts at a multiple of this many bytes (16, 8 or less)
+    // whether the residual is read non-temporally: from 256 MiB on, where the Infinity Cache cannot
+    // have it (us, fp32 8192 x 16384 x 4096: 410, 480 without; 8192 x 4096 x 4096: 105, 92 without)
+    int stream;
 };
 
 // N neighbouring elements in one piece. Non-temporal stores: outputs are not read again
@@ -111,21 +114,33 @@ struct Staged {
     static constexpr int U = N < 4 ? N : N < 16 ? 4 : 8;
 };
 
-// The residual's pieces of the rows i .. i + U - 1 of that block, as they are in memory; rows past
-// the last take row 0's, and without a residual nothing is read.
+// Buffer over `cols` columns from j0 on of the rows i0 .. i0 + rows - 1: loads of the rows behind
+// them read zeros and stores are dropped (a row's pitch is no less than its columns).
+template <class T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rsrc(const void *p, int64_t ld, int64_t i0, int rows,
+                                                             int64_t j0, int cols) {
+    return row_rsrc(static_cast<const T *>(p) + i0 * ld + j0, ((rows - 1) * ld + cols) * (int)sizeof(T));
+}
+
+// The residual's pieces of the rows i .. i + U - 1 of that block, as they are in memory.
 template <class T, int ROWS, int COLS>
 struct Residual {
     typedef Staged<T, ROWS, COLS> S;
     u32x4_t q[S::U];
     __device__ __forceinline__ void load(const Epi &ep, int64_t i0, int rows, int64_t j0, int i) {
         if (!ep.residual || ep.align < 16 || j0 + COLS > ep.n || rows <= 0 || i >= S::N) return;
-        const int lane = threadIdx.x & 63, r0 = lane / S::kLanes;
-        const int64_t j = j0 + S::EC * (lane % S::kLanes);
+        const auto rs = block_rsrc<T>(ep.residual, ep.ldr, i0, rows, j0, COLS);
+        const int lane = threadIdx.x & 63;
+        const uint32_t pitch = (uint32_t)ep.ldr * (uint32_t)sizeof(T);
+        const uint32_t at = (uint32_t)(lane / S::kLanes) * pitch + 16u * (uint32_t)(lane % S::kLanes);
+        if (ep.stream) {
 #pragma unroll
-        for (int u = 0; u < S::U; ++u) {
-            const int row = S::kRows * (i + u) + r0;
-            q[u] = *reinterpret_cast<const u32x4_t *>(static_cast<const T *>(ep.residual) +
-                                                      (i0 + (row < rows ? row : 0)) * ep.ldr + j);
+            for (int u = 0; u < S::U; ++u)
+                q[u] = __builtin_amdgcn_raw_buffer_load_b128(rs, at + (uint32_t)(S::kRows * (i + u)) * pitch, 0, 2);
+        } else {
+#pragma unroll
+            for (int u = 0; u < S::U; ++u)
+                q[u] = __builtin_amdgcn_raw_buffer_load_b128(rs, at + (uint32_t)(S::kRows * (i + u)) * pitch, 0, 0);
         }
     }
     __device__ __forceinline__ void add_to(float (&v)[S::U * S::EC]) const {
@@ -143,73 +158,116 @@ struct Residual {
     }
 };
 
+__device__ __forceinline__ u32x4_t piece_of(const float *v, const uint16_t *) {
+    return u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+__device__ __forceinline__ u32x4_t piece_of(const float *v, const float *) {
+    return u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+}
+__device__ __forceinline__ float buffer_load1(__amdgpu_buffer_rsrc_t r, uint32_t at, const uint16_t *) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0) << 16);
+}
+__device__ __forceinline__ float buffer_load1(__amdgpu_buffer_rsrc_t r, uint32_t at, const float *) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+}
+__device__ __forceinline__ void buffer_store1(__amdgpu_buffer_rsrc_t r, uint32_t at, float v, const uint16_t *) {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), r, at, 0, 0);
+}
+__device__ __forceinline__ void buffer_store1(__amdgpu_buffer_rsrc_t r, uint32_t at, float v, const float *) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at, 0, 0);
+}
+
 // Rows [0, ROWS) x columns [0, COLS) of a wave's fp32 sums, staged in LDS at reg in rows of COLS
 // with 16-byte chunk c at c ^ (row % (COLS / 4)), to O's rows i0 .. (those < rows) and columns
 // j0 ..: a lane takes 16 bytes of a row of O, or, where those are not aligned or not all inside
 // n, the wave takes a row's elements side by side. `first` holds the first rows' residual
 // (asked for before the sums were staged); each next batch's is in flight while one is finished.
+//
+// In batches, since a large tile has one wave per SIMD and nothing else to hide a row's latency:
+// with every row's bias, z, activation and residual on its own, 8192 x 16384 x 4096 took 427 us
+// instead of 346 (fp32, gelu) and 470 instead of 323 (bf16, residual), 4096 x 4001 x 2048 with a
+// residual 137 instead of 64.
 template <class T, int ROWS, int COLS>
 __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep, int64_t i0, int rows, int64_t j0,
                                               const Residual<T, ROWS, COLS> &first) {
     constexpr int CH = COLS / 4;
     const int lane = threadIdx.x & 63;
     auto at = [&](int row, int chunk) { return reg + row * (COLS * 4) + 16 * (chunk ^ (row & (CH - 1))); };
-    if (rows <= 0) return;
-    if (ep.align >= 16 && j0 + COLS <= ep.n) {
+    if (rows <= 0 || j0 >= ep.n) return;
+    const T *type = nullptr;
+    const int cols = (int)(ep.n - j0 < COLS ? ep.n - j0 : COLS);
+    const auto ro = block_rsrc<T>(ep.O, ep.ldo, i0, rows, j0, cols);
+    const auto rz = block_rsrc<T>(ep.Z, ep.ldz, i0, rows, j0, cols);
+    const uint32_t po = (uint32_t)ep.ldo * (uint32_t)sizeof(T), pz = (uint32_t)ep.ldz * (uint32_t)sizeof(T);
+    if (ep.align >= 16 && cols == COLS) {
         typedef Staged<T, ROWS, COLS> S;
         constexpr int EC = S::EC, U = S::U;
         const int c = lane % S::kLanes, r0 = lane / S::kLanes;
-        const int64_t j = j0 + EC * c;
         float bias[EC];
-        load_bias(ep, j, bias);
+        load_bias(ep, j0 + EC * c, bias);
         Residual<T, ROWS, COLS> now = first, next;
         for (int i = 0; i < S::N; i += U) {
-            auto row_of = [&](int u) { return S::kRows * (i + u) + r0; };
             next.load(ep, i0, rows, j0, i + U);
             float v[U * EC];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int e4 = 0; e4 < EC / 4; ++e4) {
-                    const floatx4_t f = *reinterpret_cast<const floatx4_t *>(at(row_of(u), (EC / 4) * c + e4));
+                    const floatx4_t f =
+                        *reinterpret_cast<const floatx4_t *>(at(S::kRows * (i + u) + r0, (EC / 4) * c + e4));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[EC * u + 4 * e4 + e] = f[e] + bias[4 * e4 + e];
                 }
-            auto store = [&](void *to, int64_t ld) {
+            // non-temporal: not read again here, so they should not push the operands' lines
+            auto store = [&](__amdgpu_buffer_rsrc_t r, uint32_t pitch) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float x[EC];
-#pragma unroll
-                    for (int e = 0; e < EC; ++e) x[e] = v[EC * u + e];
-                    if (row_of(u) < rows) store_piece(static_cast<T *>(to) + (i0 + row_of(u)) * ld + j, x);
-                }
+                for (int u = 0; u < U; ++u)
+                    __builtin_amdgcn_raw_buffer_store_b128(piece_of(v + EC * u, type), r,
+                                                           (uint32_t)(S::kRows * (i + u) + r0) * pitch + 16u * c, 0, 2);
             };
-            if (ep.Z) store(ep.Z, ep.ldz);
+            if (ep.Z) store(rz, pz);
             activate(v, ep.act);
             if (ep.residual) now.add_to(v);
-            store(ep.O, ep.ldo);
+            store(ro, po);
             now = next;
         }
         return;
     }
-    constexpr int kRows = 64 / COLS, N = ROWS / kRows, U = 8;  // kRows rows side by side
+    // kRows rows side by side, U such at a time, the next ones' residual in flight
+    constexpr int kRows = 64 / COLS, N = ROWS / kRows, U = 16;
+    static_assert(N % U == 0, "whole batches");
     const int c = lane % COLS, r0 = lane / COLS;
-    const int64_t j = j0 + c;
-    if (j >= ep.n) return;
-    const float bias = ep.bias ? ep.bias[j] : 0.f;
+    if (c >= cols) return;
+    const float bias = ep.bias ? ep.bias[j0 + c] : 0.f;
+    const auto ra = block_rsrc<T>(ep.residual, ep.ldr, i0, rows, j0, cols);
+    const uint32_t pa = (uint32_t)ep.ldr * (uint32_t)sizeof(T), along = (uint32_t)sizeof(T) * c;
+    float now[U], next[U];
+    auto fetch = [&](int i) {
+        if (!ep.residual || i >= N) return;
+#pragma unroll
+        for (int u = 0; u < U; ++u) next[u] = buffer_load1(ra, (uint32_t)(kRows * (i + u) + r0) * pa + along, type);
+    };
+    fetch(0);
     for (int i = 0; i < N; i += U) {
-        float add[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int row = kRows * (i + u) + r0;
-            add[u] = load_residual1<T>(ep, i0 + (row < rows ? row : 0), j);
-        }
+        for (int u = 0; u < U; ++u) now[u] = next[u];
+        fetch(i + U);
+        float v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int row = kRows * (i + u) + r0;
-            const float z = *reinterpret_cast<const float *>(at(row, c >> 2) + 4 * (c & 3)) + bias;
-            if (row < rows) finish1<T>(z, add[u], ep, i0 + row, j);
+        for (int u = 0; u < U; ++u)
+            v[u] = *reinterpret_cast<const float *>(at(kRows * (i + u) + r0, c >> 2) + 4 * (c & 3)) + bias;
+        auto store = [&](__amdgpu_buffer_rsrc_t r, uint32_t pitch) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                buffer_store1(r, (uint32_t)(kRows * (i + u) + r0) * pitch + along, v[u], type);
+        };
+        if (ep.Z) store(rz, pz);
+        activate(v, ep.act);
+        if (ep.residual) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] += now[u];
         }
+        store(ro, po);
     }
 }
 

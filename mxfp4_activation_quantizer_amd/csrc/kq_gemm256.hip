@@ -563,11 +563,10 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
         // Always staged in fp32, 64 columns a pass: bias, activation and residual are applied where
         // whole 128-byte (bf16) or 256-byte (fp32) runs of a row leave.
         typedef typename std::conditional<B16, uint16_t, float>::type T;
-        Residual<T, 128, 64> add, ahead;
-        add.load(ep, m0 + wm, rows_a - wm, n0 + wn, 0);
 #pragma unroll
         for (int pass = 0; pass < NB / 2; ++pass) {
-            if (pass + 1 < NB / 2) ahead.load(ep, m0 + wm, rows_a - wm, n0 + wn + 64 * (pass + 1), 0);
+            Residual<T, 128, 64> add;
+            add.load(ep, m0 + wm, rows_a - wm, n0 + wn + 64 * pass, 0);
 #pragma unroll
             for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -579,8 +578,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
                             acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
                     }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            finish_staged<T, 128, 64>(reg, ep, m0 + wm, rows_a - wm, n0 + wn + 64 * pass, add);
-            add = ahead;
+            finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn + 64 * pass, add);
         }
         return;
     }

@@ -191,7 +191,7 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
 // Why: the 256 x 256 kernel takes as long for one tile as for one on every compute unit
 // (22 us at k = 4096), so products of fewer tiles than that are faster in smaller ones.
 template <class T, int FA, int FB, int N>
-__global__ __launch_bounds__(320) void tile_kernel(const uint8_t *__restrict__ ca, const uint8_t *__restrict__ sa,
+__global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict__ ca, const uint8_t *__restrict__ sa,
                                                    const uint8_t *__restrict__ cw, const uint8_t *__restrict__ sw,
                                                    int packed, Geom g, Epi ep) {
     constexpr int TM = 64 * FA, TN = 64 * FB, kRowsAll = TM + TN;
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(320) void tile_kernel(const uint8_t *__restrict__ c
                     floatx4_t{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
             }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    finish_staged<T, WM, WN>(reg, ep, m0 + wm, rows_a - wm, n0 + wn, add);
+    finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn, add);
 }
 
 // Backward of the epilogue, any layout: workgroup (x, p) takes 256 columns of the rows
@@ -659,7 +659,7 @@ kq_status kq_mxfp4_linear(const uint8_t *codes_a, const uint8_t *scales_a, const
     if (256 * (k / 2) >= lim || m * (k / 32) >= lim || n * (k / 32) >= lim || (255 * ldo + n) * es >= lim ||
         (255 * ldr + n) * es >= lim || (255 * ldz + n) * es >= lim)
         return KQ_ERR_UNSUPPORTED;
-    kq::Epi ep{bias, residual, O, Z, m, n, ldr, ldo, ldz, act, 16};
+    kq::Epi ep{bias, residual, O, Z, m, n, ldr, ldo, ldz, act, 16, m * n * es >= (int64_t)256 << 20};
     while (ep.align > es && (!aligned(O, ep.align) || !aligned(residual, ep.align) || !aligned(Z, ep.align) ||
                              ((ldo | ldr | ldz) * es) % ep.align != 0))
         ep.align /= 2;
