@@ -23,11 +23,41 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void *p, int64_
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
 }
 
-// Eight neighbouring channels as they are loaded; NT: non-temporal (streamed_once below).
-template <class T>
+// One element through a buffer.
+template <bool NT = false>
+__device__ __forceinline__ uint32_t load_raw1(__amdgpu_buffer_rsrc_t r, uint32_t i, const uint16_t *) {
+    return __builtin_amdgcn_raw_buffer_load_b16(r, 2 * i, 0, NT ? 2 : 0);
+}
+template <bool NT = false>
+__device__ __forceinline__ uint32_t load_raw1(__amdgpu_buffer_rsrc_t r, uint32_t i, const float *) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, 4 * i, 0, NT ? 2 : 0);
+}
+template <bool NT = false>
+__device__ __forceinline__ void store1(__amdgpu_buffer_rsrc_t r, uint32_t i, float v, const uint16_t *) {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), r, 2 * i, 0, NT ? 2 : 0);
+}
+template <bool NT = false>
+__device__ __forceinline__ void store1(__amdgpu_buffer_rsrc_t r, uint32_t i, float v, const float *) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, 4 * i, 0, NT ? 2 : 0);
+}
+
+// How a wave's lanes share the 512 channels of a piece. VEC: lane l has the 8 neighbours from
+// 8 l on, in one or two 16-byte accesses (rows of whole 16-byte pieces). Otherwise lane l has
+// the channels l, 64 + l, 128 + l .., element by element, at any width and alignment; an access
+// of the wave is one run of a row either way.
+template <bool VEC>
+struct Lanes {
+    static constexpr uint32_t kStep = VEC ? 1 : 64;  // from a lane's element to its next
+    static __device__ __forceinline__ uint32_t first(uint32_t piece, int lane) {
+        return 512u * piece + (VEC ? 8u : 1u) * (uint32_t)lane;
+    }
+};
+
+// A lane's eight channels as they are loaded; NT: non-temporal (streamed_once below).
+template <class T, bool VEC = true>
 struct Chunk;
 template <>
-struct Chunk<uint16_t> {
+struct Chunk<uint16_t, true> {
     u32x4_t q;
     template <bool NT = false>
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
@@ -36,7 +66,7 @@ struct Chunk<uint16_t> {
     __device__ __forceinline__ void widen(float x[8]) const { widen8(make_uint4(q[0], q[1], q[2], q[3]), x); }
 };
 template <>
-struct Chunk<float> {
+struct Chunk<float, true> {
     u32x4_t a, b;
     template <bool NT = false>
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
@@ -51,14 +81,37 @@ struct Chunk<float> {
         }
     }
 };
-template <bool NT = false>
-__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const uint16_t *) {
+template <class T>
+struct Chunk<T, false> {
+    uint32_t q[8];
+    template <bool NT = false>
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t ch) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = load_raw1<NT>(r, ch + 64 * e, (const T *)nullptr);
+    }
+    __device__ __forceinline__ void widen(float x[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(sizeof(T) == 2 ? q[e] << 16 : q[e]);
+    }
+};
+template <bool NT = false, bool VEC = true>
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const uint16_t *type) {
+    if (!VEC) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) store1<NT>(r, ch + 64 * e, y[e], type);
+        return;
+    }
     __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
                                                    pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])},
                                            r, 2 * ch, 0, NT ? 2 : 0);
 }
-template <bool NT = false>
-__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const float *) {
+template <bool NT = false, bool VEC = true>
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t ch, const float y[8], const float *type) {
+    if (!VEC) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) store1<NT>(r, ch + 64 * e, y[e], type);
+        return;
+    }
     __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{__float_as_uint(y[0]), __float_as_uint(y[1]),
                                                    __float_as_uint(y[2]), __float_as_uint(y[3])},
                                            r, 4 * ch, 0, NT ? 2 : 0);

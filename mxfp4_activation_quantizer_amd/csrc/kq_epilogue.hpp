@@ -164,19 +164,6 @@ __device__ __forceinline__ u32x4_t piece_of(const float *v, const uint16_t *) {
 __device__ __forceinline__ u32x4_t piece_of(const float *v, const float *) {
     return u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
 }
-__device__ __forceinline__ float buffer_load1(__amdgpu_buffer_rsrc_t r, uint32_t at, const uint16_t *) {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0) << 16);
-}
-__device__ __forceinline__ float buffer_load1(__amdgpu_buffer_rsrc_t r, uint32_t at, const float *) {
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
-}
-__device__ __forceinline__ void buffer_store1(__amdgpu_buffer_rsrc_t r, uint32_t at, float v, const uint16_t *) {
-    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), r, at, 0, 0);
-}
-__device__ __forceinline__ void buffer_store1(__amdgpu_buffer_rsrc_t r, uint32_t at, float v, const float *) {
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at, 0, 0);
-}
-
 // Rows [0, ROWS) x columns [0, COLS) of a wave's fp32 sums, staged in LDS at reg in rows of COLS
 // with 16-byte chunk c at c ^ (row % (COLS / 4)), to O's rows i0 .. (those < rows) and columns
 // j0 ..: a lane takes 16 bytes of a row of O, or, where those are not aligned or not all inside
@@ -240,12 +227,11 @@ __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep,
     if (c >= cols) return;
     const float bias = ep.bias ? ep.bias[j0 + c] : 0.f;
     const auto ra = block_rsrc<T>(ep.residual, ep.ldr, i0, rows, j0, cols);
-    const uint32_t pa = (uint32_t)ep.ldr * (uint32_t)sizeof(T), along = (uint32_t)sizeof(T) * c;
-    float now[U], next[U];
+    uint32_t now[U], next[U];
     auto fetch = [&](int i) {
         if (!ep.residual || i >= N) return;
 #pragma unroll
-        for (int u = 0; u < U; ++u) next[u] = buffer_load1(ra, (uint32_t)(kRows * (i + u) + r0) * pa + along, type);
+        for (int u = 0; u < U; ++u) next[u] = load_raw1(ra, (uint32_t)(kRows * (i + u) + r0) * (uint32_t)ep.ldr + c, type);
     };
     fetch(0);
     for (int i = 0; i < N; i += U) {
@@ -256,18 +242,17 @@ __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep,
 #pragma unroll
         for (int u = 0; u < U; ++u)
             v[u] = *reinterpret_cast<const float *>(at(kRows * (i + u) + r0, c >> 2) + 4 * (c & 3)) + bias;
-        auto store = [&](__amdgpu_buffer_rsrc_t r, uint32_t pitch) {
+        auto store = [&](__amdgpu_buffer_rsrc_t r, uint32_t ld) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                buffer_store1(r, (uint32_t)(kRows * (i + u) + r0) * pitch + along, v[u], type);
+            for (int u = 0; u < U; ++u) store1(r, (uint32_t)(kRows * (i + u) + r0) * ld + c, v[u], type);
         };
-        if (ep.Z) store(rz, pz);
+        if (ep.Z) store(rz, (uint32_t)ep.ldz);
         activate(v, ep.act);
         if (ep.residual) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] += now[u];
+            for (int u = 0; u < U; ++u) v[u] += __uint_as_float(sizeof(T) == 2 ? now[u] << 16 : now[u]);
         }
-        store(ro, po);
+        store(ro, (uint32_t)ep.ldo);
     }
 }
 

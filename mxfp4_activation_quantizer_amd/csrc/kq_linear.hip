@@ -409,44 +409,12 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
     finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn, add);
 }
 
-// Backward of the epilogue, any layout: workgroup (x, p) takes 256 columns of the rows
-// p, p + parts, ..., four of them at a time.
-template <class T>
-__global__ __launch_bounds__(256) void backward_any_kernel(const T *__restrict__ dO, int64_t lddo,
-                                                           const T *__restrict__ Z, int64_t ldz, int64_t m, int64_t n,
-                                                           int act, T *__restrict__ dZ, int64_t lddz, int parts,
-                                                           float *__restrict__ part) {
-    constexpr int U = 4;
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= n) return;
-    const int p = (int)blockIdx.y;
-    float s = 0.f;
-    for (int64_t i = p; i < m; i += (int64_t)U * parts) {
-        float d[U], z[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = i + (int64_t)u * parts;
-            d[u] = row < m ? load1(dO + row * lddo + c) : 0.f;
-            z[u] = act != KQ_ACT_NONE && row < m ? load1(Z + row * ldz + c) : 0.f;
-        }
-        activate_grad(d, z, act);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = i + (int64_t)u * parts;
-            if (row >= m) break;
-            if (dZ) store1(dZ + row * lddz + c, d[u]);
-            s += d[u];
-        }
-    }
-    if (part) part[p * n + c] = s;
-}
-
-// Backward of the epilogue, rows of whole 16-byte pieces: wave w of workgroup (x, p) takes 512
+// Backward of the epilogue: wave w of workgroup (x, p) takes 512
 // columns (8 per lane: 1 KB of a bf16 row) of every fourth of the p-th `group_rows` rows, U of
 // them in flight; the waves' column sums meet in LDS in wave order. Bound by HBM: two reads and a
 // write per element against about 25 vector operations of 39 T/s for gelu_tanh (131 us without
 // an activation too at 8192 x 16384 bf16: 6.1 TB/s; with every parts-th row instead 140).
-template <class T, bool NT>
+template <class T, bool NT, bool VEC>
 __global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO, int64_t lddo,
                                                        const T *__restrict__ Z, int64_t ldz, int64_t m, int64_t n,
                                                        int act, T *__restrict__ dZ, int64_t lddz, int64_t group_rows,
@@ -456,13 +424,13 @@ __global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO,
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t c0 = (int64_t)blockIdx.x * 512, left = n - c0 < 512 ? n - c0 : 512;
     const int64_t bytes = left * (int)sizeof(T);
-    const uint32_t ch = 8u * lane;
+    const uint32_t ch = Lanes<VEC>::first(0, lane);
     const int p = (int)blockIdx.y;
     const bool reads_z = act != KQ_ACT_NONE;
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const int64_t end = m - p * group_rows < group_rows ? m : (p + 1) * group_rows;
     for (int64_t i = p * group_rows + wave; i < end; i += 4 * U) {
-        Chunk<T> d[U], z[U];
+        Chunk<T, VEC> d[U], z[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t row = i + 4 * u;
@@ -480,7 +448,7 @@ __global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO,
                 z[u].widen(x);
                 activate_grad(v, x, act);
             }
-            if (dZ) store8<NT>(row_rsrc(dZ + row * lddz + c0, bytes), ch, v, dZ);
+            if (dZ) store8<NT, VEC>(row_rsrc(dZ + row * lddz + c0, bytes), ch, v, dZ);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] += v[e];
         }
@@ -496,8 +464,15 @@ __global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO,
             const float4 o = join[w][wave][lane];
             a.x += o.x; a.y += o.y; a.z += o.z; a.w += o.w;
         }
-        const int64_t c = c0 + ch + 4 * wave;
-        if (c < n) *reinterpret_cast<float4 *>(part + p * n + c) = a;
+        const int64_t c = c0 + ch + 4 * wave * Lanes<VEC>::kStep;
+        if (VEC) {
+            if (c < n) *reinterpret_cast<float4 *>(part + p * n + c) = a;
+        } else {
+            const float one[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + 64 * e < n) part[p * n + c + 64 * e] = one[e];
+        }
     }
 }
 
@@ -532,17 +507,17 @@ int64_t column_parts(int64_t m, int64_t n) {
 template <class T>
 void launch_backward(const void *dO, int64_t lddo, const void *Z, int64_t ldz, int64_t m, int64_t n, int act, void *dZ,
                      int64_t lddz, int64_t parts, float *part, bool vec, kq_stream_t stream) {
-    const int64_t columns = vec ? 512 : 256, rows = (m + parts - 1) / parts;
-    const dim3 grid((unsigned)((n + columns - 1) / columns), (unsigned)parts);
-    if (vec && kq::streamed_once(3 * m * n * (int)sizeof(T)))
-        hipLaunchKernelGGL((kq::linear::backward_kernel<T, true>), grid, dim3(256), 0, (hipStream_t)stream,
+    const int64_t rows = (m + parts - 1) / parts;
+    const dim3 grid((unsigned)((n + 511) / 512), (unsigned)parts);
+    auto go = [&](auto NT, auto VEC) {
+        hipLaunchKernelGGL((kq::linear::backward_kernel<T, NT(), VEC()>), grid, dim3(256), 0, (hipStream_t)stream,
                            (const T *)dO, lddo, (const T *)Z, ldz, m, n, act, (T *)dZ, lddz, rows, part);
-    else if (vec)
-        hipLaunchKernelGGL((kq::linear::backward_kernel<T, false>), grid, dim3(256), 0, (hipStream_t)stream,
-                           (const T *)dO, lddo, (const T *)Z, ldz, m, n, act, (T *)dZ, lddz, rows, part);
-    else
-        hipLaunchKernelGGL((kq::linear::backward_any_kernel<T>), grid, dim3(256), 0, (hipStream_t)stream,
-                           (const T *)dO, lddo, (const T *)Z, ldz, m, n, act, (T *)dZ, lddz, (int)parts, part);
+    };
+    const bool nt = kq::streamed_once(3 * m * n * (int)sizeof(T));
+    if (vec && nt) go(std::true_type(), std::true_type());
+    else if (vec) go(std::false_type(), std::true_type());
+    else if (nt) go(std::true_type(), std::false_type());
+    else go(std::false_type(), std::false_type());
 }
 
 // The launch's work-items are counted in 32 bits.

@@ -115,7 +115,7 @@ __device__ __forceinline__ Stats row_stats(const T *x, int64_t d, float eps) {
     return st;
 }
 
-// General forward: any width, stride and alignment; one workgroup per row.
+// Forward of rows wider than registers hold; one workgroup per row.
 template <class T>
 __global__ __launch_bounds__(kThreads) void forward_any_kernel(const T *__restrict__ X, int64_t m, int64_t d,
                                                                int64_t ldx, const float *__restrict__ w,
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void forward_any_kernel(const T *__restri
     }
 }
 
-// General backward, dx: one workgroup per row.
+// Backward of such rows, dx: one workgroup per row.
 template <class T>
 __global__ __launch_bounds__(kThreads) void backward_dx_any_kernel(const T *__restrict__ dY, int64_t lddy,
                                                                    const T *__restrict__ X, int64_t ldx, int64_t m,
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void backward_dx_any_kernel(const T *__re
     }
 }
 
-// General backward, the parameters' gradients: workgroup (x, p) sums 256 columns over
+// Backward of such rows, the parameters' gradients: workgroup (x, p) sums 256 columns over
 // the rows p, p + parts, ... into row p of the partial sums.
 template <class T>
 __global__ __launch_bounds__(kThreads) void backward_params_any_kernel(
@@ -269,22 +269,28 @@ __global__ __launch_bounds__(kThreads) void quantize_wide_kernel(const T *__rest
 }
 
 // ---------------------------------------------------------------------------
-// Vector path: rows of whole 16-byte pieces, up to 16384 channels, held in
-// registers from one read. A row belongs to W waves; lane l of wave w holds the
-// C chunks of 8 channels at 8 (64 (W c + w) + l), c < C, so every access of a
-// wave is one contiguous run (1 KB of bf16). Only chunk C - 1 can lie past the
-// row's end: it reads zeros and its stores are dropped (record counts of the
-// row's bytes), and its centred values are left out of the sum of squares.
+// Rows of up to 16384 channels, held in registers from one read. A row belongs
+// to W waves; wave w holds the C pieces of 512 channels W c + w, c < C, 8 of them
+// in each lane (Lanes: neighbours in rows of whole 16-byte pieces, every 64th
+// otherwise), so every access of a wave is one contiguous run. Only piece C - 1
+// can lie past the row's end, whole or in part: there it reads zeros and its
+// stores are dropped (record counts of the row's bytes), and its centred values
+// are left out of the sum of squares.
 // Rows are walked by a persistent grid, so the parameters (fp32, four times the
 // bytes of a bf16 row) are loaded once per workgroup, and the next row's loads
 // are in flight while a row is summed. With W = 1 a workgroup's 4 waves walk
 // rows of their own and there is no barrier in the loop.
 // ---------------------------------------------------------------------------
 // Parameters of a lane's chunk (fp32; `none` where there are none or past d).
+template <bool VEC = true>
 __device__ __forceinline__ void load_params(const float *p, int64_t ch, int64_t d, float none, float v[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = none;
-    if (p && ch < d) {
+    if (!VEC) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (p && ch + 64 * e < d) v[e] = p[ch + 64 * e];
+    } else if (p && ch < d) {
         const float4 a = *reinterpret_cast<const float4 *>(p + ch), b = *reinterpret_cast<const float4 *>(p + ch + 4);
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -308,9 +314,9 @@ __device__ __forceinline__ V row_sum(V v, V *red, int wave) {
 template <int W>
 constexpr int kGroupThreads = W == 1 ? 256 : 64 * W;
 
-// A row's statistics from its chunks.
-template <class T, int W, int C>
-__device__ __forceinline__ Stats chunk_stats(const Chunk<T> (&raw)[C], bool last, int64_t d, double inv, float eps,
+// A row's statistics from its chunks; `ch`: the last chunk's first channel.
+template <int W, class T, bool VEC, int C>
+__device__ __forceinline__ Stats chunk_stats(const Chunk<T, VEC> (&raw)[C], uint32_t ch, int64_t d, double inv, float eps,
                                              double *red_sum, float *red_sq, int wave) {
     double s = 0.0;
 #pragma unroll
@@ -334,16 +340,16 @@ __device__ __forceinline__ Stats chunk_stats(const Chunk<T> (&raw)[C], bool last
         raw[c].widen(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float v = x[e] - st.c;
+            const float v = VEC || c < C - 1 || ch + 64 * e < d ? x[e] - st.c : 0.f;
             qc = fmaf(v, v, qc);
         }
-        q += c < C - 1 || last ? qc : 0.f;
+        q += !VEC || c < C - 1 || ch < d ? qc : 0.f;
     }
     st.set_rstd(row_sum<W>(q, red_sq, wave), inv, eps);
     return st;
 }
 
-template <class T, int W, int C, bool NT>
+template <class T, int W, int C, bool NT, bool VEC>
 __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__restrict__ X, int64_t m, int64_t d,
                                                                    int64_t ldx, const float *__restrict__ w,
                                                                    const float *__restrict__ b, float eps,
@@ -362,14 +368,13 @@ __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__re
     float pw[C][8], pb[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        ch[c] = 8u * (64u * (W * c + wr) + lane);
-        load_params(w, ch[c], d, 1.0f, pw[c]);
-        load_params(b, ch[c], d, 0.0f, pb[c]);
+        ch[c] = Lanes<VEC>::first(W * c + wr, lane);
+        load_params<VEC>(w, ch[c], d, 1.0f, pw[c]);
+        load_params<VEC>(b, ch[c], d, 0.0f, pb[c]);
     }
-    const bool last = ch[C - 1] < d;
     const double inv = 1.0 / (double)d;
     const int64_t bytes = d * (int)sizeof(T);
-    Chunk<T> raw[C], next[C];
+    Chunk<T, VEC> raw[C], next[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) next[c].template load<NT>(row_rsrc(X + row * ldx, bytes), ch[c]);
     for (; row < m; row += step) {
@@ -379,7 +384,7 @@ __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__re
         const auto ahead = row_rsrc(X + (row + step < m ? row + step : row) * ldx, row + step < m ? bytes : 0);
 #pragma unroll
         for (int c = 0; c < C; ++c) next[c].template load<NT>(ahead, ch[c]);
-        const Stats st = chunk_stats<T, W, C>(raw, last, d, inv, eps, red_sum, red_sq, wr);
+        const Stats st = chunk_stats<W>(raw, ch[C - 1], d, inv, eps, red_sum, red_sq, wr);
         const auto out = row_rsrc(Y + row * ldy, bytes);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -387,7 +392,7 @@ __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__re
             raw[c].widen(x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = fmaf(st.normed(x[e]), pw[c][e], pb[c][e]);
-            store8<NT>(out, ch[c], x, Y);
+            store8<NT, VEC>(out, ch[c], x, Y);
         }
         if (lane == 0 && wr == 0) {
             if (mean) mean[row] = st.c;
@@ -401,7 +406,7 @@ __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__re
 // stretch of it (16384 x 8192 bf16 152 us, 167 with runs; from the caches, runs are faster: 1024 x
 // 4096 12.4 us, 13.1 without). With W = 1, each wave takes every fourth of them. It writes their dx and keeps its lanes' columns of dweight and dbias in
 // registers; row p of the partial sums gets them at the end.
-template <class T, int W, int C, bool NT>
+template <class T, int W, int C, bool NT, bool VEC>
 __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__restrict__ dY, int64_t lddy,
                                                                     const T *__restrict__ X, int64_t ldx, int64_t m,
                                                                     int64_t d, const float *__restrict__ w,
@@ -414,6 +419,8 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wr = W == 1 ? 0 : wave;
     constexpr int R = W == 1 ? 4 : 1;
+    // 1024 threads have 128 registers each, too few for the next row beside two chunks of 32-bit values
+    constexpr bool kAhead = W < 16 || C < 2 || (VEC && sizeof(T) == 2);
     const int64_t p = blockIdx.x, run = (m + parts - 1) / parts;
     const int64_t apart = NT ? parts : 1, step = R * apart;
     const int64_t end = NT || m - p * run < run ? m : (p + 1) * run;
@@ -422,14 +429,14 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
     float wv[C][8], aw[C][8], ab[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        ch[c] = 8u * (64u * (W * c + wr) + lane);
-        load_params(w, ch[c], d, 1.0f, wv[c]);
+        ch[c] = Lanes<VEC>::first(W * c + wr, lane);
+        load_params<VEC>(w, ch[c], d, 1.0f, wv[c]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) aw[c][e] = ab[c][e] = 0.f;
     }
     const float inv = 1.0f / (float)d;
     const int64_t bytes = d * (int)sizeof(T);
-    Chunk<T> x[C], dy[C], nx[C], ndy[C];
+    Chunk<T, VEC> x[C], dy[C], nx[C], ndy[C];
     float mu = 0.f, rs = 0.f, nmu = 0.f, nrs = 0.f;
     auto fetch = [&](int64_t r) {
         const bool in = r < end;
@@ -443,8 +450,9 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
         nmu = mean[rr];
         nrs = rstd[rr];
     };
-    fetch(row);
+    if (kAhead) fetch(row);
     for (int par = 0; row < end; row += step, par ^= 1) {
+        if (!kAhead) fetch(row);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             x[c] = nx[c];
@@ -452,7 +460,7 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
         }
         mu = nmu;
         rs = nrs;
-        fetch(row + step);
+        if (kAhead) fetch(row + step);
         float g[C][8], h[C][8], a = 0.f, b = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -494,13 +502,21 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
             float t[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] = rs * fmaf(-h[c][e], b, g[c][e] - a);
-            store8(out, ch[c], t, dX);
+            store8<false, VEC>(out, ch[c], t, dX);
         }
     }
     // with W = 1, the four waves' columns meet in LDS, in wave order
     auto put = [&](float (&v)[C][8], float *to) {
         if (!to) return;
         to += p * d;
+        if (W > 1 && !VEC) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (ch[c] + 64 * e < d) to[ch[c] + 64 * e] = v[c][e];
+            return;
+        }
         if (W > 1) {
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -524,8 +540,15 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
                 const float4 o = join[k][i >> 1][i & 1][lane];
                 s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
             }
-            const uint32_t cc = 8u * (64u * (i >> 1) + lane) + 4u * (i & 1);
-            if (cc < d) *reinterpret_cast<float4 *>(to + cc) = s;
+            const uint32_t cc = Lanes<VEC>::first(i >> 1, lane) + 4 * (i & 1) * Lanes<VEC>::kStep;
+            if (VEC) {
+                if (cc < d) *reinterpret_cast<float4 *>(to + cc) = s;
+            } else {
+                const float one[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (cc + 64 * e < d) to[cc + 64 * e] = one[e];
+            }
         }
     };
     put(aw, pw);
@@ -562,7 +585,6 @@ __global__ __launch_bounds__(kGroupThreads<W>, sizeof(T) == 2 && C == 3 ? 3 : 1)
         ch[c] = 8u * (64u * (W * c + wr) + lane);
         next[c].load(row_rsrc(X + row * ldx, bytes), ch[c]);
     }
-    const bool last = ch[C - 1] < d;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         load_params(w, ch[c], d, 1.0f, pw[c]);
@@ -598,7 +620,7 @@ __global__ __launch_bounds__(kGroupThreads<W>, sizeof(T) == 2 && C == 3 ? 3 : 1)
         const auto ahead = row_rsrc(X + (row + step < m ? row + step : row) * ldx, row + step < m ? bytes : 0);
 #pragma unroll
         for (int c = 0; c < C; ++c) next[c].load(ahead, ch[c]);
-        const Stats st = chunk_stats<T, W, C>(raw, last, d, inv, eps, red_sum, red_sq, wr);
+        const Stats st = chunk_stats<W>(raw, ch[C - 1], d, inv, eps, red_sum, red_sq, wr);
         const auto rc = row_rsrc(codes + row * (d / 2), d / 2);
         const auto rs = packed ? row_rsrc(scales + 8 * row, m * (d / 32) - 8 * row) : row_rsrc(scales + row * (d / 32), d / 32);
 #pragma unroll
@@ -643,10 +665,10 @@ uintptr_t size_of(int type) { return type == KQ_BF16 ? 2 : 4; }
 // Workgroups that walk m rows: enough to fill the chip, the rest by stride.
 unsigned row_grid(int64_t m) { return (unsigned)(m < 65536 ? m : 65536); }
 
-// Rows in whole 16-byte pieces of at most 16384 channels: the vector path.
+// Whether every row is whole 16-byte pieces and so are the parameters.
 bool vector_rows(int type, int64_t d, std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> lds,
                  std::initializer_list<const float *> params) {
-    if (d % 8 != 0 || d > 16384) return false;
+    if (d % 8 != 0) return false;
     for (const void *p : ptrs)
         if (!aligned(p, 16)) return false;
     for (const int64_t ld : lds)
@@ -699,14 +721,20 @@ template <class T>
 kq_status launch_forward(const void *X, int64_t m, int64_t d, int64_t ldx, const float *weight, const float *bias,
                          float eps, void *Y, int64_t ldy, float *mean, float *rstd, bool vec, kq_stream_t stream) {
     const bool few = m < kqhost::compute_units();
-    auto go = [&](auto W, auto C, auto NT) {
-        hipLaunchKernelGGL((kq::norm::forward_kernel<T, W(), C(), NT()>), dim3(persistent_grid(m, W(), W() == 3 ? 12 : 16)),
+    auto go = [&](auto W, auto C, auto NT, auto VEC) {
+        hipLaunchKernelGGL((kq::norm::forward_kernel<T, W(), C(), NT(), VEC()>), dim3(persistent_grid(m, W(), W() == 3 ? 12 : 16)),
                            dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx, weight,
                            bias, eps, (T *)Y, ldy, mean, rstd);
     };
-    auto go_plain = [&](auto W, auto C) { go(W, C, std::false_type()); };
-    auto go_nt = [&](auto W, auto C) { go(W, C, std::true_type()); };
-    if (!vec || !(few ? first_shape(pieces_of(d), Few(), go_plain)
+    auto go_plain = [&](auto W, auto C) {
+        if (vec) go(W, C, std::false_type(), std::true_type());
+        else go(W, C, std::false_type(), std::false_type());
+    };
+    auto go_nt = [&](auto W, auto C) {
+        if (vec) go(W, C, std::true_type(), std::true_type());
+        else go(W, C, std::true_type(), std::false_type());
+    };
+    if (d > 16384 || !(few ? first_shape(pieces_of(d), Few(), go_plain)
                   : kq::streamed_once(2 * m * d * (int)sizeof(T)) ? first_shape(pieces_of(d), Many(), go_nt)
                                                                   : first_shape(pieces_of(d), Many(), go_plain)))
         hipLaunchKernelGGL((kq::norm::forward_any_kernel<T>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
@@ -718,14 +746,20 @@ template <class T>
 kq_status launch_backward(const void *dY, int64_t lddy, const void *X, int64_t ldx, int64_t m, int64_t d,
                           const float *weight, const float *mean, const float *rstd, void *dX, int64_t lddx,
                           int64_t parts, float *pw, float *pb, bool params, bool vec, kq_stream_t stream) {
-    auto go = [&](auto W, auto C, auto NT) {
-        hipLaunchKernelGGL((kq::norm::backward_kernel<T, W(), C(), NT()>), dim3((unsigned)parts),
+    auto go = [&](auto W, auto C, auto NT, auto VEC) {
+        hipLaunchKernelGGL((kq::norm::backward_kernel<T, W(), C(), NT(), VEC()>), dim3((unsigned)parts),
                            dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)dY, lddy,
                            (const T *)X, ldx, m, d, weight, mean, rstd, (T *)dX, lddx, (int)parts, pw, pb);
     };
-    auto go_plain = [&](auto W, auto C) { go(W, C, std::false_type()); };
-    auto go_nt = [&](auto W, auto C) { go(W, C, std::true_type()); };
-    if (vec && (kq::streamed_once(3 * m * d * (int)sizeof(T)) ? first_shape(pieces_of(d), Backward(), go_nt)
+    auto go_plain = [&](auto W, auto C) {
+        if (vec) go(W, C, std::false_type(), std::true_type());
+        else go(W, C, std::false_type(), std::false_type());
+    };
+    auto go_nt = [&](auto W, auto C) {
+        if (vec) go(W, C, std::true_type(), std::true_type());
+        else go(W, C, std::true_type(), std::false_type());
+    };
+    if (d <= 16384 && (kq::streamed_once(3 * m * d * (int)sizeof(T)) ? first_shape(pieces_of(d), Backward(), go_nt)
                                                               : first_shape(pieces_of(d), Backward(), go_plain)))
         return launched();
     hipLaunchKernelGGL((kq::norm::backward_dx_any_kernel<T>), dim3(row_grid(m)), dim3(kq::norm::kThreads), 0,
