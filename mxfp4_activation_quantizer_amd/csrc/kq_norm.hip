@@ -404,10 +404,10 @@ __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__re
 // Workgroup p of `parts` in the backward pass walks the p-th run of rows, or, where the rows
 // stream from memory (NT), the rows p, p + parts, ..., so that all workgroups together read one
 // stretch of it (16384 x 8192 bf16 152 us, 167 with runs; from the caches, runs are faster: 1024 x
-// 4096 12.4 us, 13.1 without). With W = 1, each wave takes every fourth of them. It writes their dx and keeps its lanes' columns of dweight and dbias in
+// 4096 12.4 us, 13.1 without). With W = 1, each of its R waves takes every R-th of them. It writes their dx and keeps its lanes' columns of dweight and dbias in
 // registers; row p of the partial sums gets them at the end.
-template <class T, int W, int C, bool NT, bool VEC>
-__global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__restrict__ dY, int64_t lddy,
+template <class T, int W, int C, int R, bool NT, bool VEC>
+__global__ __launch_bounds__(64 * W * R) void backward_kernel(const T *__restrict__ dY, int64_t lddy,
                                                                     const T *__restrict__ X, int64_t ldx, int64_t m,
                                                                     int64_t d, const float *__restrict__ w,
                                                                     const float *__restrict__ mean,
@@ -415,10 +415,10 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
                                                                     T *__restrict__ dX, int64_t lddx, int parts,
                                                                     float *__restrict__ pw, float *__restrict__ pb) {
     __shared__ float red[2][2][W];
-    __shared__ float4 join[W == 1 ? 4 : 1][W == 1 ? C : 1][2][64];
+    __shared__ float4 join[R][W == 1 ? C : 1][2][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wr = W == 1 ? 0 : wave;
-    constexpr int R = W == 1 ? 4 : 1;
+    static_assert(W == 1 || R == 1, "rows side by side have a wave each");
     // 1024 threads have 128 registers each, too few for the next row beside two chunks of 32-bit values
     constexpr bool kAhead = W < 16 || C < 2 || (VEC && sizeof(T) == 2);
     const int64_t p = blockIdx.x, run = (m + parts - 1) / parts;
@@ -505,7 +505,7 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
             store8<false, VEC>(out, ch[c], t, dX);
         }
     }
-    // with W = 1, the four waves' columns meet in LDS, in wave order
+    // with W = 1, the R waves' columns meet in LDS, in wave order
     auto put = [&](float (&v)[C][8], float *to) {
         if (!to) return;
         to += p * d;
@@ -533,10 +533,10 @@ __global__ __launch_bounds__(kGroupThreads<W>) void backward_kernel(const T *__r
             join[wave][c][1][lane] = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
         }
         __syncthreads();
-        for (int i = wave; i < 2 * C; i += 4) {
+        for (int i = wave; i < 2 * C; i += R) {
             float4 s = join[0][i >> 1][i & 1][lane];
 #pragma unroll
-            for (int k = 1; k < 4; ++k) {
+            for (int k = 1; k < R; ++k) {
                 const float4 o = join[k][i >> 1][i & 1][lane];
                 s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
             }
@@ -747,9 +747,13 @@ kq_status launch_backward(const void *dY, int64_t lddy, const void *X, int64_t l
                           const float *weight, const float *mean, const float *rstd, void *dX, int64_t lddx,
                           int64_t parts, float *pw, float *pb, bool params, bool vec, kq_stream_t stream) {
     auto go = [&](auto W, auto C, auto NT, auto VEC) {
-        hipLaunchKernelGGL((kq::norm::backward_kernel<T, W(), C(), NT(), VEC()>), dim3((unsigned)parts),
-                           dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)dY, lddy,
-                           (const T *)X, ldx, m, d, weight, mean, rstd, (T *)dX, lddx, (int)parts, pw, pb);
+        // Rows of one wave: eight at a time, so that a compute unit has two waves per SIMD (us, bf16 with 4
+        // and 8: 32768 x 512 36.5, 25.3; 29412 x 716 49.8, 36.2; 4096 x 1152 12.1, 11.6); four where the
+        // registers allow two anyway (fp32 by 16 bytes, three chunks: 4096 x 1152 14.8, 15.9)
+        constexpr int R = W() > 1 ? 1 : C() == 3 && sizeof(T) == 4 && VEC() ? 4 : 8;
+        hipLaunchKernelGGL((kq::norm::backward_kernel<T, W(), C(), R, NT(), VEC()>), dim3((unsigned)parts),
+                           dim3(64 * W() * R), 0, (hipStream_t)stream, (const T *)dY, lddy, (const T *)X, ldx, m, d,
+                           weight, mean, rstd, (T *)dX, lddx, (int)parts, pw, pb);
     };
     auto go_plain = [&](auto W, auto C) {
         if (vec) go(W, C, std::false_type(), std::true_type());
