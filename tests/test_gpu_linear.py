@@ -236,6 +236,27 @@ def test_backward_streamed(torch, kq, dt):
         ref.assert_near(g, v, t)
 
 
+@pytest.mark.parametrize("m,n", [(8311, 2729), (1, 511), (3, 513), (1000, 4001), (5, 1025)])
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_backward_odd_widths(torch, kq, m, n, dt):
+    """Rows that are no whole 16 bytes, streamed ones too: a lane takes every 64th column."""
+    dtype = getattr(torch, dt)
+    dout = torch.randn(m, n, generator=gen(torch, m), device="cuda").to(dtype)
+    z = torch.randn(m, n, generator=gen(torch, n), device="cuda").to(dtype)
+    for name in ("none", "silu"):
+        got = kq.mxfp4_linear_backward(dout, z, act=name)
+        want, tol = ref.linear_grad(dout, z, name)
+        for g, v, t in zip(got, want, tol):
+            ref.assert_near(g, v, t)
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,n", [(4100, 16384 * 2), (4099, 32771)])
+def test_residual_past_the_cache(torch, kq, m, n, dt):
+    """A residual of 256 MiB and more (read non-temporally), whole 16-byte rows and odd ones."""
+    check(torch, kq, m, n, 256, "relu", dt, True, seed=m)
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 512, 256), (64, 4001, 1184), (100, 4100, 2080), (2050, 1155, 2336), (1500, 3336, 3968)])
 def test_residual_in_place(torch, kq, m, n, k):
     """O = act(z) + O on every family of kernels, aligned rows and ragged ones."""

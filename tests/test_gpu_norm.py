@@ -139,6 +139,33 @@ def test_many_rows(torch, kq, m, d, dt):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+# the same number of pieces with widths that are no whole 16 bytes (a lane then takes every 64th element), and few rows
+ODD = [(260, 511), (300, 999), (700, 1155), (260, 2047), (257, 2059), (512, 4093), (300, 4607), (290, 6145), (260, 8191),
+       (258, 12289), (256, 16383), (33000, 1031), (8300, 4105), (5000, 8201), (2100, 16383), (9, 513), (5, 2051), (3, 9001),
+       (4, 16381), (1, 16384 + 7)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,d", ODD)
+def test_odd_widths(torch, kq, m, d, dt):
+    test_many_rows(torch, kq, m, d, dt)
+
+
+@pytest.mark.parametrize("m", [5, 31, 33, 1025, 2100])
+@pytest.mark.parametrize("d", [8, 500, 1001, 1152])
+def test_backward_of_one_wave_rows(torch, kq, m, d):
+    """Parts of fewer rows than waves, of some waves more than others; dweight and dbias each alone too."""
+    case("norm_grad %dx%d" % (m, d))
+    x, dy = rand(torch, m, d, seed=m, shift=0.5), rand(torch, m, d, seed=d)
+    w = rand(torch, d, seed=1, shift=1.0)
+    _, mean, rstd = kq.layernorm(x, w, eps=EPS, stats=True)
+    got = kq.layernorm_backward(dy, x, mean, rstd, w)
+    want, tol = ref.norm_grad(dy, x, mean, rstd, w)
+    for g, v, t, what in zip(got, want, tol, ("dx", "dw", "db")):
+        ref.assert_near(g, v, t, what)
+    assert torch.equal(kq.layernorm_backward(dy, x, mean, rstd, w, params=False)[0], got[0])
+
+
 def test_parameters_at_any_address(torch, kq):
     """weight, bias and their gradients 4-byte aligned only: the same values by the general path; the
     quantizing norm refuses them."""
