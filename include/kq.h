@@ -35,7 +35,8 @@
  *     owns and keeps alive until the enqueued work has finished. The library
  *     allocates nothing and never synchronizes; the only state it keeps
  *     between calls is a per-device cache of the compute-unit count (read once
- *     with hipDeviceGetAttribute by the packed GEMMs to size their launches).
+ *     with hipDeviceGetAttribute by the packed GEMMs, kq_mxfp4_linear and the
+ *     layer norm's entry points to size their launches).
  *   - Work is enqueued on `stream` (NULL = the default stream) and runs
  *     asynchronously; results are valid once the stream has reached it.
  *   - Arguments are checked on the host before anything is enqueued; on an
@@ -43,13 +44,17 @@
  *     runtime rejects returns KQ_ERR_HIP; kq_last_hip_error() then gives the
  *     hipError_t value (per host thread).
  *   - With m == 0 (or d == 0) nothing is read, written or launched and KQ_OK
- *     is returned.
- *   - Inputs must be finite; NaN or Inf inputs give unspecified codes.
- *   - Outputs must not overlap inputs.
+ *     is returned (but the gradients summed over no rows are set to zeros:
+ *     kq_layernorm_backward, kq_mxfp4_linear_backward).
+ *   - Inputs must be finite; NaN or Inf inputs give unspecified codes
+ *     (kq_layernorm says what they make of its outputs).
+ *   - Outputs must not overlap inputs (but kq_mxfp4_linear's residual may be
+ *     its output).
  *   - The GEMM-family entry points (kq_mxfp4_gemm*, kq_lowrank_project*,
  *     kq_dequantize_mxfp4_bf16, kq_pack_mxfp4_scales, kq_gemm_f32,
- *     kq_transform_quantize_mxfp4_gemm) refuse any size or leading dimension
- *     of 2^31 or more with KQ_ERR_UNSUPPORTED, before their finer limits.
+ *     kq_transform_quantize_mxfp4_gemm, kq_mxfp4_linear*) and the layer norm's
+ *     refuse any size or leading dimension of 2^31 or more with
+ *     KQ_ERR_UNSUPPORTED, before their finer limits.
  */
 #ifndef KQ_H
 #define KQ_H
@@ -538,21 +543,20 @@ typedef enum {
  * Layer norm over the rows of X, the norm in front of a quantized layer:
  *   mean_i = sum_c x_ic / d,  rstd_i = 1 / sqrt(sum_c (x_ic - mean_i)^2 / d + eps),
  *   y_ic = (x_ic - mean_i) rstd_i weight_c + bias_c,
- * all in fp32 (the squares are summed around the mean), y rounded once to its
- * type (nearest, ties to even).
+ * in fp32, the mean summed in fp64 (the squares are summed around it), y rounded
+ * once to its type (nearest, ties to even).
  *   X, Y          device, `type` (a kq_type) [m][ldx] and [m][ldy], ldx, ldy >= d;
- *                 aligned to their elements. With d % 8 == 0, d <= 16384, both 16-byte
- *                 aligned with rows of a multiple of 16 bytes, and weight, bias
- *                 16-byte aligned, rows are read once (the vector path); all
- *                 other layouts take a slower general path. Elements past d of
- *                 a row are neither read nor written.
+ *                 aligned to their elements. Rows of d <= 16384 are read once: in
+ *                 16-byte pieces with d % 8 == 0, X and Y 16-byte aligned with
+ *                 rows of a multiple of 16 bytes and weight, bias 16-byte
+ *                 aligned, else element by element (up to 1.5 times slower);
+ *                 wider rows are read three times. Elements past d of a row
+ *                 are neither read nor written.
  *   weight, bias  device, fp32 [d], or NULL (1 and 0)
  *   eps           >= 0 and finite (KQ_ERR_SHAPE)
  *   mean, rstd    device, fp32 [m], or NULL (not written); what
  *                 kq_layernorm_backward reads
- * Any d >= 1. Sizes or leading
- * dimensions of 2^31 or more: KQ_ERR_UNSUPPORTED. An unknown type:
- * KQ_ERR_UNSUPPORTED. A NaN or an infinity in X makes its own row and its rstd NaN
+ * Any d >= 1. An unknown type: KQ_ERR_UNSUPPORTED. A NaN or an infinity in X makes its own row and its rstd NaN
  * and no other. Range: |x| < 2^124, the sum of squares finite in fp32 (beyond it the
  * row's y are bias_c or NaN) and its mean plus eps at least 2^-126 (below it, so for
  * equal values with eps = 0, rstd is infinite and the row NaN or infinite).
@@ -567,8 +571,8 @@ kq_status kq_layernorm(const void *X, int type, int64_t m, int64_t d, int64_t ld
  *   dx = rstd (g - sum_c g / d - h sum_c g h / d),
  * and, summed over the rows in fp32 in a fixed order (the same result on every call),
  *   dweight_c = sum_i dy_ic h_ic,  dbias_c = sum_i dy_ic.
- *   dY, X, dX      device, `type` [m][lddy], [m][ldx], [m][lddx] (all >= d); vector
- *                  path as kq_layernorm
+ *   dY, X, dX      device, `type` [m][lddy], [m][ldx], [m][lddx] (all >= d); read
+ *                  and aligned as kq_layernorm's
  *   weight         device, fp32 [d], or NULL (1)
  *   mean, rstd     device, fp32 [m], as kq_layernorm wrote them
  *   dweight, dbias device, fp32 [d], or NULL (not wanted); written, not added to
@@ -624,9 +628,11 @@ kq_status kq_layernorm_quantize_mxfp4(const void *X, int type, int64_t m, int64_
  *                         kq_mxfp4_linear_backward reads)
  * Any m, n >= 0 and k % 32 == 0 (KQ_ERR_SHAPE; k == 0: z = bias, the operands are not
  * read). 256 rows of codes, m k/32 and n k/32 scale bytes and 256 rows of the outputs
- * and the residual must each span fewer than 2^31 bytes (KQ_ERR_UNSUPPORTED). A few rows (tokens being generated) run on a kernel that
- * streams W once with k split over the waves of a workgroup, many on the 256 x 256
- * tiles of kq_mxfp4_gemm_packed; the sums agree to fp32 rounding.
+ * and the residual must each span fewer than 2^31 bytes (KQ_ERR_UNSUPPORTED). A few
+ * rows (tokens being generated) run on a kernel that streams W once with k split over
+ * the waves of a workgroup, more on 64 x 64 or 128 x 128 tiles, many on the 256 x 256
+ * tiles of kq_mxfp4_gemm_packed, chosen by the sizes, the scales' layout and alignment
+ * alone: the same call gives the same bits, and the kernels agree to fp32 rounding.
  */
 kq_status kq_mxfp4_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
                           const uint8_t *scales_w, int packed, int64_t m, int64_t n, int64_t k, const float *bias,

@@ -1,7 +1,8 @@
-// The W4A4 product with a linear layer's epilogue, for few rows or few tiles,
+// The W4A4 product with a linear layer's epilogue,
 //   z = deq(A) deq(W)^T + bias,  O = act(z) + residual
 // (KroQuant, arXiv 2607.21446v1, Sec. 1 Eq. 2 for the product), and the
-// gradients of that epilogue.
+// gradients of that epilogue: here the kernels for few rows and for few tiles
+// and the choice between them and the 256 x 256 one (kq_gemm256.hip).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -40,6 +41,12 @@ enum Scales { kBytes = 0, kRows8 = 1, kPacked8 = 2 };
 // scale byte), and receives O row l % 16, columns 4 (l / 16) + 0..3 of the fragment.
 // Rows past m or n and k groups past k are past a record count (or pushed past it) and
 // read zero codes.
+//
+// Why: with few rows a product is its weights' bytes, and a tile's time the latency of its
+// stages one after the other, so k is split over the waves and the tiles are as small as the
+// instruction. 1 x 4096 x 4096 takes 5.0 us (W and its scales, 8.9 MB, from the Infinity
+// Cache: launch, two dependent latencies, the joined sums), 1 x 16384 x 8192 with W from HBM
+// 19.2 (71 MB, 3.7 TB/s). Deeper prefetch (D of 2, 4) is level or slower.
 template <int F>
 struct Stage {
     u32x4_t code[2][F];
@@ -190,6 +197,9 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
 //
 // Why: the 256 x 256 kernel takes as long for one tile as for one on every compute unit
 // (22 us at k = 4096), so products of fewer tiles than that are faster in smaller ones.
+// Bound by the lines in flight: a compute unit takes in about 55 GB/s whatever N is (128 x 4096
+// x 4096 8.3 us; two sets of waves on halves of a stage, or scales asked for 8 stages ahead, are
+// level).
 template <class T, int FA, int FB, int N>
 __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict__ ca, const uint8_t *__restrict__ sa,
                                                    const uint8_t *__restrict__ cw, const uint8_t *__restrict__ sw,

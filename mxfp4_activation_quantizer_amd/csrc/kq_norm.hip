@@ -115,7 +115,8 @@ __device__ __forceinline__ Stats row_stats(const T *x, int64_t d, float eps) {
     return st;
 }
 
-// Forward of rows wider than registers hold; one workgroup per row.
+// Forward of rows wider than registers hold; one workgroup per row, the row read three times
+// (twice from the caches).
 template <class T>
 __global__ __launch_bounds__(kThreads) void forward_any_kernel(const T *__restrict__ X, int64_t m, int64_t d,
                                                                int64_t ldx, const float *__restrict__ w,
@@ -220,7 +221,7 @@ __global__ __launch_bounds__(kColumns *kChains) void reduce_parts_kernel(const f
     }
 }
 
-// Layer norm, transform and quantizer of rows wider than the vector path holds: one
+// Layer norm, transform and quantizer of rows wider than registers hold: one
 // workgroup per row, a quad of lanes per 32-channel block, the row read three times.
 template <class T>
 __global__ __launch_bounds__(kThreads) void quantize_wide_kernel(const T *__restrict__ X, int64_t m, int64_t d,
@@ -278,8 +279,15 @@ __global__ __launch_bounds__(kThreads) void quantize_wide_kernel(const T *__rest
 // are left out of the sum of squares.
 // Rows are walked by a persistent grid, so the parameters (fp32, four times the
 // bytes of a bf16 row) are loaded once per workgroup, and the next row's loads
-// are in flight while a row is summed. With W = 1 a workgroup's 4 waves walk
+// are in flight while a row is summed. With W = 1 a workgroup's waves walk
 // rows of their own and there is no barrier in the loop.
+//
+// Bound by memory where there are many rows (us on the device; the bytes of one
+// read and one write): forward 8192 x 4608 bf16 27 (5.6 TB/s), 4096 x 16384 bf16
+// 47 (5.7), 8192 x 4609 bf16, element by element, 40 (3.8), 29412 x 716 19 (4.5);
+// backward 16384 x 4096 fp32 141 (5.7), 4096 x 1152 bf16 9.5 and 2.2 for the sum of
+// its parts. By the launch and two dependent latencies where there are few: one row
+// of 4096 2.3.
 // ---------------------------------------------------------------------------
 // Parameters of a lane's chunk (fp32; `none` where there are none or past d).
 template <bool VEC = true>
@@ -404,8 +412,9 @@ __global__ __launch_bounds__(kGroupThreads<W>) void forward_kernel(const T *__re
 // Workgroup p of `parts` in the backward pass walks the p-th run of rows, or, where the rows
 // stream from memory (NT), the rows p, p + parts, ..., so that all workgroups together read one
 // stretch of it (16384 x 8192 bf16 152 us, 167 with runs; from the caches, runs are faster: 1024 x
-// 4096 12.4 us, 13.1 without). With W = 1, each of its R waves takes every R-th of them. It writes their dx and keeps its lanes' columns of dweight and dbias in
-// registers; row p of the partial sums gets them at the end.
+// 4096 12.4 us, 13.1 without). With W = 1, each of its R waves takes every R-th of them. It writes
+// their dx and keeps its lanes' columns of dweight and dbias in registers; row p of the partial
+// sums gets them at the end.
 template <class T, int W, int C, int R, bool NT, bool VEC>
 __global__ __launch_bounds__(64 * W * R) void backward_kernel(const T *__restrict__ dY, int64_t lddy,
                                                                     const T *__restrict__ X, int64_t ldx, int64_t m,
@@ -555,11 +564,14 @@ __global__ __launch_bounds__(64 * W * R) void backward_kernel(const T *__restric
     put(ab, pb);
 }
 
-// Layer norm, transform and quantizer (vector path). A quad of lanes holds a 32-channel block and a wave's
+// Layer norm, transform and quantizer (lanes with 8 neighbours). A quad of lanes holds a 32-channel block and a wave's
 // chunk 16 of them (the segments of the fused transform kernels), for which every lane keeps
 // its block's 16 coefficients and its channels' parameters over all rows of the workgroup.
 // (bf16 with 3 chunks: held to the 168 registers of three waves per SIMD; at 170, two, 8192 x
 // 4608 takes 37 us instead of 28.5.)
+// Bound by vector instructions: 8192 x 4096 bf16 25 to 27 us, with the vector units busy 68% of
+// it (330 instructions per wave and row: statistics, norm, five transform stages, quantizer),
+// where its bytes take 17 at 5.1 TB/s. The sums on the matrix unit cost registers and gained nothing.
 template <class T, int W, int C>
 __global__ __launch_bounds__(kGroupThreads<W>, sizeof(T) == 2 && C == 3 ? 3 : 1) void quantize_kernel(
     const T *__restrict__ X, int64_t m, int64_t d, int64_t ldx, const float *__restrict__ w,
