@@ -114,6 +114,21 @@ struct Staged {
     static constexpr int U = N < 4 ? N : N < 16 ? 4 : 8;
 };
 
+// The bias of a lane's columns in such a block (0 past n).
+template <class T, int ROWS, int COLS>
+struct Bias {
+    typedef Staged<T, ROWS, COLS> S;
+    u32x4_t q[S::EC / 4];
+    __device__ __forceinline__ void load(const Epi &ep, int64_t j0) {
+        const int64_t left = ep.n - j0;
+        const auto rb = row_rsrc(ep.bias + j0, ep.bias && left > 0 ? 4 * (left < COLS ? left : COLS) : 0);
+        const uint32_t c = S::EC * ((threadIdx.x & 63) % S::kLanes);
+#pragma unroll
+        for (int i = 0; i < S::EC / 4; ++i) q[i] = __builtin_amdgcn_raw_buffer_load_b128(rb, 4 * c + 16 * i, 0, 0);
+    }
+    __device__ __forceinline__ float operator[](int e) const { return __uint_as_float(q[e >> 2][e & 3]); }
+};
+
 // Buffer over `cols` columns from j0 on of the rows i0 .. i0 + rows - 1: loads of the rows behind
 // them read zeros and stores are dropped (a row's pitch is no less than its columns).
 template <class T>
@@ -167,8 +182,8 @@ __device__ __forceinline__ u32x4_t piece_of(const float *v, const float *) {
 // Rows [0, ROWS) x columns [0, COLS) of a wave's fp32 sums, staged in LDS at reg in rows of COLS
 // with 16-byte chunk c at c ^ (row % (COLS / 4)), to O's rows i0 .. (those < rows) and columns
 // j0 ..: a lane takes 16 bytes of a row of O, or, where those are not aligned or not all inside
-// n, the wave takes a row's elements side by side. `first` holds the first rows' residual
-// (asked for before the sums were staged); each next batch's is in flight while one is finished.
+// n, the wave takes a row's elements side by side. `bias` and `first`, the first rows' residual,
+// were asked for before the sums were staged; each next batch's is in flight while one is finished.
 //
 // In batches, since a large tile has one wave per SIMD and nothing else to hide a row's latency:
 // with every row's bias, z, activation and residual on its own, 8192 x 16384 x 4096 took 427 us
@@ -176,6 +191,7 @@ __device__ __forceinline__ u32x4_t piece_of(const float *v, const float *) {
 // residual 137 instead of 64.
 template <class T, int ROWS, int COLS>
 __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep, int64_t i0, int rows, int64_t j0,
+                                              const Bias<T, ROWS, COLS> &bias,
                                               const Residual<T, ROWS, COLS> &first) {
     constexpr int CH = COLS / 4;
     const int lane = threadIdx.x & 63;
@@ -190,8 +206,6 @@ __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep,
         typedef Staged<T, ROWS, COLS> S;
         constexpr int EC = S::EC, U = S::U;
         const int c = lane % S::kLanes, r0 = lane / S::kLanes;
-        float bias[EC];
-        load_bias(ep, j0 + EC * c, bias);
         Residual<T, ROWS, COLS> now = first, next;
         for (int i = 0; i < S::N; i += U) {
             next.load(ep, i0, rows, j0, i + U);
@@ -225,7 +239,7 @@ __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep,
     static_assert(N % U == 0, "whole batches");
     const int c = lane % COLS, r0 = lane / COLS;
     if (c >= cols) return;
-    const float bias = ep.bias ? ep.bias[j0 + c] : 0.f;
+    const float bias1 = ep.bias ? ep.bias[j0 + c] : 0.f;
     const auto ra = block_rsrc<T>(ep.residual, ep.ldr, i0, rows, j0, cols);
     uint32_t now[U], next[U];
     auto fetch = [&](int i) {
@@ -241,7 +255,7 @@ __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep,
         float v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            v[u] = *reinterpret_cast<const float *>(at(kRows * (i + u) + r0, c >> 2) + 4 * (c & 3)) + bias;
+            v[u] = *reinterpret_cast<const float *>(at(kRows * (i + u) + r0, c >> 2) + 4 * (c & 3)) + bias1;
         auto store = [&](__amdgpu_buffer_rsrc_t r, uint32_t ld) {
 #pragma unroll
             for (int u = 0; u < U; ++u) store1(r, (uint32_t)(kRows * (i + u) + r0) * ld + c, v[u], type);

@@ -557,6 +557,12 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     // whole 16-byte pieces: columns inside n and aligned rows; otherwise element by
     // element, columns checked (rows past m are past the record count, or checked)
     const bool whole = g.rows16 && n0 + TN <= g.n;
+    typedef typename std::conditional<B16, uint16_t, float>::type T;
+    Bias<T, 128, 64> bias[NB / 2];
+    if constexpr (EPI) {
+#pragma unroll
+        for (int pass = 0; pass < NB / 2; ++pass) bias[pass].load(ep, n0 + wn + 64 * pass);
+    }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     uint8_t *reg = smem + 32768 * w;
     if constexpr (EPI) {
@@ -564,7 +570,6 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
         // whole 128-byte (bf16) or 256-byte (fp32) runs of a row leave. 8192 x 16384 x 4096 bf16, packed:
         // 276 us as kq_mxfp4_gemm_packed_bf16, 320 with a bias, 325 to 340 with gelu_tanh (vector
         // instructions) and with z too, 325 with a residual.
-        typedef typename std::conditional<B16, uint16_t, float>::type T;
 #pragma unroll
         for (int pass = 0; pass < NB / 2; ++pass) {
             Residual<T, 128, 64> add;
@@ -580,7 +585,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
                             acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
                     }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn + 64 * pass, add);
+            finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn + 64 * pass, bias[pass], add);
         }
         return;
     }

@@ -398,6 +398,8 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
     }
 
     constexpr int WM = TM / 2, WN = TN / 2, CH = WN / 4;
+    Bias<T, WM, WN> bias;
+    bias.load(ep, n0 + wn);
     Residual<T, WM, WN> add;
     add.load(ep, m0 + wm, rows_a - wm, n0 + wn, 0);
     // every load into LDS has landed (the ones past k too) and every wave is done with the stages
@@ -416,7 +418,7 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
                     floatx4_t{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
             }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn, add);
+    finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn, bias, add);
 }
 
 // Backward of the epilogue: wave w of workgroup (x, p) takes 512
