@@ -567,9 +567,9 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     uint8_t *reg = smem + 32768 * w;
     if constexpr (EPI) {
         // Always staged in fp32, 64 columns a pass: bias, activation and residual are applied where
-        // whole 128-byte (bf16) or 256-byte (fp32) runs of a row leave. 8192 x 16384 x 4096 bf16, packed:
-        // 276 us as kq_mxfp4_gemm_packed_bf16, 320 with a bias, 325 to 340 with gelu_tanh (vector
-        // instructions) and with z too, 325 with a residual.
+        // whole 128-byte (bf16) or 256-byte (fp32) runs of a row leave. us, 8192 x 16384 x 4096 bf16: 265 as
+        // kq_mxfp4_gemm_packed_bf16, 272 with a bias, 297 with gelu_tanh (vector instructions), 315 with z
+        // too, 302 with a residual.
 #pragma unroll
         for (int pass = 0; pass < NB / 2; ++pass) {
             Residual<T, 128, 64> add;
