@@ -626,19 +626,18 @@ __global__ __launch_bounds__(kGroupThreads<W>, sizeof(T) == 2 && C == 3 ? 3 : 1)
             }
         }
     }
-    for (; row < m; row += step) {
+    // one row in `now` while the next one comes into `ahead`
+    auto one = [&](Chunk<T> (&now)[C], Chunk<T> (&ahead)[C]) {
+        const auto rx = row_rsrc(X + (row + step < m ? row + step : row) * ldx, row + step < m ? bytes : 0);
 #pragma unroll
-        for (int c = 0; c < C; ++c) raw[c] = next[c];
-        const auto ahead = row_rsrc(X + (row + step < m ? row + step : row) * ldx, row + step < m ? bytes : 0);
-#pragma unroll
-        for (int c = 0; c < C; ++c) next[c].load(ahead, ch[c]);
-        const Stats st = chunk_stats<W>(raw, ch[C - 1], d, inv, eps, red_sum, red_sq, wr);
+        for (int c = 0; c < C; ++c) ahead[c].load(rx, ch[c]);
+        const Stats st = chunk_stats<W>(now, ch[C - 1], d, inv, eps, red_sum, red_sq, wr);
         const auto rc = row_rsrc(codes + row * (d / 2), d / 2);
         const auto rs = packed ? row_rsrc(scales + 8 * row, m * (d / 32) - 8 * row) : row_rsrc(scales + row * (d / 32), d / 32);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float y[8];
-            raw[c].widen(y);
+            now[c].widen(y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = fmaf(st.normed(y[e]), pw[c][e], pb[c][e]);
             if (factors) {
@@ -655,6 +654,15 @@ __global__ __launch_bounds__(kGroupThreads<W>, sizeof(T) == 2 && C == 3 ? 3 : 1)
             if (mean) mean[row] = st.c;
             if (rstd) rstd[row] = st.rstd;
         }
+    };
+    // two sets in turn: no register is copied
+    for (;;) {
+        one(next, raw);
+        row += step;
+        if (row >= m) break;
+        one(raw, next);
+        row += step;
+        if (row >= m) break;
     }
 }
 
