@@ -567,13 +567,14 @@ __global__ __launch_bounds__(64 * W * R) void backward_kernel(const T *__restric
 // Layer norm, transform and quantizer (lanes with 8 neighbours). A quad of lanes holds a 32-channel block and a wave's
 // chunk 16 of them (the segments of the fused transform kernels), for which every lane keeps
 // its block's 16 coefficients and its channels' parameters over all rows of the workgroup.
-// (bf16 with 3 chunks: held to the 168 registers of three waves per SIMD; at 170, two, 8192 x
-// 4608 takes 37 us instead of 28.5.)
+// (bf16 with 3 chunks and fewer than 8 waves: held to the 168 registers of three waves per SIMD;
+// at 170, two, 8192 x 4608 takes 37 us instead of 28.5. fp32 spills there: 8192 x 4608 44, 42
+// without, 2048 x 12288 68 and 33.)
 // Bound by vector instructions: 8192 x 4096 bf16 25 to 27 us, with the vector units busy 68% of
 // it (330 instructions per wave and row: statistics, norm, five transform stages, quantizer),
 // where its bytes take 17 at 5.1 TB/s. The sums on the matrix unit cost registers and gained nothing.
 template <class T, int W, int C>
-__global__ __launch_bounds__(kGroupThreads<W>, sizeof(T) == 2 && C == 3 ? 3 : 1) void quantize_kernel(
+__global__ __launch_bounds__(kGroupThreads<W>, sizeof(T) == 2 && C == 3 && W < 8 ? 3 : 1) void quantize_kernel(
     const T *__restrict__ X, int64_t m, int64_t d, int64_t ldx, const float *__restrict__ w,
     const float *__restrict__ b, float eps, const float *__restrict__ factors, uint8_t *__restrict__ codes,
     uint8_t *__restrict__ scales, int packed, float *__restrict__ y_debug, float *__restrict__ mean,
@@ -742,7 +743,13 @@ kq_status launch_forward(const void *X, int64_t m, int64_t d, int64_t ldx, const
                          float eps, void *Y, int64_t ldy, float *mean, float *rstd, bool vec, kq_stream_t stream) {
     const bool few = m < kqhost::compute_units();
     auto go = [&](auto W, auto C, auto NT, auto VEC) {
-        hipLaunchKernelGGL((kq::norm::forward_kernel<T, W(), C(), NT(), VEC()>), dim3(persistent_grid(m, W(), W() == 3 ? 12 : 16)),
+        // one resident round, by the registers that the shapes of more chunks leave (us, 1000 x 16384 bf16
+        // 13.5, 16.9 in two rounds); two for fp32 rows of 16-byte pieces (8192 x 16384 249, 267 in one)
+        constexpr int per_cu = W() == 8 && C() == 4 && (sizeof(T) == 2 || !VEC()) ? 8
+                               : C() == 3 && !VEC() ? (W() == 8 ? 8 : W() == 3 ? 9 : 12)
+                               : W() == 3           ? 12
+                                                    : 16;
+        hipLaunchKernelGGL((kq::norm::forward_kernel<T, W(), C(), NT(), VEC()>), dim3(persistent_grid(m, W(), per_cu)),
                            dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx, weight,
                            bias, eps, (T *)Y, ldy, mean, rstd);
     };
@@ -801,9 +808,16 @@ kq_status launch_quantize(const void *X, int64_t m, int64_t d, int64_t ldx, cons
                           float eps, const float *factors, uint8_t *codes, uint8_t *scales, int packed, float *y_debug,
                           float *mean, float *rstd, kq_stream_t stream) {
     auto go = [&](auto W, auto C) {
-        // one resident round; with one wave per row the coefficients' setup weighs more and 8 waves per
+        // one resident round: bf16 rows of three chunks leave registers for three waves per SIMD, fp32 ones
+        // and eight waves a workgroup for two (us, 8192 x 12288 bf16 71, 92 in 1.5 rounds; 4096 x 10240 37, 49);
+        // with one wave per row the coefficients' setup weighs more and 8 waves per
         // compute unit are faster (8192 x 512 5.9 us, 6.0 with 16)
-        hipLaunchKernelGGL((kq::norm::quantize_kernel<T, W(), C()>), dim3(persistent_grid(m, W(), C() == 3 ? 12 : W() == 1 ? 8 : 16)),
+        constexpr int per_cu = W() == 8 && C() >= 3       ? 8
+                               : C() == 3 && sizeof(T) == 4 ? (W() == 3 ? 6 : 8)
+                               : C() == 3                   ? 12
+                               : W() == 1                   ? 8
+                                                            : 16;
+        hipLaunchKernelGGL((kq::norm::quantize_kernel<T, W(), C()>), dim3(persistent_grid(m, W(), per_cu)),
                            dim3(kq::norm::kGroupThreads<W()>), 0, (hipStream_t)stream, (const T *)X, m, d, ldx, weight,
                            bias, eps, factors, codes, scales, packed, y_debug, mean, rstd);
     };
