@@ -1,10 +1,22 @@
 """The host side of the layer norm's and kq_mxfp4_linear's entry points under AddressSanitizer and
 UndefinedBehaviorSanitizer on the CPU (no GPU): argument checks at the extremes of int64 sizes."""
 import os
+import subprocess
 
 import pytest
 
-from tests.test_sanitizers import CLANG, ENV, HIPCC, HOST_SAN, SAN, run
+SAN = os.path.join(os.path.dirname(os.path.abspath(__file__)), "sanitize")
+HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CLANG = "/opt/rocm/llvm/bin/clang"
+# sanitizers on the host pass only
+HOST_SAN = "-Xarch_host -fsanitize=address -Xarch_host -fsanitize=undefined -Xarch_host -fno-sanitize-recover=all".split()
+ENV = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1", UBSAN_OPTIONS="halt_on_error=1")
+
+
+def run(cmd, **kw):
+    p = subprocess.run(cmd, capture_output=True, text=True, **kw)
+    assert p.returncode == 0, "%s\n%s\n%s" % (" ".join(cmd), p.stdout[-4000:], p.stderr[-4000:])
+    return p
 
 
 @pytest.mark.skipif(not os.path.exists(HIPCC) or not os.path.exists(CLANG), reason="ROCm toolchain not found")
