@@ -571,7 +571,7 @@ __global__ __launch_bounds__(64 * W * R) void backward_kernel(const T *__restric
 // at 170, two, 8192 x 4608 takes 37 us instead of 28.5. fp32 spills there: 8192 x 4608 44, 42
 // without, 2048 x 12288 68 and 33.)
 // Bound by vector instructions: 8192 x 4096 bf16 25 to 27 us, with the vector units busy 68% of
-// it (330 instructions per wave and row: statistics, norm, five transform stages, quantizer),
+// it (about 290 instructions per wave and row: statistics, norm, five transform stages, quantizer),
 // where its bytes take 17 at 5.1 TB/s. The sums on the matrix unit cost registers and gained nothing.
 template <class T, int W, int C>
 __global__ __launch_bounds__(kGroupThreads<W>, sizeof(T) == 2 && C == 3 && W < 8 ? 3 : 1) void quantize_kernel(

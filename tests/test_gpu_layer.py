@@ -215,3 +215,67 @@ def test_backward_captured_while_an_eager_graph_lives(torch, kq):
         assert all(torch.equal(a, b) for a, b in zip(dz, kq.mxfp4_linear_backward(dy, xd, act="silu")))
     loss.backward()
     assert bool((x.grad == 2).all())
+
+
+@pytest.mark.parametrize("m,d", [(3, 515), (3, 1024), (300, 515), (300, 1024), (40, 16390)])
+def test_each_gradient_alone(torch, kq, m, d):
+    """The C entry points with one of the summed gradients, or with the sum alone: the values of the whole call,
+    and nothing else written."""
+    import ctypes
+    L = kq.lib()
+    x, dy = torch.randn(m, d, device="cuda"), torch.randn(m, d, device="cuda")
+    w = torch.rand(d, device="cuda") + 0.5
+    _, mean, rstd = kq.layernorm(x, w, stats=True)
+    dx, dw, db = kq.layernorm_backward(dy, x, mean, rstd, w)
+    n = ctypes.c_int64(0)
+    assert L.kq_layernorm_backward_workspace_bytes(m, d, ctypes.byref(n)) == 0
+    ws = torch.empty(max(n.value, 16), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    for which in (0, 1):
+        got, gx = torch.full((d + 8,), 7.0, device="cuda"), torch.empty_like(x)
+        out = got.data_ptr()
+        assert L.kq_layernorm_backward(dy.data_ptr(), d, x.data_ptr(), d, 0, m, d, w.data_ptr(), mean.data_ptr(),
+                                       rstd.data_ptr(), gx.data_ptr(), d, None if which else out, out if which else None,
+                                       ws.data_ptr(), n.value, stream) == 0
+        assert torch.equal(gx, dx) and torch.equal(got[:d], (dw, db)[which]) and bool((got[d:] == 7.0).all())
+    dz, dbias = kq.mxfp4_linear_backward(dy, x, act="silu")
+    assert L.kq_mxfp4_linear_backward_workspace_bytes(m, d, ctypes.byref(n)) == 0
+    ws = torch.empty(max(n.value, 16), dtype=torch.uint8, device="cuda")
+    got, gz = torch.full((d + 8,), 7.0, device="cuda"), torch.empty_like(x)
+    silu = kq.ACTS["silu"]
+    assert L.kq_mxfp4_linear_backward(dy.data_ptr(), d, x.data_ptr(), d, 0, m, d, silu, None, 0, got.data_ptr(),
+                                      ws.data_ptr(), n.value, stream) == 0
+    assert torch.equal(got[:d], dbias) and bool((got[d:] == 7.0).all())
+    assert L.kq_mxfp4_linear_backward(dy.data_ptr(), d, x.data_ptr(), d, 0, m, d, silu, gz.data_ptr(), d, None, None, 0,
+                                      stream) == 0
+    assert torch.equal(gz, dz)
+
+
+def test_two_streams_at_once(torch, kq):
+    """Calls of every operator on two streams at the same time, each with its own workspace: each the values of a
+    call alone."""
+    m, d = 600, 1152
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    x = [torch.randn(m, d, device="cuda") for _ in streams]
+    dy = torch.randn(m, d, device="cuda")
+    w = torch.rand(d, device="cuda") + 0.5
+    cw, sw = kq.quantize_mxfp4_f32(torch.randn(1000, d, device="cuda"))
+
+    def run(v):
+        y, mean, rstd = kq.layernorm(v, w, stats=True)
+        codes, scales = kq.layernorm_quantize_mxfp4(v, w)
+        o, z = kq.mxfp4_linear(codes, scales, cw, sw, act="gelu", want_pre=True, bf16=False)
+        return (y, codes, scales, o, z) + kq.layernorm_backward(dy, v, mean, rstd, w) + \
+            kq.mxfp4_linear_backward(o, z, act="gelu")
+
+    want = [run(v) for v in x]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(x[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
