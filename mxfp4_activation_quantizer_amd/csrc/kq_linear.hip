@@ -512,8 +512,9 @@ bool good_type(int type) { return type == KQ_F32 || type == KQ_BF16; }
 bool good_act(int act) { return act >= KQ_ACT_NONE && act <= KQ_ACT_GELU_TANH; }
 
 // Parts of the bias gradient's sum: those of m rows, at most as many as give 8192 workgroups of
-// 512 columns.
+// 512 columns; none of no columns.
 int64_t column_parts(int64_t m, int64_t n) {
+    if (n == 0) return 0;
     const int64_t strips = (n + 511) / 512, most = 8192 / (strips < 128 ? strips : 128), p = kqhost::row_parts(m);
     return p < most ? p : most;
 }

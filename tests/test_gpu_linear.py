@@ -343,3 +343,11 @@ def test_refusals(torch, kq):
         kq.mxfp4_linear_backward(x, x.bfloat16(), act="relu")
     with pytest.raises(TypeError):
         kq.mxfp4_linear_backward(x.double(), x, act="relu")
+
+
+@pytest.mark.parametrize("m,n", [(5, 0), (0, 0), (0, 5)])
+def test_backward_of_nothing(torch, kq, m, n):
+    """No columns: an empty dz and an empty dbias; no rows: dbias of zeros."""
+    x = torch.empty((m, n), device="cuda")
+    dz, dbias = kq.mxfp4_linear_backward(x, x, act="silu")
+    assert dz.shape == (m, n) and dbias.shape == (n,) and not bool(dbias.any())
