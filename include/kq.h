@@ -557,8 +557,8 @@ typedef enum {
  *   mean, rstd    device, fp32 [m], or NULL (not written); what
  *                 kq_layernorm_backward reads
  * Any d >= 1. An unknown type: KQ_ERR_UNSUPPORTED. A NaN or an infinity in X makes its own row and its rstd NaN
- * and no other. Range: |x| < 2^124, the sum of squares finite in fp32 (beyond it the
- * row's y are bias_c or NaN) and its mean plus eps at least 2^-126 (below it, so for
+ * and no other. Range: the sum of squares finite in fp32 (beyond it the row's y are
+ * bias_c or NaN) and its mean plus eps at least 2^-126 (below it, so for
  * equal values with eps = 0, rstd is infinite and the row NaN or infinite).
  */
 kq_status kq_layernorm(const void *X, int type, int64_t m, int64_t d, int64_t ldx, const float *weight,

@@ -331,13 +331,11 @@ __device__ __forceinline__ Stats chunk_stats(const Chunk<T, VEC> (&raw)[C], uint
     for (int c = 0; c < C; ++c) {
         float x[8];
         raw[c].widen(x);
-        if (sizeof(T) == 2) {
-            // eight bf16 values add up exactly in fp32 unless their exponents differ by 13 or more
-            s += (double)(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += (double)x[e];
-        }
+        // each value widened first: eight bf16 values whose exponents differ by 13 or more do not add up
+        // exactly in fp32, and a mean that is left of large ones cancelling would show it (with the eight
+        // summed in fp32: norm into codes 8192 x 4096 24.1 us, 24.9; norm 8192 x 4608 27.7, 27.9)
+        auto pair = [&](int e) { return (double)x[e] + (double)x[e + 1]; };
+        s += (pair(0) + pair(2)) + (pair(4) + pair(6));
     }
     Stats st;
     st.set_mean(row_sum<W>(s, red_sum, wave), inv);

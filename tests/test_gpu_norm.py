@@ -372,3 +372,31 @@ def test_refusals(torch, kq):
         kq.layernorm_quantize_mxfp4(x, packed=True)
     with pytest.raises(ValueError):
         kq.layernorm_quantize_mxfp4(x, factors=v)
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,d", [(3, 40), (300, 512), (300, 1152), (5, 4096), (300, 4096), (300, 4609), (260, 16384), (2, 20000)])
+def test_mean_of_cancelling_values(torch, kq, m, d, dt):
+    """The mean is summed in 64 bits whatever the type, the width and a lane's share of the row: large
+    values that cancel, within eight neighbours and 64 apart, leave it with 64 bits' rounding. The
+    sum of d terms is off by at most d 2^-53 of the sum of their magnitudes (its scaling by 1 / d adds 2
+    such roundings) and the mean itself is rounded to fp32 once."""
+    dtype = getattr(torch, dt)
+    g = torch.Generator("cuda").manual_seed(d)
+    x = torch.randn(m, d, generator=g, device="cuda")
+    for apart in (1, 3, 64):
+        at = torch.arange(0, max(0, d - apart), 2 * apart + 8, device="cuda")
+        big = 1e4 * torch.rand(m, at.numel(), generator=g, device="cuda").to(dtype).float() + 256
+        x[:, at], x[:, at + apart] = big, -big
+    x = x.to(dtype)
+
+    def near(mean):
+        e = x.double()
+        mu = e.mean(1)
+        tol = ref.U * (1 + 2.0 ** -20) * mu.abs() + (d + 4) * 2.0 ** -53 * e.abs().mean(1)
+        assert bool(((mean.double() - mu).abs() <= tol).all()), float(((mean.double() - mu).abs() / tol).max())
+
+    near(kq.layernorm(x, eps=EPS, stats=True)[1])
+    near(kq.layernorm(strided(torch, x, 3, 1)[0], eps=EPS, stats=True)[1])  # element by element
+    if d % 32 == 0:
+        near(kq.layernorm_quantize_mxfp4(x, eps=EPS, stats=True)[2])
