@@ -528,7 +528,8 @@ typedef enum { KQ_F32 = 0, KQ_BF16 = 1 } kq_type;
  *   KQ_ACT_NONE       z
  *   KQ_ACT_RELU       max(z, 0); slope 1 where z > 0, else 0
  *   KQ_ACT_SILU       z / (1 + exp(-z))
- *   KQ_ACT_GELU       z (1 + erf(z / sqrt 2)) / 2 (erf to 1.5e-7 absolute)
+ *   KQ_ACT_GELU       z (1 + erf(z / sqrt 2)) / 2 (fp32 outputs to 8e-7 of themselves,
+ *                     z >= -13; bf16 ones to 1.5e-5 before their rounding)
  *   KQ_ACT_GELU_TANH  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
  */
 typedef enum {

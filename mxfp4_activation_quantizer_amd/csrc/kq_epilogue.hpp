@@ -84,7 +84,7 @@ __device__ __forceinline__ void load_residual(const Epi &ep, int64_t i, int64_t 
 template <class T, int N>
 __device__ __forceinline__ void finish(float (&v)[N], const float (&add)[N], const Epi &ep, int64_t i, int64_t j) {
     if (ep.Z) store_piece(static_cast<T *>(ep.Z) + i * ep.ldz + j, v);
-    activate(v, ep.act);
+    activate<T>(v, ep.act);
     if (ep.residual) {
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] += add[e];
@@ -101,7 +101,7 @@ template <class T>
 __device__ __forceinline__ void finish1(float z, float add, const Epi &ep, int64_t i, int64_t j) {
     float v[1] = {z};
     if (ep.Z) store1(static_cast<T *>(ep.Z) + i * ep.ldz + j, z);
-    activate(v, ep.act);
+    activate<T>(v, ep.act);
     store1(static_cast<T *>(ep.O) + i * ep.ldo + j, ep.residual ? v[0] + add : v[0]);
 }
 
@@ -228,7 +228,7 @@ __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep,
                                                            (uint32_t)(S::kRows * (i + u) + r0) * pitch + 16u * c, 0, 2);
             };
             if (ep.Z) store(rz, pz);
-            activate(v, ep.act);
+            activate<T>(v, ep.act);
             if (ep.residual) now.add_to(v);
             store(ro, po);
             now = next;
@@ -262,7 +262,7 @@ __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep,
             for (int u = 0; u < U; ++u) store1(r, (uint32_t)(kRows * (i + u) + r0) * ld + c, v[u], type);
         };
         if (ep.Z) store(rz, (uint32_t)ep.ldz);
-        activate(v, ep.act);
+        activate<T>(v, ep.act);
         if (ep.residual) {
 #pragma unroll
             for (int u = 0; u < U; ++u) v[u] += __uint_as_float(sizeof(T) == 2 ? now[u] << 16 : now[u]);

@@ -351,3 +351,29 @@ def test_backward_of_nothing(torch, kq, m, n):
     x = torch.empty((m, n), device="cuda")
     dz, dbias = kq.mxfp4_linear_backward(x, x, act="silu")
     assert dz.shape == (m, n) and dbias.shape == (n,) and not bool(dbias.any())
+
+
+def with_activation(torch, kq, z, name, dt):
+    """act(z) and its slope at given fp32 z: k = 0 makes z the bias; the slope is dz of dout = 1."""
+    n = z.numel()
+    none = [torch.empty((r, 0), dtype=torch.uint8, device="cuda") for r in (1, 1, n, n)]
+    out = kq.mxfp4_linear(*none, bias=z, act=name, bf16=dt == "bfloat16")[0]
+    slope = kq.mxfp4_linear_backward(torch.ones(1, n, device="cuda"), z.view(1, n), act=name)[0][0]
+    return out, slope
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_gelu_is_good_to_its_last_bits(torch, kq, dt):
+    """gelu keeps a relative error where it vanishes: P(z) to 13 u of itself (t to 2 u, times at most 2.3 = the
+    slope of log R in log t: 4.6; the polynomial 0.6 of its fit and 1.5 of rounding; the exponential 2 u of the
+    instruction and 2 of its correction; two products; 1 - tail adds a rounding), and one more for the product
+    with z. bf16 outputs: the fit 30 u, t to 3 u times 2.3, the polynomial and its products 4, the exponential 2
+    and its exponent's roundings 1.2 z^2, before the output's own. The slope P + z phi adds the exponential's 4 u and three products' u of z phi, and its own sum's."""
+    z = torch.cat((torch.linspace(-13, 13, 40001), torch.linspace(-1e-3, 1e-3, 2001))).cuda()
+    out, slope = with_activation(torch, kq, z, "gelu", dt)
+    e = z.double()
+    p = 0.5 * torch.erfc(-e * 0.5 ** 0.5)
+    u = 14 if dt == "float32" else 46 + 1.2 * e * e
+    ref.assert_near(out, e * p, u * ref.U * (e * p).abs(), "gelu")
+    zphi = e * torch.exp(-e * e / 2) * 0.3989422804014327
+    ref.assert_near(slope, p + zphi, 13 * ref.U * p + 8 * ref.U * zphi.abs() + ref.U * (p + zphi).abs(), "slope")
