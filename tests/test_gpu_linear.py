@@ -377,3 +377,16 @@ def test_gelu_is_good_to_its_last_bits(torch, kq, dt):
     ref.assert_near(out, e * p, u * ref.U * (e * p).abs(), "gelu")
     zphi = e * torch.exp(-e * e / 2) * 0.3989422804014327
     ref.assert_near(slope, p + zphi, 13 * ref.U * p + 8 * ref.U * zphi.abs() + ref.U * (p + zphi).abs(), "slope")
+
+
+@pytest.mark.parametrize("name,low", [("silu", -80.0), ("gelu_tanh", -9.0)])
+def test_logistic_error_grows_with_its_exponent_alone(torch, kq, name, low):
+    """silu and gelu_tanh in fp32 relative to their values: the logistic's exponent y is off by 1.3 u of
+    itself in silu (the constant 0.23 u, the product 1 u), by 6 u in gelu_tanh (constants 1 and 3, z^2, the sum
+    and the product 1 each), which exp(y) multiplies by |y|; exp2 2 u, 1 + e 1 u, the reciprocal 2 u, z s 1 u."""
+    z = torch.linspace(low, 30.0, 30011).cuda()
+    out, _ = with_activation(torch, kq, z, name, "float32")
+    e = z.double()
+    y = -e if name == "silu" else -2 * (2 / torch.pi) ** 0.5 * (e + 0.044715 * e ** 3)
+    want = e / (1 + torch.exp(y))
+    ref.assert_near(out, want, ((1.3 if name == "silu" else 6) * y.clamp(min=0) + 7) * ref.U * want.abs(), name)
