@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "kq.h"
+#include "kq_choice.hpp"
 #include "kq_device.hpp"
 #include "kq_dma.hpp"
 #include "kq_epilogue.hpp"
@@ -561,47 +562,13 @@ kq_status launch_tiles(const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, 
     return launched();
 }
 
-// Which kernel a product of m x n outputs over `stages` 256-k stages runs on: the least of
-// seven estimates, in us, fitted to 535 measured products (m = 1 .. 8192, n = 512 .. 11008, k = 256
-// .. 8192; the choice is 1.1% slower than the fastest on average, 30% at worst): a launch, and per
-// round of tiles a tile's own time and that of its stages. Up to 16 rows only the kernel that
-// splits k is considered (16384 x 8192, W from HBM: one row 19.2 us, 20.5 with 64 x 64 tiles, 16 rows
-// 19.8 and 20.9).
-// Measured at k = 4096, n = 4096, in the order of the list:
-//      16 rows  5.7   6.4   6.8   8.2  10.6  14.3
-//      64      12.9   9.9   7.6   8.4  10.8  14.6
-//     128      22.5  16.3  12.0   8.3  10.8  15.0  19.2
-//     512                  39.1  15.8  13.1  16.4  21.8
-//    1024                        27.9  24.3  17.7  22.8
-//    4096                       100.6  78.4  56.0  41.6
-enum Kernel { kProduct11, kProduct12, kProduct22, kTile64Deep, kTile64, kTile128, kTile256 };
-
-Kernel choose_kernel(int64_t m, int64_t n, int stages, bool packed, bool can256) {
-    const int cus = kqhost::compute_units();
-    const double st = stages;
-    auto tiles = [&](int64_t tm, int64_t tn) {  // per compute unit
-        return (double)((m + tm - 1) / tm) * (double)((n + tn - 1) / tn) / cus;
-    };
-    Kernel best = kProduct11;
-    double least = 2.8 + ceil(tiles(16, 16)) * (0.148 * st + 0.14);
-    auto consider = [&](Kernel k, double us) {
-        if (us < least) best = k, least = us;
-    };
-    consider(kProduct12, 2.6 + ceil(tiles(16, 32)) * (0.21 * st + 0.13));
-    if (m <= 16) return best;
-    consider(kProduct22, 2.6 + ceil(tiles(32, 32)) * (0.277 * st + 0.27));
-    consider(kTile64Deep, 2.5 + ceil(tiles(64, 64)) * (0.296 * st + 2.69));
-    // four at a time per compute unit, a stage's latency each while there are fewer
-    consider(kTile64, 2.8 + fmax(0.63 * st, 0.25 * st + tiles(64, 64) * (0.2 * st + 0.89)));
-    consider(kTile128, 2.9 + ceil(tiles(128, 128)) * (0.65 * st + 2.65));
-    if (can256) {
-        // whole rounds, and a last one of at most half the compute units in half tiles
-        const double full = packed ? 13.55 + 1.41 * st : 2.1 + 2.33 * st, half = packed ? 6.07 + 1.05 * st : 3.16 + 1.48 * st;
-        const double t256 = tiles(256, 256), rem = t256 - floor(t256);
-        consider(kTile256, 1.65 + floor(t256) * full + (rem == 0 ? 0 : rem <= 0.5 ? half : full));
-    }
-    return best;
-}
+using kq::linear::Kernel;
+using kq::linear::kProduct11;
+using kq::linear::kProduct12;
+using kq::linear::kProduct22;
+using kq::linear::kTile256;
+using kq::linear::kTile64;
+using kq::linear::kTile64Deep;
 
 template <class T, int MF, int NF, int WK>
 kq_status launch_any_product(const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, const uint8_t *sw, int packed,
@@ -660,7 +627,7 @@ kq_status kq_mxfp4_linear(const uint8_t *codes_a, const uint8_t *scales_a, const
     if (k == 0) packed = 0;
     const bool big = k > 0 && (packed ? aligned(scales_a, 16) && aligned(scales_w, 16)
                                       : k % 128 == 0 && aligned(scales_a, 4) && aligned(scales_w, 4));
-    const Kernel kernel = choose_kernel(m, n, g.stages, packed != 0, big);
+    const Kernel kernel = kq::linear::choose_kernel(m, n, g.stages, packed != 0, big, kqhost::compute_units());
     if (kernel == kTile256)
         return kqhost::gemm256_linear(codes_a, scales_a, codes_w, scales_w, packed, k, type, ep, stream);
     return type == KQ_BF16

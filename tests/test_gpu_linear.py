@@ -390,3 +390,48 @@ def test_logistic_error_grows_with_its_exponent_alone(torch, kq, name, low):
     y = -e if name == "silu" else -2 * (2 / torch.pi) ** 0.5 * (e + 0.044715 * e ** 3)
     want = e / (1 + torch.exp(y))
     ref.assert_near(out, want, ((1.3 if name == "silu" else 6) * y.clamp(min=0) + 7) * ref.U * want.abs(), name)
+
+
+# products of the 256 x 256 kernel (tests/test_linear_choice.py holds them to it): tiles computed whole and as
+# halves, rows of whole 16 bytes and not, ragged last tiles, k of whole stages (either layout) and with a half one
+BIG = [(4096, 4096, 4096), (4100, 4360, 4096), (4093, 4103, 2304), (3333, 4104, 4096), (4096, 4096, 768),
+       (4096, 4096, 3968), (4100, 4363, 1920), (4100, 4360, 1920), (4100, 8200, 1152)]
+BIG_IN_PLACE = [(4100, 4360, 4096), (4093, 4103, 2304)]
+# with outputs of 256 MiB and more, whose residual is read non-temporally
+BIG_STREAMED = [(8192, 16384, 1024, "bfloat16"), (8192, 8192, 1024, "float32"), (8200, 16391, 1024, "bfloat16")]
+
+# 32 x 32 tiles of ragged products with a partial last stage
+PART = [(50, 4001, 1184), (90, 2050, 800)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,n,k", PART)
+def test_partial_stages(torch, kq, m, n, k, dt):
+    check(torch, kq, m, n, k, "silu", dt, False, seed=k, pad=5)
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,n,k", BIG)
+def test_big_tiles(torch, kq, m, n, k, dt):
+    for i, packed in enumerate([False, True] if k % 256 == 0 else [False]):
+        check(torch, kq, m, n, k, ACTS[(m + k // 128 + i) % 5], dt, packed, seed=k, pad=(0, 8, 5)[(m + i) % 3])
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("m,n,k", BIG_IN_PLACE)
+def test_big_residual_in_place(torch, kq, m, n, k, packed):
+    ca, sa = operand(torch, kq, m, k, 1)
+    cw, sw = operand(torch, kq, n, k, 2, k ** -0.5)
+    if packed:
+        sa, sw = kq.pack_mxfp4_scales(sa), kq.pack_mxfp4_scales(sw)
+    for bf16 in (True, False):
+        x = torch.randn(m, n, generator=gen(torch, 4), device="cuda").to(torch.bfloat16 if bf16 else torch.float32)
+        want = kq.mxfp4_linear(ca, sa, cw, sw, act="silu", residual=x, bf16=bf16, packed=packed)
+        got = kq.mxfp4_linear(ca, sa, cw, sw, act="silu", residual=x, out=x, bf16=bf16, packed=packed)
+        assert got is x and torch.equal(x, want)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("m,n,k,dt", BIG_STREAMED)
+def test_big_residual_past_the_cache(torch, kq, m, n, k, dt, packed):
+    check(torch, kq, m, n, k, "relu", dt, packed, seed=m)
