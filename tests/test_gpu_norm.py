@@ -400,3 +400,79 @@ def test_mean_of_cancelling_values(torch, kq, m, d, dt):
     near(kq.layernorm(strided(torch, x, 3, 1)[0], eps=EPS, stats=True)[1])  # element by element
     if d % 32 == 0:
         near(kq.layernorm_quantize_mxfp4(x, eps=EPS, stats=True)[2])
+
+
+def resident(torch, waves, per_cu):
+    """Rows that the persistent grid has at a time with `per_cu` waves per compute unit."""
+    return torch.cuda.get_device_properties(0).multi_processor_count * per_cu // waves
+
+
+# a width for every shape that many rows take, whole rows and partial last pieces, with its waves per row and the most
+# waves per compute unit that any of its launches keeps
+LOOPED = [(512, 1, 16), (416, 1, 16), (1024, 1, 16), (1152, 1, 16), (2048, 2, 16), (4096, 4, 16), (2592, 4, 16), (4608, 3, 12),
+          (5120, 4, 16), (8192, 8, 16), (12288, 8, 16), (16384, 8, 16), (14336, 8, 16)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("d,waves,per_cu", LOOPED)
+def test_rows_one_after_another(torch, kq, d, waves, per_cu, dt):
+    """Three rows and more per workgroup or wave, and a remainder: the norm and the quantizing norm give each row
+    what they give it in a call of as many rows as are resident at once, where no workgroup has a second one (the
+    same shape of kernel, so the same bits); that call is checked against 64 bits by the other tests' bounds."""
+    dtype = getattr(torch, dt)
+    once = resident(torch, waves, 4)  # a row each whatever the launch keeps, and still the shapes of many rows
+    once = max(once, torch.cuda.get_device_properties(0).multi_processor_count)
+    m = 3 * resident(torch, waves, per_cu) + 5
+    case("rows in turn %dx%d %s, %d at once" % (m, d, dt, once))
+    x = rand(torch, m, d, seed=d, scale=2.0, shift=0.5, dtype=dtype)
+    x *= torch.linspace(0.5, 3.0, m, device="cuda")[:, None].to(dtype)  # no two rows of one scale
+    w, b = rand(torch, d, seed=1, scale=0.3, shift=1.0), rand(torch, d, seed=2, scale=0.2)
+    fac = torch.from_numpy(synth.lu_perturbed_factors(d // 32, 4)).cuda()
+    y, mean, rstd = kq.layernorm(x, w, b, eps=EPS, stats=True)
+    quant = [kq.layernorm_quantize_mxfp4(x, w, b, f, eps=EPS, packed=p, stats=True)
+             for f in (fac, None) for p in ((False, True) if d % 256 == 0 else (False,))]
+    for lo in range(0, m, once):
+        hi = min(m, lo + once)
+        lo = max(0, hi - once)  # the last call has as many rows too
+        rows = x[lo:hi]
+        part = kq.layernorm(rows, w, b, eps=EPS, stats=True)
+        assert all(torch.equal(a[lo:hi], c) for a, c in zip((y, mean, rstd), part)), (lo, hi)
+        q = kq.layernorm_quantize_mxfp4(rows, w, b, fac, eps=EPS, stats=True)
+        assert all(torch.equal(a[lo:hi], c) for a, c in zip(quant[0], q)), (lo, hi)
+    y0, mu, rs, y_tol, mu_tol, rs_tol = ref.norm(x, w, b, EPS)
+    ref.assert_near(y, y0, y_tol, "y")
+    ref.assert_near(quant[0][2], mu, mu_tol, "mean")
+    ref.assert_near(quant[0][3], rs, rs * rs_tol, "rstd")
+    if d % 256 == 0:
+        for plain, packed in ((quant[0], quant[1]), (quant[2], quant[3])):
+            assert torch.equal(plain[0], packed[0]) and torch.equal(plain[2], packed[2]) and torch.equal(plain[3], packed[3])
+            assert torch.equal(kq.pack_mxfp4_scales(plain[1]).view(-1), packed[1].view(-1))
+    # T = I: the codes are those of the quantizer on the norm in check mode, row by row
+    yt = torch.empty((m, d), device="cuda")
+    plain = kq.layernorm_quantize_mxfp4(x, w, b, None, eps=EPS, y_debug=yt)
+    want = kq.quantize_mxfp4_f32(yt)
+    same = quant[-1] if d % 256 else quant[2]
+    assert torch.equal(plain[0], want[0]) and torch.equal(plain[1], want[1])
+    assert torch.equal(plain[0], same[0]) and torch.equal(plain[1], same[1])
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("d,waves,per_cu", [(511, 1, 16), (999, 1, 16), (1155, 1, 16), (2047, 2, 16), (4093, 4, 16), (4607, 3, 12),
+                                            (5123, 4, 16), (8191, 8, 16), (12281, 8, 16), (16383, 8, 16)])
+def test_odd_rows_one_after_another(torch, kq, d, waves, per_cu, dt):
+    """The same for the norm of rows that are no whole 16 bytes."""
+    dtype = getattr(torch, dt)
+    once = max(resident(torch, waves, 4), torch.cuda.get_device_properties(0).multi_processor_count)
+    m = 3 * resident(torch, waves, per_cu) + 5
+    x = rand(torch, m, d, seed=d, scale=2.0, shift=0.5, dtype=dtype)
+    w, b = rand(torch, d, seed=1, scale=0.3, shift=1.0), rand(torch, d, seed=2, scale=0.2)
+    got = kq.layernorm(x, w, b, eps=EPS, stats=True)
+    for lo in range(0, m, once):
+        hi = min(m, lo + once)
+        lo = max(0, hi - once)
+        part = kq.layernorm(x[lo:hi], w, b, eps=EPS, stats=True)
+        assert all(torch.equal(a[lo:hi], c) for a, c in zip(got, part)), (lo, hi)
+    y0, mu, rs, y_tol, mu_tol, rs_tol = ref.norm(x, w, b, EPS)
+    ref.assert_near(got[0], y0, y_tol, "y")
+    ref.assert_near(got[1], mu, mu_tol, "mean")
+    ref.assert_near(got[2], rs, rs * rs_tol, "rstd")
