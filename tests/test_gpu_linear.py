@@ -435,3 +435,30 @@ def test_big_residual_in_place(torch, kq, m, n, k, packed):
 @pytest.mark.parametrize("m,n,k,dt", BIG_STREAMED)
 def test_big_residual_past_the_cache(torch, kq, m, n, k, dt, packed):
     check(torch, kq, m, n, k, "relu", dt, packed, seed=m)
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m", [1, 2, 3, 5, 17, 33, 127, 255, 1023, 1025, 1027, 2053, 9001])
+@pytest.mark.parametrize("n", [8, 72, 511, 1032, 4101])
+def test_backward_sums_every_row_once(torch, kq, m, n, dt):
+    """With dout small integers dbias is an integer without any rounding (relu keeps or drops whole ones), below
+    2^24: a row left out or counted twice shows in every column."""
+    sums_every_row_once(torch, kq, m, n, dt)
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,n", [(8311, 2728), (8311, 2729), (1033, 21680), (1033, 21681), (45013, 520)])
+def test_backward_sums_every_row_once_streamed(torch, kq, m, n, dt):
+    sums_every_row_once(torch, kq, m, n, dt)
+
+
+def sums_every_row_once(torch, kq, m, n, dt):
+    dtype = getattr(torch, dt)
+    v = torch.randint(1, 4, (m, n), generator=gen(torch, m), device="cuda")
+    z = torch.randn(m, n, generator=gen(torch, n), device="cuda").to(dtype)
+    dout = torch.where(torch.rand(m, n, generator=gen(torch, m + n), device="cuda") < 0.5, -v, v).to(dtype)
+    dz, dbias = kq.mxfp4_linear_backward(dout)
+    assert torch.equal(dz, dout) and torch.equal(dbias.double(), dout.double().sum(0))
+    dz, dbias = kq.mxfp4_linear_backward(dout, z, act="relu")
+    want = torch.where(z > 0, dout, torch.zeros_like(dout))
+    assert torch.equal(dz, want) and torch.equal(dbias.double(), want.double().sum(0))

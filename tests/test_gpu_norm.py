@@ -476,3 +476,32 @@ def test_odd_rows_one_after_another(torch, kq, d, waves, per_cu, dt):
     ref.assert_near(got[0], y0, y_tol, "y")
     ref.assert_near(got[1], mu, mu_tol, "mean")
     ref.assert_near(got[2], rs, rs * rs_tol, "rstd")
+
+
+def small_integers(torch, shape, seed, dtype):
+    """-3 .. 3 without 0: a column's sum stays below 2^24 up to 2^22 rows, so that every order of fp32 sums is exact."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    v = torch.randint(1, 4, shape, generator=g, device="cuda")
+    return torch.where(torch.rand(shape, generator=g, device="cuda") < 0.5, -v, v).to(dtype)
+
+
+# rows that leave remainders of the parts (at most 256, of 4 rows and more), of the rows that a workgroup has side by
+# side (4 or 8) and of both; a width for every shape of the backward kernel, whole 16-byte rows and odd ones; at the end
+# calls of 128 MiB and more, whose parts take every parts-th row
+EXACT = [(m, d) for m in (1, 3, 5, 7, 9, 31, 33, 1023, 1025, 1027, 2053, 4111) for d in (8, 1000, 1001, 1152)] + \
+    [(m, d) for m in (1, 6, 1025, 1531) for d in (513, 2048, 2047, 4096, 4093, 8192, 8191, 12288, 12281, 16384, 16383, 16400)] + \
+    [(33001, 1032), (33001, 1031), (50021, 520), (11003, 4096), (11003, 4095), (5531, 8200), (2801, 16384), (2801, 16383)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,d", EXACT)
+def test_backward_sums_every_row_once(torch, kq, m, d, dt):
+    """With dy small integers, x = 1 or -1, mean 0 and rstd 1 the parameters' gradients are integers without any
+    rounding: a row left out or counted twice shows in every column."""
+    dtype = getattr(torch, dt)
+    dy = small_integers(torch, (m, d), m + d, dtype)
+    x = torch.where(small_integers(torch, (m, d), m, torch.float32) > 0, 1.0, -1.0).to(dtype)
+    zero, one = torch.zeros(m, device="cuda"), torch.ones(m, device="cuda")
+    _, dw, db = kq.layernorm_backward(dy, x, zero, one)
+    assert torch.equal(dw.double(), (dy.double() * x.double()).sum(0)), "dweight"
+    assert torch.equal(db.double(), dy.double().sum(0)), "dbias"
