@@ -11,7 +11,8 @@ Algorithmic bytes per element: 2 (bf16 in) + 0.5 (E2M1 codes) + 1/32 (E8M0
 scale) = 2.53125. Inputs are rotated over enough buffer sets (>= 512 MB) that
 no launch is served from the 256 MB Infinity Cache.
 
-Prints ONE JSON line on stdout (rank 0, N = 1).
+Prints ONE JSON line on stdout (rank 0, N = 1), short enough to survive where only
+the end of the output is kept; --tables FILE has everything measured.
 """
 from __future__ import annotations
 
@@ -58,6 +59,9 @@ def parse():
                     help="time steps as eager launches instead of replaying one HIP graph per step")
     ap.add_argument("--no-extras", action="store_true",
                     help="skip the other configs, the MFMA form, the fold and the W4A4 GEMM timings")
+    ap.add_argument("--tables", metavar="FILE",
+                    help="also write the whole result, with every measurement's statistics, to FILE as JSON "
+                         "(the line on stdout has their medians)")
     ap.add_argument("--tensor", type=int, choices=[3072, 12288], default=None,
                     help="time only the tensor with this d (for profiler runs)")
     ap.add_argument("--gemm-launches", type=int, default=0, metavar="N",
@@ -627,6 +631,27 @@ def gemm_launches(n, shape, out="fp32"):
     log("packed gemm %s %s: %d launches, median %.1f us" % (shape, out, n, float(np.median(d))))
 
 
+# the line has to be whole where the last 8000 characters of the output are kept
+LINE_LIMIT = 7500
+
+
+def medians(v):
+    """v with every measurement's statistics replaced by its median in us, and without notes."""
+    if isinstance(v, dict):
+        if "median_us" in v and not any(isinstance(x, (dict, list)) for x in v.values()):
+            return v["median_us"]
+        return {k: medians(x) for k, x in v.items() if not isinstance(x, str)}
+    return [medians(x) for x in v] if isinstance(v, list) else v
+
+
+def headline(out):
+    """The result as one line: the extras' medians, and none of them where even those would not fit."""
+    line = json.dumps(dict(out, **({"extras": medians(out["extras"])} if "extras" in out else {})))
+    if len(line) > LINE_LIMIT:
+        line = json.dumps({k: v for k, v in out.items() if k != "extras"})
+    return line
+
+
 def main():
     args = parse()
     if args.summarize_pmc:
@@ -737,7 +762,10 @@ def main():
     if args.cpu_seconds > 0 and not args.only:
         log("CPU oracle baseline (>= %.0f s)" % args.cpu_seconds)
         out["cpu_baseline"] = cpu_baseline(ws, args.cpu_seconds)
-    print(json.dumps(out), flush=True)
+    if args.tables:
+        with open(args.tables, "w") as f:
+            json.dump(out, f, indent=1)
+    print(headline(out), flush=True)
 
 
 if __name__ == "__main__":
