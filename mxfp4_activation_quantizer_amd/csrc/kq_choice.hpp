@@ -9,18 +9,18 @@ namespace kq {
 namespace linear {
 
 // Which kernel a product of m x n outputs over `stages` 256-k stages runs on: the least of
-// seven estimates, in us, fitted to 535 measured products (m = 1 .. 8192, n = 512 .. 11008, k = 256
-// .. 8192; the choice is 1.1% slower than the fastest on average, 30% at worst): a launch, and per
-// round of tiles a tile's own time and that of its stages. Up to 16 rows only the kernel that
+// seven estimates, in us, fitted to 535 measured products (profiles/linear_products_by_kernel.md: m = 1
+// .. 8192, n = 512 .. 11008, k = 256 .. 8192; the choice is 1.0% slower than the fastest on average, 35% at
+// worst): a launch, and per round of tiles a tile's own time and that of its stages. Up to 16 rows only the kernel that
 // splits k is considered (16384 x 8192, W from HBM: one row 19.2 us, 20.5 with 64 x 64 tiles, 16 rows
 // 19.8 and 20.9).
 // Measured at k = 4096, n = 4096, in the order of the list:
-//      16 rows  5.7   6.4   6.8   8.2  10.6  14.3
-//      64      12.9   9.9   7.6   8.4  10.8  14.6
-//     128      22.5  16.3  12.0   8.3  10.8  15.0  19.2
-//     512                  39.1  15.8  13.1  16.4  21.8
-//    1024                        27.9  24.3  17.7  22.8
-//    4096                       100.6  78.4  56.0  41.6
+//      16 rows  5.7   6.4   6.8   8.2  10.5  14.1
+//      64      12.9   9.9   7.6   8.1  10.7  14.4
+//     128      22.5  16.3  12.1   8.2  10.6  14.8  19.0
+//     512                  39.1  15.6  12.7  16.0  21.3
+//    1024                        27.0  22.9  16.9  22.0
+//    4096                        94.2  71.4  52.6  38.2
 enum Kernel { kProduct11, kProduct12, kProduct22, kTile64Deep, kTile64, kTile128, kTile256 };
 
 // can256: the scales' alignment and k allow the 256 x 256 kernel; cus: compute units.

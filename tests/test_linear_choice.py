@@ -72,3 +72,17 @@ def test_big_residuals(ask):
     assert all(r[0] == "256 x 256" for r in ask(in_place + streamed))
     for m, n, _, dt in gpu.BIG_STREAMED:
         assert m * n * (2 if dt == "bfloat16" else 4) >= 256 << 20
+
+
+def test_choice_follows_the_measured_products(ask):
+    """On the measured products (profiles/linear_products_by_kernel.md) the chosen kernel is hardly ever far from the
+    fastest one."""
+    products, times = [], []
+    for row in open(os.path.join(ROOT, "profiles", "linear_products_by_kernel.md")):
+        c = [x.strip() for x in row.strip().strip("|").split("|")]
+        if c[0] in ("packed", "MX"):
+            products.append((int(c[1]), int(c[2]), int(c[3]), int(c[0] == "packed")))
+            times.append({k: float(t) for k, t in zip(KERNELS, c[4:]) if t})
+    assert len(products) == 535
+    loss = [t[kernel] / min(t.values()) for t, (kernel, _, _) in zip(times, ask(products))]
+    assert sum(loss) / len(loss) < 1.015 and max(loss) < 1.36 and sum(x > 1.1 for x in loss) <= 23
