@@ -426,7 +426,8 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
 // columns (8 per lane: 1 KB of a bf16 row) of every fourth of the p-th `group_rows` rows, U of
 // them in flight; the waves' column sums meet in LDS in wave order. Bound by HBM: two reads and a
 // write per element against about 25 vector operations of 39 T/s for gelu_tanh (131 us without
-// an activation too at 8192 x 16384 bf16: 6.1 TB/s; with every parts-th row instead 140).
+// an activation too at 8192 x 16384 bf16: 6.1 TB/s; with every parts-th row instead 140). gelu has
+// more operations than fit under that: 142.
 template <class T, bool NT, bool VEC>
 __global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO, int64_t lddo,
                                                        const T *__restrict__ Z, int64_t ldz, int64_t m, int64_t n,

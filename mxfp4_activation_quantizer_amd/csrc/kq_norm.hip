@@ -283,8 +283,8 @@ __global__ __launch_bounds__(kThreads) void quantize_wide_kernel(const T *__rest
 // rows of their own and there is no barrier in the loop.
 //
 // Bound by memory where there are many rows (us on the device; the bytes of one
-// read and one write): forward 8192 x 4608 bf16 27 (5.6 TB/s), 4096 x 16384 bf16
-// 47 (5.7), 8192 x 4609 bf16, element by element, 40 (3.8), 29412 x 716 19 (4.5);
+// read and one write): forward 8192 x 4608 bf16 28 (5.4 TB/s), 4096 x 16384 bf16
+// 45 (5.9), 8192 x 4609 bf16, element by element, 35 (4.3), 29412 x 716 17.5 (4.8);
 // backward 16384 x 4096 fp32 141 (5.7), 4096 x 1152 bf16 9.5 and 2.2 for the sum of
 // its parts. By the launch and two dependent latencies where there are few: one row
 // of 4096 2.3.
@@ -565,12 +565,14 @@ __global__ __launch_bounds__(64 * W * R) void backward_kernel(const T *__restric
 // Layer norm, transform and quantizer (lanes with 8 neighbours). A quad of lanes holds a 32-channel block and a wave's
 // chunk 16 of them (the segments of the fused transform kernels), for which every lane keeps
 // its block's 16 coefficients and its channels' parameters over all rows of the workgroup.
-// (bf16 with 3 chunks and fewer than 8 waves: held to the 168 registers of three waves per SIMD;
-// at 170, two, 8192 x 4608 takes 37 us instead of 28.5. fp32 spills there: 8192 x 4608 44, 42
+// (bf16 with 3 chunks and fewer than 8 waves: held to the 168 registers of three waves per SIMD:
+// 8192 x 1152 11.8 us, 14.3 without, 8192 x 4608 28.9 and 29.7. fp32 spills there: 8192 x 4608 44, 42
 // without, 2048 x 12288 68 and 33.)
-// Bound by vector instructions: 8192 x 4096 bf16 25 to 27 us, with the vector units busy 68% of
-// it (about 290 instructions per wave and row: statistics, norm, five transform stages, quantizer),
-// where its bytes take 17 at 5.1 TB/s. The sums on the matrix unit cost registers and gained nothing.
+// 8192 x 4096 bf16 takes 25 to 28 us, its bytes 17 at 5.1 TB/s. Neither memory nor the vector units
+// alone bound it (profiles/counters_norm_into_codes.md): 340 vector instructions per wave and row
+// (statistics, norm, five transform stages, quantizer) keep the units busy 71% of the time; the
+// waves wait for a row or at the two barriers of its sums 31% of theirs, and for their turn to issue
+// another 31%. The sums on the matrix unit cost registers and gained nothing.
 template <class T, int W, int C>
 __global__ __launch_bounds__(kGroupThreads<W>, sizeof(T) == 2 && C == 3 && W < 8 ? 3 : 1) void quantize_kernel(
     const T *__restrict__ X, int64_t m, int64_t d, int64_t ldx, const float *__restrict__ w,
@@ -713,11 +715,13 @@ bool first_shape(int64_t pieces, std::integer_sequence<int, W, C, Rest...>, F f)
 // In each list, an entry is reached only by rows of more than W (C - 1) pieces, so that no chunk but
 // the last has places past the row's end.
 // Many rows: few waves per row, so that a wave has work between its sums, with as few empty
-// places as the lists allow (us at 8192 x 1152: norm 8.5 with 1 x 3, 10.2 with 2 x 2, 11.0 with
-// 4 x 1; norm and quantizer 12.5, 14.6, 14.8).
+// places as the lists allow (us at 8192 x 1152: norm 8.8 with 1 x 3, 10.7 with 2 x 2, 12.7 with
+// 4 x 1; norm and quantizer 11.8, 14.6, 16.2).
 // Above three waves, multiples of four: a workgroup's waves are dealt to the four SIMDs from
 // the first on, so 5 waves take a second place on one of them in every workgroup. 3 x 3 is for
-// rows of 9 pieces (norm and quantizer 8192 x 4608: 28.7 us, 32.5 with 4 x 3, 41 with 8 x 2).
+// rows of 9 pieces (norm and quantizer 8192 x 4608: 28.9 us, 33.1 with 4 x 3, 41.0 with 8 x 2; the norm
+// 28.1, 28.3 and 30.4). Rows of 5 and 6 pieces take 4 x 2, with up to three of its eight places
+// empty; 3 x 2 was not measured for them.
 using Many = std::integer_sequence<int, 1, 1, 1, 2, 1, 3, 2, 2, 4, 2, 3, 3, 4, 3, 8, 2, 8, 3, 8, 4>;
 // Fewer rows than compute units: one chunk per lane where 16 waves reach, so that a row's time
 // is one memory latency.
