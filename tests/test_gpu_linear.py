@@ -462,3 +462,88 @@ def sums_every_row_once(torch, kq, m, n, dt):
     dz, dbias = kq.mxfp4_linear_backward(dout, z, act="relu")
     want = torch.where(z > 0, dout, torch.zeros_like(dout))
     assert torch.equal(dz, want) and torch.equal(dbias.double(), want.double().sum(0))
+
+
+# a product for each kernel, with rows of O of whole 16 bytes
+PLACES = [(5, 512, 512), (40, 4096, 512), (60, 4096, 2304), (130, 4096, 4096), (600, 4096, 1024), (2050, 1160, 2304),
+          (4096, 4096, 768)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,n,k", PLACES)
+def test_operands_at_unlike_addresses(torch, kq, m, n, k, dt):
+    """Residual, output, z and bias each with a row stride and an address of its own, aligned as their elements at
+    least, in every combination of one that is not 16-byte aligned: the same bits as with all of them aligned."""
+    dtype, g = getattr(torch, dt), gen(torch, k)
+    ca, sa = operand(torch, kq, m, k, 1)
+    cw, sw = operand(torch, kq, n, k, 2, k ** -0.5)
+    res0 = torch.randn(m, n, generator=g, device="cuda").to(dtype)
+    bias0 = torch.randn(n, generator=g, device="cuda")
+    want, pre0 = kq.mxfp4_linear(ca, sa, cw, sw, bias=bias0, act="gelu", residual=res0, bf16=dt == "bfloat16",
+                                 want_pre=True)
+
+    def place(extra, offset):
+        buf = torch.full((m * (n + extra) + offset,), float("nan"), dtype=dtype, device="cuda")
+        return buf, buf[offset:].view(m, n + extra)[:, :n]
+
+    for odd in ("none", "residual", "out", "pre", "bias", "all"):
+        at = lambda name: (7, 3) if odd in (name, "all") else (16, 0)
+        _, res = place(*at("residual"))
+        res.copy_(res0)
+        (obuf, out), (zbuf, pre) = place(*at("out")), place(*at("pre"))
+        bias = torch.empty(n + 3, device="cuda")[at("bias")[1]:][:n]
+        bias.copy_(bias0)
+        kq.mxfp4_linear(ca, sa, cw, sw, bias=bias, act="gelu", residual=res, out=out, pre=pre, bf16=dt == "bfloat16")
+        assert torch.equal(out, want) and torch.equal(pre, pre0), odd
+        assert int(obuf.isnan().sum()) == obuf.numel() - m * n and int(zbuf.isnan().sum()) == zbuf.numel() - m * n
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 4096, 512), (600, 4096, 1024), (2050, 1160, 2304), (4096, 4096, 768)])
+def test_packed_scales_8_byte_aligned(torch, kq, m, n, k):
+    """Packed scales need 8 bytes of alignment; the 256 x 256 kernel, which wants 16, is passed over without them."""
+    ca, sa = operand(torch, kq, m, k, 1)
+    cw, sw = operand(torch, kq, n, k, 2, k ** -0.5)
+    pa, pw = kq.pack_mxfp4_scales(sa), kq.pack_mxfp4_scales(sw)
+    o, z, o_tol, z_tol = ref.linear(ca, sa, cw, sw, None, "silu", None)
+
+    def moved(s, by):
+        v = torch.empty(s.numel() + by, dtype=torch.uint8, device="cuda")[by:].view(s.shape)
+        v.copy_(s)
+        return v
+
+    for by_a, by_w in ((0, 0), (8, 0), (0, 8), (8, 8)):
+        ref.assert_near(kq.mxfp4_linear(ca, moved(pa, by_a), cw, moved(pw, by_w), act="silu", bf16=False, packed=True), o, o_tol)
+    with pytest.raises(kq.KQError):
+        kq.mxfp4_linear(ca, moved(pa, 4), cw, pw, packed=True)
+
+
+@pytest.mark.parametrize("m,n,k", [(4100, 4360, 1920), (4096, 4096, 768)])
+def test_big_tiles_with_scales_at_any_address(torch, kq, m, n, k):
+    """MX scales 4-byte aligned stay on the 256 x 256 kernel, the same bits; at other addresses another one runs."""
+    ca, sa = operand(torch, kq, m, k, 1)
+    cw, sw = operand(torch, kq, n, k, 2, k ** -0.5)
+    want = kq.mxfp4_linear(ca, sa, cw, sw, act="silu", bf16=False)
+    o, z, o_tol, z_tol = ref.linear(ca, sa, cw, sw, None, "silu", None)
+    ref.assert_near(want, o, o_tol)
+    for by in (4, 12, 1, 2):
+        a = torch.empty(sa.numel() + by, dtype=torch.uint8, device="cuda")[by:].view(sa.shape)
+        a.copy_(sa)
+        got = kq.mxfp4_linear(ca, a, cw, sw, act="silu", bf16=False)
+        if by % 4 == 0:
+            assert torch.equal(got, want)
+        ref.assert_near(got, o, o_tol)
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_far_arguments(torch, kq, dt):
+    """Activations where they are saturated and far beyond: 0 or z itself; NaN stays NaN, and alone."""
+    far = torch.tensor([-1e30, -3e19, -200.0, -105.0, 0.0, 60.0, 200.0, 3e19, 1e30], device="cuda")
+    z = torch.cat((far, torch.full((1,), float("nan"), device="cuda"), far))
+    n = far.numel()
+    for name in ACTS[1:]:
+        out, slope = with_activation(torch, kq, z, name, dt)
+        assert bool(out[n].isnan()) and int(out.isnan().sum()) == 1, name
+        assert int(slope.isnan().sum()) == (name != "relu"), name  # z > 0 is false for NaN: relu's slope is 0
+        want = torch.where(far > 0, far, 0 * far).to(out.dtype)
+        for part in (out[:n], out[n + 1:]):
+            assert bool(((part - want).abs() <= 1e-30).all()) and torch.equal(part[5:], want[5:]), name

@@ -505,3 +505,49 @@ def test_backward_sums_every_row_once(torch, kq, m, d, dt):
     _, dw, db = kq.layernorm_backward(dy, x, zero, one)
     assert torch.equal(dw.double(), (dy.double() * x.double()).sum(0)), "dweight"
     assert torch.equal(db.double(), dy.double().sum(0)), "dbias"
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("m,d", [(7, 1152), (300, 1152), (300, 4096), (5, 16400)])
+def test_rows_at_unlike_addresses(torch, kq, m, d, dt):
+    """Input, output and gradients each with a row stride and an address of its own, one of them not 16-byte aligned:
+    within the bounds of the aligned call."""
+    dtype = getattr(torch, dt)
+    x0, dy0 = rand(torch, m, d, seed=5, dtype=dtype), rand(torch, m, d, seed=6, dtype=dtype)
+    w, b = rand(torch, d, seed=1, shift=1.0), rand(torch, d, seed=2)
+    y0, mu, rs, y_tol, mu_tol, rs_tol = ref.norm(x0, w, b, EPS)
+    for odd in ("x", "y", "dy", "dx"):
+        at = lambda name: (3, 1) if odd == name else (16, 0)
+        x, _ = strided(torch, x0, *at("x"))
+        dy, _ = strided(torch, dy0, *at("dy"))
+        y, ybuf = strided(torch, torch.zeros_like(x0), *at("y"))
+        dx, xbuf = strided(torch, torch.zeros_like(x0), *at("dx"))
+        _, mean, rstd = kq.layernorm(x, w, b, eps=EPS, out=y, stats=True)
+        ref.assert_near(y, y0, y_tol, odd)
+        _, dw, db = kq.layernorm_backward(dy, x, mean, rstd, w, dx=dx)
+        want, tol = ref.norm_grad(dy0, x0, mean, rstd, w)
+        for got, v, t, what in zip((dx, dw, db), want, tol, ("dx", "dw", "db")):
+            ref.assert_near(got, v, t, odd + " " + what)
+        for buf in (ybuf, xbuf):
+            assert int(buf.isnan().sum()) == buf.numel() - m * d
+
+
+def test_more_wide_rows_than_workgroups(torch, kq):
+    """Rows too wide for registers, more than the 65536 workgroups of their launch: the rows behind get what they get
+    in a call of their own."""
+    m, d, cut = 65536 + 700, 16416, 65536
+    case("wide rows %dx%d" % (m, d))
+    x = torch.empty(m, d, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(3))
+    w, b = rand(torch, d, seed=1, shift=1.0), rand(torch, d, seed=2)
+    whole = kq.layernorm(x, w, b, eps=EPS, stats=True)
+    part = kq.layernorm(x[cut:], w, b, eps=EPS, stats=True)
+    assert all(torch.equal(a[cut:], c) for a, c in zip(whole, part))
+    y, mean, rstd = whole
+    y0, mu, rs, y_tol, _, _ = ref.norm(x[-600:], w, b, EPS)
+    ref.assert_near(y[-600:], y0, y_tol, "y")
+    codes, scales, _, _ = kq.layernorm_quantize_mxfp4(x, w, b, eps=EPS, stats=True)
+    c2, s2 = kq.layernorm_quantize_mxfp4(x[cut:], w, b, eps=EPS)
+    assert torch.equal(codes[cut:], c2) and torch.equal(scales[cut:], s2)
+    dx = kq.layernorm_backward(y, x, mean, rstd, w, params=False)[0]
+    want, tol = ref.norm_grad(y[-600:], x[-600:], mean[-600:], rstd[-600:], w)
+    ref.assert_near(dx[-600:], want[0], tol[0], "dx")
