@@ -10,7 +10,7 @@
 // and no cancellation for negative z. Error of s for negative z, relative: the exponent's roundings
 // are multiplied by the exponent, so (1.3 |z| + 5) 2^-24 in silu and (6 w + 5) 2^-24 in gelu_tanh,
 // w = 2 |u| (20 2^-24 for silu at z = -12 and 300 for gelu_tanh at -8, where s is 6e-6 and 4e-22);
-// 5 2^-24 and less for positive z. Absolute, at most 8 2^-24 |z| of the value.
+// 6 2^-24 and less for positive z. Absolute, at most 8 2^-24 |z| of the value.
 //
 // P, the normal distribution function, is 1 - tail(|z|) or, for negative z, tail(|z|) itself:
 //   tail(a) = erfc(a / sqrt 2) / 2 = exp(-a^2 / 2) R(a),
