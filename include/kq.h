@@ -35,8 +35,8 @@
  *     owns and keeps alive until the enqueued work has finished. The library
  *     allocates nothing and never synchronizes; the only state it keeps
  *     between calls is a per-device cache of the compute-unit count (read once
- *     with hipDeviceGetAttribute by the packed GEMMs, kq_mxfp4_linear and the
- *     layer norm's entry points to size their launches).
+ *     with hipDeviceGetAttribute by the packed GEMMs, kq_mxfp4_linear, the
+ *     layer norm's, the heads' and the cache's entry points to size their launches).
  *   - Work is enqueued on `stream` (NULL = the default stream) and runs
  *     asynchronously; results are valid once the stream has reached it.
  *   - Arguments are checked on the host before anything is enqueued; on an
@@ -45,15 +45,15 @@
  *     hipError_t value (per host thread).
  *   - With m == 0 (or d == 0) nothing is read, written or launched and KQ_OK
  *     is returned (but the gradients summed over no rows are set to zeros:
- *     kq_layernorm_backward, kq_mxfp4_linear_backward).
+ *     kq_layernorm_backward, kq_mxfp4_linear_backward, kq_headnorm_rope_backward).
  *   - Inputs must be finite; NaN or Inf inputs give unspecified codes
  *     (kq_layernorm says what they make of its outputs).
  *   - Outputs must not overlap inputs (but kq_mxfp4_linear's residual may be
- *     its output).
+ *     its output, and kq_headnorm_rope and its backward may work in place).
  *   - The GEMM-family entry points (kq_mxfp4_gemm*, kq_lowrank_project*,
  *     kq_dequantize_mxfp4_bf16, kq_pack_mxfp4_scales, kq_gemm_f32,
- *     kq_transform_quantize_mxfp4_gemm, kq_mxfp4_linear*) and the layer norm's
- *     refuse any size or leading dimension of 2^31 or more with
+ *     kq_transform_quantize_mxfp4_gemm, kq_mxfp4_linear*), the layer norm's,
+ *     the heads' and the cache's refuse any size or leading dimension of 2^31 or more with
  *     KQ_ERR_UNSUPPORTED, before their finer limits.
  */
 #ifndef KQ_H
@@ -655,6 +655,129 @@ kq_status kq_mxfp4_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t
 kq_status kq_mxfp4_linear_backward(const void *dO, int64_t lddo, const void *Z, int64_t ldz, int type, int64_t m,
                                    int64_t n, int act, void *dZ, int64_t lddz, float *dbias, void *workspace,
                                    int64_t workspace_bytes, kq_stream_t stream);
+
+/*
+ * Position rotation of a head: pair i < rot / 2 of its first `rot` channels turns by
+ * t = p freq[i], p the token's position,
+ *   (a, b) -> amplitude (a cos t - b sin t, b cos t + a sin t);
+ * the other channels are left as they are. The angle is reduced in fp64 (p freq[i] is off
+ * by 2^-52 of itself), sine and cosine are taken in fp32. Read by the host during the call.
+ *   positions    device, int64 [m][axes], 8-byte aligned, any values
+ *   freq         device, fp64 [rot / 2], radians per position (kq_rope_frequencies; an fp32
+ *                table converts exactly)
+ *   rot          even, 0 <= rot <= d; with 0 the other members are not read
+ *   interleaved  0: pairs (i, i + rot / 2); else pairs (2 i, 2 i + 1)
+ *   amplitude    of the rotated channels (1, or what a scaling for long contexts asks for)
+ *   axes         1 .. 4 coordinates of a position; the first axis_pairs[0] pairs turn with
+ *                the first, the next axis_pairs[1] with the second .. (their sum is rot / 2)
+ */
+typedef struct {
+    const int64_t *positions;
+    const double *freq;
+    int64_t rot;
+    int interleaved;
+    float amplitude;
+    int axes;
+    int64_t axis_pairs[4];
+} kq_rope;
+
+/*
+ * Host-only: the frequencies of a rotation of `rot` channels, freq[i] = base^(-2 i / rot),
+ * i < rot / 2, scaled for contexts longer than those of training:
+ *   KQ_ROPE_PLAIN   as they are
+ *   KQ_ROPE_LINEAR  freq[i] / factor (positions interpolated)
+ *   KQ_ROPE_BASE    base factor^(rot / (rot - 2)) in the place of base: the lowest frequency
+ *                   is divided by factor, the highest stays (rot <= 2: as they are)
+ *   KQ_ROPE_PARTS   with turns = original freq[i] / (2 pi) in the `original` positions of
+ *                   training and g = (turns - low) / (high - low) held to [0, 1]:
+ *                   g freq[i] + (1 - g) freq[i] / factor ("NTK-by-parts", arXiv 2309.00071)
+ *   freq  host, fp64 [rot / 2]
+ * rot < 0 or odd, base, factor or original not positive and finite, low >= high:
+ * KQ_ERR_SHAPE; an unknown scaling: KQ_ERR_UNSUPPORTED. Arguments that a scaling does not
+ * name are not read.
+ */
+typedef enum { KQ_ROPE_PLAIN = 0, KQ_ROPE_LINEAR = 1, KQ_ROPE_BASE = 2, KQ_ROPE_PARTS = 3 } kq_rope_scaling;
+kq_status kq_rope_frequencies(int64_t rot, double base, int scaling, double factor, double original, double low,
+                              double high, double *freq);
+
+/*
+ * Norm of every head of queries and keys with the rotation in the same pass: for head x of
+ * d channels,
+ *   n_c = x_c w_c / sqrt(sum_c x_c^2 / d + eps), then the rotation above,
+ * in fp32, rounded once to Y's type. Heads h < q_heads take weight_q, the others weight_k, so
+ * the query and key heads of a product's output are one call.
+ *   X, Y       device, `type` (a kq_type) [m][heads][d]: token i's head h at i ldx + h hsx
+ *              elements (the strides of a single token or head are not read), channels side
+ *              by side; element aligned. Strides of X may be anything from 0 on, heads of Y
+ *              must not overlap (KQ_ERR_SHAPE). Y may be X with its strides. Channels are
+ *              moved 8 or 4 at a time where d, the rotated part (its half, unless interleaved),
+ *              addresses and strides are multiples of that, else one by one (slower).
+ *   norm       0: the rotation alone (weights and eps are not used)
+ *   weight_q, weight_k  device, fp32 [d], or NULL (1)
+ *   eps        >= 0 and finite (KQ_ERR_SHAPE)
+ *   rope       host, or NULL (no rotation)
+ * 1 <= d <= 1024 and heads <= 65536 (KQ_ERR_UNSUPPORTED above). A NaN or an infinity makes its
+ * own head NaN or infinite and no other. Range: a head's sum of squares finite in fp32 (beyond it its
+ * outputs are 0 or NaN) and its mean plus eps at least 2^-126 (below it NaN or infinite).
+ */
+kq_status kq_headnorm_rope(const void *X, int type, int64_t m, int64_t heads, int64_t d, int64_t ldx, int64_t hsx,
+                           int norm, const float *weight_q, const float *weight_k, int64_t q_heads, float eps,
+                           const kq_rope *rope, void *Y, int64_t ldy, int64_t hsy, kq_stream_t stream);
+
+/*
+ * The gradients of kq_headnorm_rope for the gradient dY of its output: with e = dY turned by
+ * the opposite angles (times the amplitude), s = 1 / sqrt(sum x^2 / d + eps), h = x s, g = e w,
+ *   dx = s (g - h sum_c g_c h_c / d),  dweight_c = sum of e_c h_c
+ * over the tokens and the heads that use that weight, in fp32 in a fixed order (the same bits
+ * on every call). With norm 0: dx = e, and X is not read.
+ *   dY, X, dX             as kq_headnorm_rope's X, X and Y (dX may be dY or X with its strides)
+ *   dweight_q, dweight_k  device, fp32 [d], or NULL (not wanted; KQ_ERR_SHAPE with norm 0);
+ *                         written, not added to; zeros where no head uses that weight
+ *   workspace             device, 16-byte aligned, at least
+ *                         kq_headnorm_rope_backward_workspace_bytes(m, d) bytes (KQ_ERR_SHAPE
+ *                         when less); may be NULL when that is 0 or no dweight is wanted. Calls
+ *                         that may overlap need one each.
+ * With m == 0 or heads == 0 and d > 0 the dweights are set to zeros.
+ */
+kq_status kq_headnorm_rope_backward_workspace_bytes(int64_t m, int64_t d, int64_t *bytes);
+kq_status kq_headnorm_rope_backward(const void *dY, int64_t lddy, int64_t hsdy, const void *X, int64_t ldx, int64_t hsx,
+                                    int type, int64_t m, int64_t heads, int64_t d, int norm, const float *weight_q,
+                                    const float *weight_k, int64_t q_heads, float eps, const kq_rope *rope, void *dX,
+                                    int64_t lddx, int64_t hsdx, float *dweight_q, float *dweight_k, void *workspace,
+                                    int64_t workspace_bytes, kq_stream_t stream);
+
+/*
+ * A cache of keys and values in MXFP4, quantized as it is written. It has `cache_slots` slots
+ * (pages of P tokens: slot = P page + place), each with the heads of one token:
+ *   codes   device, [cache_slots][heads][d/2] bytes, 4-byte aligned
+ *   scales  device, [cache_slots][heads][d/32]
+ * kq_cache_write_mxfp4 puts token i's heads into slot slots[i]: key heads after norm, weight
+ * and rotation as kq_headnorm_rope's (quantized from fp32, not rounded in between), value heads
+ * as they are.
+ *   K, V          device, `type` [m][k_heads][d], [m][v_heads][d], strides as kq_headnorm_rope's
+ *                 X; a tensor of no heads is not read
+ *   norm, weight, eps, rope  of the keys, as kq_headnorm_rope's
+ *   slots         device, int64 [m], 8-byte aligned. A token whose slot is negative or no less
+ *                 than cache_slots is left out (padding); no other slot is written to. Two
+ *                 tokens of a call must not share a slot (that slot would hold a mixture).
+ * d % 32 == 0 (KQ_ERR_SHAPE), d <= 1024, k_heads + v_heads <= 65536 (KQ_ERR_UNSUPPORTED). The
+ * inputs' range is kq_headnorm_rope's and the quantizers'.
+ */
+kq_status kq_cache_write_mxfp4(const void *K, int64_t ldk, int64_t hsk, int64_t k_heads, const void *V, int64_t ldv,
+                               int64_t hsv, int64_t v_heads, int type, int64_t m, int64_t d, int norm,
+                               const float *weight, float eps, const kq_rope *rope, const int64_t *slots,
+                               int64_t cache_slots, uint8_t *codes_k, uint8_t *scales_k, uint8_t *codes_v,
+                               uint8_t *scales_v, kq_stream_t stream);
+
+/*
+ * Reads slots of such a cache (its keys or its values) back: Y[i][h] = deq(codes, scales) of
+ * slot slots[i], exact in either type (as kq_dequantize_mxfp4_bf16); zeros for a slot that is
+ * negative or no less than cache_slots. A slot may be named any number of times.
+ *   Y  device, `type` [m][heads][d], strides as kq_headnorm_rope's Y
+ */
+kq_status kq_cache_read_mxfp4(const int64_t *slots, int64_t m, const uint8_t *codes, const uint8_t *scales,
+                              int64_t cache_slots, int64_t heads, int64_t d, int type, void *Y, int64_t ldy, int64_t hsy,
+                              kq_stream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *kq_status_string(kq_status s);

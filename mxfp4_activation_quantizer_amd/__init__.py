@@ -57,6 +57,12 @@ EXPORTS = (
     "kq_mxfp4_linear",
     "kq_mxfp4_linear_backward_workspace_bytes",
     "kq_mxfp4_linear_backward",
+    "kq_rope_frequencies",
+    "kq_headnorm_rope",
+    "kq_headnorm_rope_backward_workspace_bytes",
+    "kq_headnorm_rope_backward",
+    "kq_cache_write_mxfp4",
+    "kq_cache_read_mxfp4",
     "kq_status_string",
     "kq_last_hip_error",
     "kq_factors_from_lu",
@@ -81,7 +87,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError("libkq.so is not built: run `python -m mxfp4_activation_quantizer_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
-        p, i64, st = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+        p, i64, st, f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
         for name, args in {
             "kq_quantize_mxfp4": [p, i64, i64, i64, p, p, p],
             "kq_transform_quantize_mxfp4": [p, i64, i64, i64, p, p, p, p, p],
@@ -122,6 +128,14 @@ def lib():
             "kq_mxfp4_linear": [p, p, p, p, st, i64, i64, i64, p, st, st, p, i64, p, i64, p, i64, p],
             "kq_mxfp4_linear_backward_workspace_bytes": [i64, i64, p],
             "kq_mxfp4_linear_backward": [p, i64, p, i64, st, i64, i64, st, p, i64, p, p, i64, p],
+            "kq_rope_frequencies": [i64, f64, st, f64, f64, f64, f64, p],
+            "kq_headnorm_rope": [p, st, i64, i64, i64, i64, i64, st, p, p, i64, ctypes.c_float, p, p, i64, i64, p],
+            "kq_headnorm_rope_backward_workspace_bytes": [i64, i64, p],
+            "kq_headnorm_rope_backward": [p, i64, i64, p, i64, i64, st, i64, i64, i64, st, p, p, i64, ctypes.c_float,
+                                          p, p, i64, i64, p, p, p, i64, p],
+            "kq_cache_write_mxfp4": [p, i64, i64, i64, p, i64, i64, i64, st, i64, i64, st, p, ctypes.c_float, p, p,
+                                     i64, p, p, p, p, p],
+            "kq_cache_read_mxfp4": [p, i64, p, p, i64, i64, i64, st, p, i64, i64, p],
         }.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -1075,6 +1089,240 @@ def mxfp4_linear_backward(dout, z=None, act="none", dz=None, dbias=None, workspa
                                           m, n, ACTS[act], dz.data_ptr(), lddz, _vector(dbias, "dbias", n, index),
                                           ws.data_ptr(), ws_bytes, _current_stream(index)))
     return dz, dbias
+
+
+# ---------------------------------------------------------------------------
+# Queries, keys and values: norm and rotation of heads, the MXFP4 cache
+# ---------------------------------------------------------------------------
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}  # kq_rope_scaling
+
+
+class _Rope(ctypes.Structure):  # kq_rope
+    _fields_ = [("positions", ctypes.c_void_p), ("freq", ctypes.c_void_p), ("rot", ctypes.c_int64),
+                ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float), ("axes", ctypes.c_int),
+                ("axis_pairs", ctypes.c_int64 * 4)]
+
+
+def rope_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, original=0.0, low=1.0, high=32.0):
+    """Host helper: the frequencies (radians per position, float64 [rot / 2]) of a rotation of ``rot``
+    channels, base^(-2 i / rot), scaled for contexts longer than those of training (kq_rope_frequencies): "linear"
+    divides them by factor, "base" stretches the base so that the lowest is, "parts" divides those of
+    fewer than ``low`` turns in ``original`` positions, keeps those of more than ``high`` and blends between."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+    out = np.empty(max(0, rot // 2), dtype=np.float64)
+    _check("kq_rope_frequencies",
+           lib().kq_rope_frequencies(rot, base, ROPE_SCALINGS[scaling], factor, original, low, high,
+                                     ctypes.c_void_p(out.ctypes.data)))
+    return out
+
+
+def _rope(positions, freq, m, index, interleaved, amplitude, axis_pairs):
+    """kq_rope of the rotation's arguments on device ``index``, by reference (freq None: NULL)."""
+    if freq is None:
+        return None
+    torch = _torch()
+    if not isinstance(freq, torch.Tensor) or freq.dtype is not torch.float64 or freq.dim() != 1 or not freq.is_contiguous():
+        raise TypeError("freq must be a contiguous float64 vector")
+    if positions is None or positions.dtype is not torch.int64 or not positions.is_contiguous():
+        raise TypeError("positions must be a contiguous int64 tensor")
+    if freq.get_device() != index or positions.get_device() != index:
+        raise ValueError("positions and freq must be on device %d" % index)
+    shape = positions.shape
+    axes = 1 if len(shape) == 1 else shape[1] if len(shape) == 2 else 0
+    if len(shape) == 0 or shape[0] != m or not 1 <= axes <= 4:
+        raise ValueError("positions has shape %s, expected [%d] or [%d][1 to 4 axes]" % (tuple(shape), m, m))
+    n = freq.shape[0]
+    pairs = tuple(axis_pairs) if axis_pairs is not None else (n,)
+    if len(pairs) != axes:
+        raise ValueError("axis_pairs must name the pairs of each of the %d axes" % axes)
+    return ctypes.byref(_Rope(positions.data_ptr(), freq.data_ptr(), 2 * n, 1 if interleaved else 0, amplitude, axes,
+                              pairs))
+
+
+def _heads(t, name, dtype, index, shape=None):
+    """t's token and head strides: a [tokens][heads][channels] tensor of dtype on device ``index`` with
+    unit channel stride. The stride of a single token or head does not matter."""
+    if t.dtype is not dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected device %d" % (name, t.device, index))
+    got = t.shape
+    if len(got) != 3 or (shape is not None and got != shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(got), "[tokens][heads][channels]"
+                                                            if shape is None else tuple(shape)))
+    ld, hs, c = t.stride()
+    if c != 1 and got[2] > 1:
+        raise ValueError("%s must have unit channel stride" % name)
+    return ld if got[0] > 1 else got[1] * got[2], hs if got[1] > 1 else got[2]
+
+
+def headnorm_rope(x, positions=None, freq=None, weight_q=None, weight_k=None, q_heads=None, norm=True, eps=1e-6,
+                  interleaved=False, amplitude=1.0, axis_pairs=None, out=None, stream=None):
+    """The norm of each head of x (bf16 or fp32 [m][heads][d], a view of a product's output say) and the rotation
+    of its position, in x's type: x w / sqrt(mean(x^2) + eps), then the first 2 len(freq) channels turned
+    by positions freq.
+
+    weight_q: fp32 [d], of the first ``q_heads`` heads (None: all); weight_k: of the others; None: 1.
+    ``norm=False``: the rotation alone. positions: int64 [m] or [m][axes]; freq: float64, one per
+    pair (rope_frequencies; None: no rotation); axis_pairs: how many pairs turn with each axis. Pairs are
+    (i, i + len(freq)), or (2 i, 2 i + 1) with ``interleaved``; amplitude multiplies the rotated
+    channels. out: [m][heads][d] of any strides (x itself: in place).
+    """
+    bf16, index = _activation(x, "x")
+    here = _elsewhere(index, stream)
+    if here is not None:
+        with here:
+            return headnorm_rope(x, positions, freq, weight_q, weight_k, q_heads, norm, eps, interleaved, amplitude,
+                                 axis_pairs, out)
+    ldx, hsx = _heads(x, "x", x.dtype, index)
+    m, heads, d = x.shape
+    if out is None:
+        out, ldy, hsy = x.new_empty((m, heads, d)), heads * d, d
+    else:
+        ldy, hsy = _heads(out, "out", x.dtype, index, x.shape)
+    _check("kq_headnorm_rope",
+           lib().kq_headnorm_rope(x.data_ptr(), int(bf16), m, heads, d, ldx, hsx, 1 if norm else 0,
+                                  _vector(weight_q, "weight_q", d, index), _vector(weight_k, "weight_k", d, index),
+                                  heads if q_heads is None else q_heads, eps,
+                                  _rope(positions, freq, m, index, interleaved, amplitude, axis_pairs),
+                                  out.data_ptr(), ldy, hsy, _current_stream(index)))
+    return out
+
+
+def headnorm_rope_backward(dy, x=None, positions=None, freq=None, weight_q=None, weight_k=None, q_heads=None,
+                           norm=True, eps=1e-6, interleaved=False, amplitude=1.0, axis_pairs=None, dx=None,
+                           dweight_q=None, dweight_k=None, params=True, workspace=None, stream=None):
+    """Gradients of headnorm_rope for its output's gradient dy (x's type and shape): (dx, dweight_q, dweight_k).
+
+    ``params=False`` (or ``norm=False``, where x is not needed) computes dx alone, with None for the
+    others. workspace: at least kq_headnorm_rope_backward_workspace_bytes bytes, or None
+    (allocated for this call). The rest as headnorm_rope.
+    """
+    torch = _torch()
+    bf16, index = _activation(dy, "dy")
+    here = _elsewhere(index, stream)
+    if here is not None:
+        with here:
+            return headnorm_rope_backward(dy, x, positions, freq, weight_q, weight_k, q_heads, norm, eps, interleaved,
+                                          amplitude, axis_pairs, dx, dweight_q, dweight_k, params, workspace)
+    lddy, hsdy = _heads(dy, "dy", dy.dtype, index)
+    m, heads, d = dy.shape
+    ldx = hsx = 0
+    if norm:
+        if x is None:
+            raise ValueError("x is required with norm=True")
+        ldx, hsx = _heads(x, "x", dy.dtype, index, dy.shape)
+    if dx is None:
+        dx, lddx, hsdx = dy.new_empty((m, heads, d)), heads * d, d
+    else:
+        lddx, hsdx = _heads(dx, "dx", dy.dtype, index, dy.shape)
+    ws, ws_bytes = None, 0
+    if params and norm:
+        if dweight_q is None:
+            dweight_q = dy.new_empty(d, dtype=torch.float32)
+        if dweight_k is None:
+            dweight_k = dy.new_empty(d, dtype=torch.float32)
+        ws, ws_bytes = _workspace("kq_headnorm_rope_backward_workspace_bytes", m, d, workspace, dy)
+    elif dweight_q is not None or dweight_k is not None:
+        raise ValueError("params=False and norm=False compute no dweight")
+    _check("kq_headnorm_rope_backward",
+           lib().kq_headnorm_rope_backward(dy.data_ptr(), lddy, hsdy, x.data_ptr() if norm else None, ldx, hsx,
+                                           int(bf16), m, heads, d, 1 if norm else 0,
+                                           _vector(weight_q, "weight_q", d, index),
+                                           _vector(weight_k, "weight_k", d, index),
+                                           heads if q_heads is None else q_heads, eps,
+                                           _rope(positions, freq, m, index, interleaved, amplitude, axis_pairs),
+                                           dx.data_ptr(), lddx, hsdx, _vector(dweight_q, "dweight_q", d, index),
+                                           _vector(dweight_k, "dweight_k", d, index),
+                                           ws.data_ptr() if ws is not None else None, ws_bytes,
+                                           _current_stream(index)))
+    return dx, dweight_q, dweight_k
+
+
+def _slots(t, index):
+    """Pointer of the int64 slot list t on device ``index``."""
+    if t.dtype is not _torch().int64 or t.dim() != 1 or not t.is_contiguous():
+        raise TypeError("slots must be a contiguous int64 vector")
+    if t.get_device() != index:
+        raise ValueError("slots is on %s, expected device %d" % (t.device, index))
+    return t.data_ptr()
+
+
+def _cache(codes, scales, name, heads, d, index, slots=None):
+    """(slots, codes pointer, scales pointer) of one half of a cache."""
+    n = codes.shape[0]
+    if tuple(codes.shape) != (n, heads, d // 2) or tuple(scales.shape) != (n, heads, d // 32) or slots not in (None, n):
+        raise ValueError("codes%s and scales%s have shapes %s and %s, expected [slots][%d][%d] and [slots][%d][%d]" % (
+            name, name, tuple(codes.shape), tuple(scales.shape), heads, d // 2, heads, d // 32))
+    return (n, _bytes(codes, "codes" + name, n * heads, d // 2, index),
+            _bytes(scales, "scales" + name, n * heads, d // 32, index))
+
+
+def cache_write_mxfp4(slots, k=None, codes_k=None, scales_k=None, v=None, codes_v=None, scales_v=None,
+                      norm=False, weight=None, eps=1e-6, positions=None, freq=None, interleaved=False, amplitude=1.0,
+                      axis_pairs=None, stream=None):
+    """Quantizes keys and values (bf16 or fp32 [m][heads][d]; either may be None) into their cache of MXFP4: codes
+    uint8 [slots][heads][d/2] and scales uint8 [slots][heads][d/32]. Token i goes to slot slots[i] (int64 [m]);
+    one that is negative or past the cache is left out. Keys are normed (``norm``, with weight) and rotated
+    first, as by headnorm_rope, without a rounding in between; values go in as they are.
+    """
+    one = k if k is not None else v
+    if one is None:
+        raise ValueError("keys or values are required")
+    bf16, index = _activation(one, "k" if k is not None else "v")
+    here = _elsewhere(index, stream)
+    if here is not None:
+        with here:
+            return cache_write_mxfp4(slots, k, codes_k, scales_k, v, codes_v, scales_v, norm, weight, eps, positions,
+                                     freq, interleaved, amplitude, axis_pairs)
+    m, _, d = one.shape if one.dim() == 3 else (0, 0, 0)
+    n, parts = None, []
+    for t, codes, scales, name in ((k, codes_k, scales_k, "_k"), (v, codes_v, scales_v, "_v")):
+        if t is None:
+            parts.append((None, 0, 0, 0, None, None))
+            continue
+        ld, hs = _heads(t, name[1:], one.dtype, index)
+        heads = t.shape[1]
+        if t.shape[0] != m or t.shape[2] != d:
+            raise ValueError("k and v must have the same tokens and channels, got %s and %s" % (tuple(k.shape), tuple(v.shape)))
+        n, cp, sp = _cache(codes, scales, name, heads, d, index, n)
+        parts.append((t.data_ptr(), ld, hs, heads, cp, sp))
+    (kp, ldk, hsk, kh, ckp, skp), (vp, ldv, hsv, vh, cvp, svp) = parts
+    if slots.numel() != m:
+        raise ValueError("slots has %d entries, expected %d" % (slots.numel(), m))
+    _check("kq_cache_write_mxfp4",
+           lib().kq_cache_write_mxfp4(kp, ldk, hsk, kh, vp, ldv, hsv, vh, int(bf16), m, d, 1 if norm else 0,
+                                      _vector(weight, "weight", d, index), eps,
+                                      _rope(positions, freq, m, index, interleaved, amplitude, axis_pairs),
+                                      _slots(slots, index), n, ckp, skp, cvp, svp, _current_stream(index)))
+
+
+def cache_read_mxfp4(slots, codes, scales, bf16=True, out=None, stream=None):
+    """The rows slots[i] (int64 [m]) of a cache of keys or of values (codes uint8 [slots][heads][d/2], scales uint8
+    [slots][heads][d/32]) decoded, bf16 (or fp32) [m][heads][d], exactly. A slot that is negative or past the
+    cache reads as zeros. out: [m][heads][d] of any strides.
+    """
+    torch = _torch()
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dim() != 3:
+        raise TypeError("codes must be a CUDA (HIP) tensor [slots][heads][d/2]")
+    index = codes.get_device()
+    here = _elsewhere(index, stream)
+    if here is not None:
+        with here:
+            return cache_read_mxfp4(slots, codes, scales, bf16, out)
+    heads, d = codes.shape[1], 2 * codes.shape[2]
+    n, cp, sp = _cache(codes, scales, "", heads, d, index)
+    dtype = torch.bfloat16 if bf16 else torch.float32
+    m = slots.numel()
+    if out is None:
+        out, ldy, hsy = codes.new_empty((m, heads, d), dtype=dtype), heads * d, d
+    else:
+        ldy, hsy = _heads(out, "out", dtype, index, (m, heads, d))
+    _check("kq_cache_read_mxfp4",
+           lib().kq_cache_read_mxfp4(_slots(slots, index), m, cp, sp, n, heads, d, 1 if bf16 else 0, out.data_ptr(),
+                                     ldy, hsy, _current_stream(index)))
+    return out
 
 
 def factors_from_lu(abc):
