@@ -35,7 +35,7 @@
  *     owns and keeps alive until the enqueued work has finished. The library
  *     allocates nothing and never synchronizes; the only state it keeps
  *     between calls is a per-device cache of the compute-unit count (read once
- *     with hipDeviceGetAttribute by the packed GEMMs, kq_mxfp4_linear, the
+ *     with hipDeviceGetAttribute by the packed GEMMs, kq_mxfp4_linear, kq_mxfp4_gated_linear, the
  *     layer norm's, the heads' and the cache's entry points to size their launches).
  *   - Work is enqueued on `stream` (NULL = the default stream) and runs
  *     asynchronously; results are valid once the stream has reached it.
@@ -45,14 +45,14 @@
  *     hipError_t value (per host thread).
  *   - With m == 0 (or d == 0) nothing is read, written or launched and KQ_OK
  *     is returned (but the gradients summed over no rows are set to zeros:
- *     kq_layernorm_backward, kq_mxfp4_linear_backward, kq_headnorm_rope_backward).
+ *     the *_backward entry points).
  *   - Inputs must be finite; NaN or Inf inputs give unspecified codes
  *     (kq_layernorm says what they make of its outputs).
  *   - Outputs must not overlap inputs (but kq_mxfp4_linear's residual may be
  *     its output, and kq_headnorm_rope and its backward may work in place).
  *   - The GEMM-family entry points (kq_mxfp4_gemm*, kq_lowrank_project*,
  *     kq_dequantize_mxfp4_bf16, kq_pack_mxfp4_scales, kq_gemm_f32,
- *     kq_transform_quantize_mxfp4_gemm, kq_mxfp4_linear*), the layer norm's,
+ *     kq_transform_quantize_mxfp4_gemm, kq_mxfp4_linear*, kq_mxfp4_gated_linear*), the layer norm's,
  *     the heads' and the cache's refuse any size or leading dimension of 2^31 or more with
  *     KQ_ERR_UNSUPPORTED, before their finer limits.
  */
@@ -655,6 +655,44 @@ kq_status kq_mxfp4_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t
 kq_status kq_mxfp4_linear_backward(const void *dO, int64_t lddo, const void *Z, int64_t ldz, int type, int64_t m,
                                    int64_t n, int act, void *dZ, int64_t lddz, float *dbias, void *workspace,
                                    int64_t workspace_bytes, kq_stream_t stream);
+
+/*
+ * Two W4A4 products of the same A with the gate of a feed-forward block in their epilogue:
+ *   g = deq(A) deq(Wg)^T + bias_g,  u = deq(A) deq(Wu)^T + bias_u,  O = act(g) u,
+ * fp32 up to one rounding of each output to its type (nearest, ties to even).
+ *   codes_a, scales_a, packed, m, n, k  as kq_mxfp4_linear
+ *   codes_g .. scales_u   the two weights, each [n][k/2] and its scales, laid out as
+ *                         kq_mxfp4_linear's W (a fused weight's two halves, say, each packed by itself)
+ *   bias_g, bias_u        device, fp32 [n], or NULL (0)
+ *   act                   a kq_act value of g (KQ_ACT_SILU, KQ_ACT_GELU .. ; NONE: a bilinear gate)
+ *   type                  type of O, G and U (a kq_type)
+ *   O                     device, `type` [m][ldo], ldo >= n; element aligned, written
+ *   G, U                  device, `type` [m][ldg], [m][ldu] (>= n), or NULL: receive g and u
+ *                         (what kq_mxfp4_gated_linear_backward reads)
+ * Any m, n >= 0; limits, alignment and the choice of the kernel by the sizes as kq_mxfp4_linear's.
+ */
+kq_status kq_mxfp4_gated_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_g,
+                                const uint8_t *scales_g, const uint8_t *codes_u, const uint8_t *scales_u, int packed,
+                                int64_t m, int64_t n, int64_t k, const float *bias_g, const float *bias_u, int act,
+                                int type, void *O, int64_t ldo, void *G, int64_t ldg, void *U, int64_t ldu,
+                                kq_stream_t stream);
+
+/*
+ * The gradients of that epilogue for the gradient dO of its output:
+ *   dG = dO u act'(g),  dU = dO act(g),  dbias_g, dbias_u = their sums over the rows
+ * (before their rounding; fp32, fixed order). The operands' follow from dG and dU (straight
+ * through the quantizer): dA = dG deq(Wg) + dU deq(Wu), dWg = dG^T deq(A), dWu = dU^T deq(A).
+ *   dO, G, U, dG, dU  device, `type` [m][ld] (ld >= n), element aligned; dG, dU NULL when not
+ *                     wanted. dG may be dO, G or U with its stride, and dU likewise, but not both one.
+ *   dbias_g, dbias_u  device, fp32 [n], or NULL; written, not added to
+ *   workspace         as kq_layernorm_backward, kq_mxfp4_gated_linear_backward_workspace_bytes(m, n)
+ * With m == 0 and n > 0 the dbiases are set to zeros.
+ */
+kq_status kq_mxfp4_gated_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t *bytes);
+kq_status kq_mxfp4_gated_linear_backward(const void *dO, int64_t lddo, const void *G, int64_t ldg, const void *U,
+                                         int64_t ldu, int type, int64_t m, int64_t n, int act, void *dG, int64_t lddg,
+                                         void *dU, int64_t lddu, float *dbias_g, float *dbias_u, void *workspace,
+                                         int64_t workspace_bytes, kq_stream_t stream);
 
 /*
  * Position rotation of a head: pair i < rot / 2 of its first `rot` channels turns by

@@ -57,6 +57,9 @@ EXPORTS = (
     "kq_mxfp4_linear",
     "kq_mxfp4_linear_backward_workspace_bytes",
     "kq_mxfp4_linear_backward",
+    "kq_mxfp4_gated_linear",
+    "kq_mxfp4_gated_linear_backward_workspace_bytes",
+    "kq_mxfp4_gated_linear_backward",
     "kq_rope_frequencies",
     "kq_headnorm_rope",
     "kq_headnorm_rope_backward_workspace_bytes",
@@ -128,6 +131,9 @@ def lib():
             "kq_mxfp4_linear": [p, p, p, p, st, i64, i64, i64, p, st, st, p, i64, p, i64, p, i64, p],
             "kq_mxfp4_linear_backward_workspace_bytes": [i64, i64, p],
             "kq_mxfp4_linear_backward": [p, i64, p, i64, st, i64, i64, st, p, i64, p, p, i64, p],
+            "kq_mxfp4_gated_linear": [p, p, p, p, p, p, st, i64, i64, i64, p, p, st, st, p, i64, p, i64, p, i64, p],
+            "kq_mxfp4_gated_linear_backward_workspace_bytes": [i64, i64, p],
+            "kq_mxfp4_gated_linear_backward": [p, i64, p, i64, p, i64, st, i64, i64, st, p, i64, p, i64, p, p, p, i64, p],
             "kq_rope_frequencies": [i64, f64, st, f64, f64, f64, f64, p],
             "kq_headnorm_rope": [p, st, i64, i64, i64, i64, i64, st, p, p, i64, ctypes.c_float, p, p, i64, i64, p],
             "kq_headnorm_rope_backward_workspace_bytes": [i64, i64, p],
@@ -1089,6 +1095,107 @@ def mxfp4_linear_backward(dout, z=None, act="none", dz=None, dbias=None, workspa
                                           m, n, ACTS[act], dz.data_ptr(), lddz, _vector(dbias, "dbias", n, index),
                                           ws.data_ptr(), ws_bytes, _current_stream(index)))
     return dz, dbias
+
+
+def mxfp4_gated_linear(codes_a, scales_a, codes_g, scales_g, codes_u, scales_u, bias_g=None, bias_u=None, act="silu",
+                       out=None, g=None, u=None, bf16=True, packed=False, want_pre=False, stream=None):
+    """act(deq(A) deq(Wg)^T + bias_g) * (deq(A) deq(Wu)^T + bias_u) from MXFP4 operands, bf16 (or fp32) [m][n]: both
+    projections of a gated feed-forward block in one kernel.
+
+    Operands, ``packed`` and act as mxfp4_linear; bias_g, bias_u: fp32 [n]; out, g, u: [m][n] of the output's
+    type. ``want_pre=True`` (or g or u given) also returns the two products, (out, g, u), what
+    mxfp4_gated_linear_backward takes.
+    """
+    torch = _torch()
+    if not isinstance(codes_a, torch.Tensor) or not codes_a.is_cuda or codes_a.dtype is not torch.uint8:
+        raise TypeError("codes_a must be a uint8 CUDA (HIP) tensor")
+    index = codes_a.get_device()
+    here = _elsewhere(index, stream)
+    if here is not None:
+        with here:
+            return mxfp4_gated_linear(codes_a, scales_a, codes_g, scales_g, codes_u, scales_u, bias_g, bias_u, act, out,
+                                      g, u, bf16, packed, want_pre)
+    if act not in ACTS:
+        raise ValueError("act must be one of %s" % ", ".join(ACTS))
+    sa, sg, su = codes_a.shape, codes_g.shape, codes_u.shape
+    if len(sa) != 2 or len(sg) != 2 or sg != su or sa[1] != sg[1]:
+        raise ValueError("codes_a must be [m][k/2] and codes_g, codes_u [n][k/2], got %s, %s and %s" % (
+            tuple(sa), tuple(sg), tuple(su)))
+    m, kb = sa
+    n, k = sg[0], 2 * kb
+    dtype = torch.bfloat16 if bf16 else torch.float32
+    if out is None:
+        out, ldo = codes_a.new_empty((m, n), dtype=dtype), n
+    else:
+        ldo = _matrix(out, "out", dtype, index, m, n)
+    gp = up = None
+    ldg = ldu = 0
+    want_pre = want_pre or g is not None or u is not None
+    if want_pre:
+        if g is None:
+            g = codes_a.new_empty((m, n), dtype=dtype)
+        if u is None:
+            u = codes_a.new_empty((m, n), dtype=dtype)
+        ldg, ldu = _matrix(g, "g", dtype, index, m, n), _matrix(u, "u", dtype, index, m, n)
+        gp, up = g.data_ptr(), u.data_ptr()
+    _check("kq_mxfp4_gated_linear",
+           lib().kq_mxfp4_gated_linear(_bytes(codes_a, "codes_a", m, kb, index),
+                                       _packed_scales(scales_a, "scales_a", m, k, index, packed),
+                                       _bytes(codes_g, "codes_g", n, kb, index),
+                                       _packed_scales(scales_g, "scales_g", n, k, index, packed),
+                                       _bytes(codes_u, "codes_u", n, kb, index),
+                                       _packed_scales(scales_u, "scales_u", n, k, index, packed), 1 if packed else 0, m,
+                                       n, k, _vector(bias_g, "bias_g", n, index), _vector(bias_u, "bias_u", n, index),
+                                       ACTS[act], 1 if bf16 else 0, out.data_ptr(), ldo, gp, ldg, up, ldu,
+                                       _current_stream(index)))
+    return (out, g, u) if want_pre else out
+
+
+def mxfp4_gated_linear_backward(dout, g, u, act="silu", dg=None, du=None, dbias_g=None, dbias_u=None, biases=True,
+                                workspace=None, stream=None):
+    """Gradients of mxfp4_gated_linear's epilogue for its output's gradient dout (bf16 or fp32 [m][n]):
+    (dg, du, dbias_g, dbias_u) with dg = dout u act'(g), du = dout act(g) and the biases' their column sums (fp32 [n]).
+
+    g, u: the two products (mxfp4_gated_linear's). ``biases=False``: None for the sums. dg and du may be halves of
+    one [m][2 n] tensor. The operands' gradients are dg deq(Wg) + du deq(Wu), dg^T deq(A) and du^T deq(A).
+    """
+    torch = _torch()
+    bf16, index = _activation(dout, "dout")
+    here = _elsewhere(index, stream)
+    if here is not None:
+        with here:
+            return mxfp4_gated_linear_backward(dout, g, u, act, dg, du, dbias_g, dbias_u, biases, workspace)
+    dtype = dout.dtype
+    if act not in ACTS:
+        raise ValueError("act must be one of %s" % ", ".join(ACTS))
+    lddo = _matrix(dout, "dout", dtype, index)
+    m, n = dout.shape
+    ldg, ldu = _matrix(g, "g", dtype, index, m, n), _matrix(u, "u", dtype, index, m, n)
+    if dg is None:
+        dg, lddg = dout.new_empty((m, n)), n
+    else:
+        lddg = _matrix(dg, "dg", dtype, index, m, n)
+    if du is None:
+        du, lddu = dout.new_empty((m, n)), n
+    else:
+        lddu = _matrix(du, "du", dtype, index, m, n)
+    ws, ws_bytes = None, 0
+    if biases:
+        if dbias_g is None:
+            dbias_g = dout.new_empty(n, dtype=torch.float32)
+        if dbias_u is None:
+            dbias_u = dout.new_empty(n, dtype=torch.float32)
+        ws, ws_bytes = _workspace("kq_mxfp4_gated_linear_backward_workspace_bytes", m, n, workspace, dout)
+    elif dbias_g is not None or dbias_u is not None:
+        raise ValueError("biases=False computes neither dbias_g nor dbias_u")
+    _check("kq_mxfp4_gated_linear_backward",
+           lib().kq_mxfp4_gated_linear_backward(dout.data_ptr(), lddo, g.data_ptr(), ldg, u.data_ptr(), ldu, int(bf16), m,
+                                                n, ACTS[act], dg.data_ptr(), lddg, du.data_ptr(), lddu,
+                                                _vector(dbias_g, "dbias_g", n, index),
+                                                _vector(dbias_u, "dbias_u", n, index),
+                                                ws.data_ptr() if ws is not None else None, ws_bytes,
+                                                _current_stream(index)))
+    return dg, du, dbias_g, dbias_u
 
 
 # ---------------------------------------------------------------------------

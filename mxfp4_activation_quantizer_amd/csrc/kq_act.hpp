@@ -143,4 +143,50 @@ __device__ __forceinline__ void activate_grad(float (&d)[N], const float (&z)[N]
     }
 }
 
+// The gradients of act(z) u for the gradient d of it: d[i] = d[i] u[i] act'(z[i]), u[i] = d[i] act(z[i]), with
+// activate's value in its long form and activate_grad's slope.
+template <int N>
+__device__ __forceinline__ void activate_gated_grad(float (&d)[N], float (&u)[N], const float (&z)[N], int act) {
+    auto put = [&](int i, float value, float slope) {
+        const float t = d[i];
+        d[i] = t * slope * u[i];
+        u[i] = t * value;
+    };
+    switch (act) {
+        case KQ_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) put(i, z[i] < 0.f ? 0.f : z[i], z[i] > 0.f ? 1.f : 0.f);
+            break;
+        case KQ_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float s = logistic2(-kLog2e * z[i]), v = z[i] * s;
+                put(i, v, fmaf(v, 1.0f - s, s));
+            }
+            break;
+        case KQ_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float e;
+                const float p = normal_cdf<true>(z[i], e);
+                put(i, z[i] * p, fmaf(z[i] * 0.39894228040143268f, e, p));
+            }
+            break;
+        case KQ_ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float z2 = fminf(z[i] * z[i], 0x1p96f);
+                const float s = logistic2(gelu_tanh_exponent(z[i], z2));
+                constexpr float c = 1.59576912160573f;  // 2 sqrt(2 / pi)
+                const float v = z[i] * s;
+                put(i, v, fmaf(v * (1.0f - s), fmaf(3.0f * 0.044715f * c, z2, c), s));
+            }
+            break;
+        default:
+#pragma unroll
+            for (int i = 0; i < N; ++i) put(i, z[i], 1.f);
+            break;
+    }
+}
+
 }  // namespace kq

@@ -50,5 +50,32 @@ inline Kernel choose_kernel(int64_t m, int64_t n, int stages, bool packed, bool 
     return best;
 }
 
+// The same for kq_mxfp4_gated_linear, whose tiles hold as many columns of both weights: `n` is the output's. Tiles of
+// 16 x 16, 32 x 16, 64 x 64 (deep and not), 128 x 64 and 256 x 128 outputs.
+enum GatedKernel { kGatedProduct1, kGatedProduct2, kGatedTile64Deep, kGatedTile64, kGatedTile128, kGatedTile256 };
+
+inline GatedKernel choose_gated_kernel(int64_t m, int64_t n, int stages, bool packed, bool can256, int cus) {
+    const double st = stages;
+    auto tiles = [&](int64_t tm, int64_t tn) {  // per compute unit
+        return (double)((m + tm - 1) / tm) * (double)((n + tn - 1) / tn) / cus;
+    };
+    GatedKernel best = kGatedProduct1;
+    double least = 2.6 + ceil(tiles(16, 16)) * (0.21 * st + 0.13);
+    auto consider = [&](GatedKernel k, double us) {
+        if (us < least) best = k, least = us;
+    };
+    if (m <= 16) return best;
+    consider(kGatedProduct2, 2.6 + ceil(tiles(32, 16)) * (0.277 * st + 0.27));
+    consider(kGatedTile64Deep, 2.5 + ceil(tiles(64, 64)) * (0.45 * st + 2.69));
+    consider(kGatedTile64, 2.8 + fmax(0.63 * st, 0.25 * st + tiles(64, 64) * (0.35 * st + 1.3)));
+    consider(kGatedTile128, 2.9 + ceil(tiles(128, 64)) * (0.65 * st + 2.65));
+    if (can256) {
+        const double full = packed ? 13.55 + 1.41 * st : 2.1 + 2.33 * st, half = packed ? 6.07 + 1.05 * st : 3.16 + 1.48 * st;
+        const double t256 = tiles(256, 128), rem = t256 - floor(t256);
+        consider(kGatedTile256, 1.65 + floor(t256) * full + (rem == 0 ? 0 : rem <= 0.5 ? half : full));
+    }
+    return best;
+}
+
 }  // namespace linear
 }  // namespace kq

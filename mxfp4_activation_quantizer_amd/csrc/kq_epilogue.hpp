@@ -26,6 +26,18 @@ struct Epi {
     int stream;
 };
 
+// The epilogue of kq_mxfp4_gated_linear on the sums of two products with the same A,
+//   g = sum + bias,  u = sum_u + bias_u,  O = act(g) u,
+// and the second product's operand.
+struct GatedEpi {
+    const float *bias, *bias_u;  // [n] or NULL
+    void *O, *G, *U;             // [m][ld], bf16 bits or fp32; G, U may be NULL: receive g and u
+    int64_t m, n, ldo, ldg, ldu;
+    int act;
+    int align;  // every row of O, G and U starts at a multiple of this many bytes (16, 8 or less)
+    const uint8_t *cu, *su;  // codes and scales, laid out as the first product's
+};
+
 // N neighbouring elements in one piece. Non-temporal stores: outputs are not read again
 // here, so they should not push the operand lines that other workgroups still read.
 template <int N>
@@ -68,6 +80,12 @@ template <int N>
 __device__ __forceinline__ void load_bias(const Epi &ep, int64_t j, float (&b)[N]) {
 #pragma unroll
     for (int e = 0; e < N; ++e) b[e] = ep.bias && j + e < ep.n ? ep.bias[j + e] : 0.f;
+}
+
+template <int N>
+__device__ __forceinline__ void load_bias(const float *bias, int64_t n, int64_t j, float (&b)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) b[e] = bias && j + e < n ? bias[j + e] : 0.f;
 }
 
 // The residual of row i, columns j .. j + N - 1 (0 without one); they are inside n, in one
@@ -268,6 +286,105 @@ __device__ __forceinline__ void finish_staged(const uint8_t *reg, const Epi &ep,
             for (int u = 0; u < U; ++u) v[u] += __uint_as_float(sizeof(T) == 2 ? now[u] << 16 : now[u]);
         }
         store(ro, (uint32_t)ep.ldo);
+    }
+}
+
+// N columns j .. of row i from g and u (their bias added): one aligned piece inside n, or one element.
+template <class T, int N>
+__device__ __forceinline__ void finish_gated(float (&g)[N], const float (&u)[N], const GatedEpi &ep, int64_t i, int64_t j) {
+    if (ep.G) store_piece(static_cast<T *>(ep.G) + i * ep.ldg + j, g);
+    if (ep.U) store_piece(static_cast<T *>(ep.U) + i * ep.ldu + j, u);
+    activate<T>(g, ep.act);
+#pragma unroll
+    for (int e = 0; e < N; ++e) g[e] *= u[e];
+    store_piece(static_cast<T *>(ep.O) + i * ep.ldo + j, g);
+}
+template <class T>
+__device__ __forceinline__ void finish_gated1(float g, float u, const GatedEpi &ep, int64_t i, int64_t j) {
+    float v[1] = {g};
+    if (ep.G) store1(static_cast<T *>(ep.G) + i * ep.ldg + j, g);
+    if (ep.U) store1(static_cast<T *>(ep.U) + i * ep.ldu + j, u);
+    activate<T>(v, ep.act);
+    store1(static_cast<T *>(ep.O) + i * ep.ldo + j, v[0] * u);
+}
+
+// Rows [0, ROWS) of a wave's fp32 sums for 32 columns of both products, staged in LDS at reg in rows of 64
+// (the first product's 32, then the second's) with 16-byte chunk c at c ^ (row % 16), to the outputs'
+// rows i0 .. (those < rows) and columns j0 ..
+template <class T, int ROWS>
+__device__ __forceinline__ void finish_gated_staged(const uint8_t *reg, const GatedEpi &ep, int64_t i0, int rows,
+                                                    int64_t j0) {
+    constexpr int COLS = 32;
+    const int lane = threadIdx.x & 63;
+    auto at = [&](int row, int chunk) { return reg + row * 256 + 16 * (chunk ^ (row & 15)); };
+    if (rows <= 0 || j0 >= ep.n) return;
+    const T *type = nullptr;
+    const int cols = (int)(ep.n - j0 < COLS ? ep.n - j0 : COLS);
+    const auto ro = block_rsrc<T>(ep.O, ep.ldo, i0, rows, j0, cols);
+    const auto rg = block_rsrc<T>(ep.G, ep.ldg, i0, rows, j0, cols);
+    const auto ru = block_rsrc<T>(ep.U, ep.ldu, i0, rows, j0, cols);
+    const uint32_t po = (uint32_t)ep.ldo, pg = (uint32_t)ep.ldg, pu = (uint32_t)ep.ldu;
+    if (ep.align >= 16 && cols == COLS) {
+        typedef Staged<T, ROWS, COLS> S;
+        constexpr int EC = S::EC, U = S::N < 4 ? S::N : 4;
+        const int c = lane % S::kLanes, r0 = lane / S::kLanes;
+        float bg[EC], bu[EC];
+        load_bias(ep.bias, ep.n, j0 + EC * c, bg);
+        load_bias(ep.bias_u, ep.n, j0 + EC * c, bu);
+        for (int i = 0; i < S::N; i += U) {
+            float g[U * EC], u[U * EC];
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+#pragma unroll
+                for (int e4 = 0; e4 < EC / 4; ++e4) {
+                    const int row = S::kRows * (i + k) + r0, chunk = (EC / 4) * c + e4;
+                    const floatx4_t fg = *reinterpret_cast<const floatx4_t *>(at(row, chunk));
+                    const floatx4_t fu = *reinterpret_cast<const floatx4_t *>(at(row, 8 + chunk));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        g[EC * k + 4 * e4 + e] = fg[e] + bg[4 * e4 + e];
+                        u[EC * k + 4 * e4 + e] = fu[e] + bu[4 * e4 + e];
+                    }
+                }
+            auto store = [&](__amdgpu_buffer_rsrc_t r, uint32_t ld, const float *v) {
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        piece_of(v + EC * k, type), r,
+                        (uint32_t)(S::kRows * (i + k) + r0) * ld * (uint32_t)sizeof(T) + 16u * c, 0, 2);
+            };
+            if (ep.G) store(rg, pg, g);
+            if (ep.U) store(ru, pu, u);
+            activate<T>(g, ep.act);
+#pragma unroll
+            for (int e = 0; e < U * EC; ++e) g[e] *= u[e];
+            store(ro, po, g);
+        }
+        return;
+    }
+    constexpr int N = ROWS / 2, U = 8;
+    static_assert(N % U == 0, "whole batches");
+    const int c = lane % COLS, r0 = lane / COLS;
+    if (c >= cols) return;
+    const float bg = ep.bias ? ep.bias[j0 + c] : 0.f, bu = ep.bias_u ? ep.bias_u[j0 + c] : 0.f;
+    for (int i = 0; i < N; i += U) {
+        float g[U], u[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int row = 2 * (i + k) + r0;
+            g[k] = *reinterpret_cast<const float *>(at(row, c >> 2) + 4 * (c & 3)) + bg;
+            u[k] = *reinterpret_cast<const float *>(at(row, 8 + (c >> 2)) + 4 * (c & 3)) + bu;
+        }
+        auto store = [&](__amdgpu_buffer_rsrc_t r, uint32_t ld, const float *v) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) store1(r, (uint32_t)(2 * (i + k) + r0) * ld + c, v[k], type);
+        };
+        if (ep.G) store(rg, pg, g);
+        if (ep.U) store(ru, pu, u);
+        activate<T>(g, ep.act);
+#pragma unroll
+        for (int k = 0; k < U; ++k) g[k] *= u[k];
+        store(ro, po, g);
     }
 }
 

@@ -204,12 +204,13 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 
     }
 }
 
+// X and Y may be the same memory: a lane has read all of its pieces before it writes any of them.
 // A workgroup takes the heads of a few tokens; a wave 64 / LG of them at a time, the next ones' loads in flight
 // while these are finished. The table of angles is made once per token and read back by every head.
 template <class T, int V, int LG, int U, bool INTER>
-__global__ __launch_bounds__(kThreads) void forward_kernel(const T *__restrict__ X, int64_t ldx, int64_t hsx,
+__global__ __launch_bounds__(kThreads) void forward_kernel(const T *X, int64_t ldx, int64_t hsx,
                                                            const float *__restrict__ w0, const float *__restrict__ w1,
-                                                           Geom g, Rope rope, T *__restrict__ Y, int64_t ldy,
+                                                           Geom g, Rope rope, T *Y, int64_t ldy,
                                                            int64_t hsy) {
     extern __shared__ float2 table[];
     constexpr int HP = 64 / LG, G = U > 1 ? 1 : 2;
@@ -313,11 +314,11 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(const T *__restrict__
 // Workgroup p of `parts` takes the blocks of tokens p, p + parts, ...; its lanes keep their channels of both dw in
 // registers, and row p of the partial sums gets them at the end, the waves joined in their order.
 template <class T, int V, int LG, int U, bool INTER>
-__global__ __launch_bounds__(kBackThreads) void backward_kernel(const T *__restrict__ dY, int64_t lddy, int64_t hsdy,
-                                                                const T *__restrict__ X, int64_t ldx, int64_t hsx,
+__global__ __launch_bounds__(kBackThreads) void backward_kernel(const T *dY, int64_t lddy, int64_t hsdy,
+                                                                const T *X, int64_t ldx, int64_t hsx,
                                                                 const float *__restrict__ w0,
                                                                 const float *__restrict__ w1, Geom g, Rope rope,
-                                                                T *__restrict__ dX, int64_t lddx, int64_t hsdx,
+                                                                T *dX, int64_t lddx, int64_t hsdx,
                                                                 int parts, float *__restrict__ p0,
                                                                 float *__restrict__ p1) {
     extern __shared__ float2 table[];

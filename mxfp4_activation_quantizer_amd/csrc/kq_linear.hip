@@ -54,12 +54,18 @@ struct Stage {
     uint32_t scl[2][F];
 };
 
-template <class T, int SC, int MF, int NF, int WK, int D>
+// With GatedEpi a workgroup multiplies the same rows of A by as many of both weights: the second's fragments and
+// sums stand behind the first's.
+template <class E>
+constexpr bool kGated = std::is_same<E, GatedEpi>::value;
+
+template <class T, int SC, int MF, int NF, int WK, int D, class E>
 __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restrict__ ca,
                                                           const uint8_t *__restrict__ sa,
                                                           const uint8_t *__restrict__ cw,
-                                                          const uint8_t *__restrict__ sw, Geom g, Epi ep) {
-    __shared__ float4 red[WK][MF * NF][64];
+                                                          const uint8_t *__restrict__ sw, Geom g, E ep) {
+    constexpr int NW = kGated<E> ? 2 : 1;
+    __shared__ float4 red[WK][NW * MF * NF][64];
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int tn = (int)(blockIdx.x % (unsigned)g.tiles_n), tm = (int)(blockIdx.x / (unsigned)g.tiles_n);
     const int64_t m0 = (int64_t)tm * (16 * MF), n0 = (int64_t)tn * (16 * NF);
@@ -78,13 +84,20 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
                                     : rsrc(sa + m0 * g.kblocks, (int64_t)rows_a * g.kblocks);
     const auto rsw = SC == kPacked8 ? rsrc(sw + 8 * n0, (int64_t)g.stages * 8 * ep.n - 8 * n0)
                                     : rsrc(sw + n0 * g.kblocks, (int64_t)rows_w * g.kblocks);
+    const uint8_t *cu = cw, *su = sw;
+    if constexpr (kGated<E>) cu = ep.cu, su = ep.su;
+    const auto rcu = rsrc(cu + n0 * g.kbytes, (int64_t)rows_w * g.kbytes);
+    const auto rsu = SC == kPacked8 ? rsrc(su + 8 * n0, (int64_t)g.stages * 8 * ep.n - 8 * n0)
+                                    : rsrc(su + n0 * g.kblocks, (int64_t)rows_w * g.kblocks);
     constexpr uint32_t kNone = 0x80000000u;
 
-    floatx4_t acc[NF][MF];
+    floatx4_t acc[NW][NF][MF];
 #pragma unroll
-    for (int b = 0; b < NF; ++b)
+    for (int w = 0; w < NW; ++w)
 #pragma unroll
-        for (int a = 0; a < MF; ++a) acc[b][a] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        for (int b = 0; b < NF; ++b)
+#pragma unroll
+            for (int a = 0; a < MF; ++a) acc[w][b][a] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
     // stage s of the F fragments of one operand of `rows` rows
     auto fetch = [&](auto &S, __amdgpu_buffer_rsrc_t rc, __amdgpu_buffer_rsrc_t rs, int64_t rows, int s) {
@@ -119,11 +132,15 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
     constexpr int kSel1 = SC == kPacked8 ? 2 : 0;
 
     Stage<MF> A[D];
-    Stage<NF> B[D];
+    Stage<NF> B[D][NW];
+    auto fetch_w = [&](int i, int s) {
+        fetch(B[i][0], rcw, rsw, ep.n, s);
+        if constexpr (kGated<E>) fetch(B[i][1], rcu, rsu, ep.n, s);
+    };
 #pragma unroll
     for (int i = 0; i < D; ++i) {
         fetch(A[i], rca, rsa, ep.m, wave + WK * i);
-        fetch(B[i], rcw, rsw, ep.n, wave + WK * i);
+        fetch_w(i, wave + WK * i);
     }
     for (int s = wave; s < g.stages; s += WK * D) {
 #pragma unroll
@@ -132,32 +149,36 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int b = 0; b < NF; ++b) {
-                        const u32x4_t w4 = B[i].code[h][b];
+                    for (int wb = 0; wb < NW * NF; ++wb) {
+                        const int w = wb / NF, b = wb % NF;
+                        const u32x4_t w4 = B[i][w].code[h][b];
                         const i32x8_t fw = {(int)w4[0], (int)w4[1], (int)w4[2], (int)w4[3], 0, 0, 0, 0};
-                        const int xw = scale(B[i], h, b);
+                        const int xw = scale(B[i][w], h, b);
 #pragma unroll
                         for (int a = 0; a < MF; ++a) {
                             const u32x4_t a4 = A[i].code[h][a];
                             const i32x8_t fa = {(int)a4[0], (int)a4[1], (int)a4[2], (int)a4[3], 0, 0, 0, 0};
                             if (h == 0)
-                                acc[b][a] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                    fw, fa, acc[b][a], 4, 4, 0, xw, 0, scale(A[i], h, a));
+                                acc[w][b][a] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                    fw, fa, acc[w][b][a], 4, 4, 0, xw, 0, scale(A[i], h, a));
                             else
-                                acc[b][a] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                    fw, fa, acc[b][a], 4, 4, kSel1, xw, kSel1, scale(A[i], h, a));
+                                acc[w][b][a] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                    fw, fa, acc[w][b][a], 4, 4, kSel1, xw, kSel1, scale(A[i], h, a));
                         }
                     }
             }
             fetch(A[i], rca, rsa, ep.m, s + WK * (i + D));
-            fetch(B[i], rcw, rsw, ep.n, s + WK * (i + D));
+            fetch_w(i, s + WK * (i + D));
         }
     }
 #pragma unroll
-    for (int b = 0; b < NF; ++b)
+    for (int w = 0; w < NW; ++w)
 #pragma unroll
-        for (int a = 0; a < MF; ++a)
-            red[wave][b * MF + a][lane] = make_float4(acc[b][a][0], acc[b][a][1], acc[b][a][2], acc[b][a][3]);
+        for (int b = 0; b < NF; ++b)
+#pragma unroll
+            for (int a = 0; a < MF; ++a)
+                red[wave][(w * NF + b) * MF + a][lane] =
+                    make_float4(acc[w][b][a][0], acc[w][b][a][1], acc[w][b][a][2], acc[w][b][a][3]);
     __syncthreads();
     // group q of four columns: row q / (4 NF) of the tile, columns 4 (q % (4 NF)) ..
     for (int q = t; q < 64 * MF * NF; q += 64 * WK) {
@@ -169,7 +190,32 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
             const float4 v = red[w][f][l];
             z[0] += v.x; z[1] += v.y; z[2] += v.z; z[3] += v.w;
         }
-        if (r < rows_a && 4 * c4 < rows_w) {
+        if constexpr (kGated<E>) {
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < WK; ++w) {
+                const float4 v = red[w][MF * NF + f][l];
+                y[0] += v.x; y[1] += v.y; y[2] += v.z; y[3] += v.w;
+            }
+            if (r < rows_a && 4 * c4 < rows_w) {
+                const int64_t i = m0 + r, j = n0 + 4 * c4;
+                float b[4], bu[4];
+                load_bias(ep.bias, ep.n, j, b);
+                load_bias(ep.bias_u, ep.n, j, bu);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    z[e] += b[e];
+                    y[e] += bu[e];
+                }
+                if (ep.align >= 4 * (int)sizeof(T) && j + 4 <= ep.n) {
+                    finish_gated<T>(z, y, ep, i, j);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (j + e < ep.n) finish_gated1<T>(z[e], y[e], ep, i, j + e);
+                }
+            }
+        } else if (r < rows_a && 4 * c4 < rows_w) {
             const int64_t i = m0 + r, j = n0 + 4 * c4;
             float b[4];
             load_bias(ep, j, b);
@@ -201,11 +247,17 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
 // Bound by the lines in flight: a compute unit takes in about 55 GB/s whatever N is (128 x 4096
 // x 4096 8.3 us; two sets of waves on halves of a stage, or scales asked for 8 stages ahead, are
 // level).
-template <class T, int FA, int FB, int N>
+//
+// With GatedEpi (FB = 2) half of the staged rows of W are the first weight's and half the second's, and each wave
+// multiplies one fragment of both, so that both sums of an output are the same lane's.
+template <class T, int FA, int FB, int N, class E>
 __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict__ ca, const uint8_t *__restrict__ sa,
                                                    const uint8_t *__restrict__ cw, const uint8_t *__restrict__ sw,
-                                                   int packed, Geom g, Epi ep) {
+                                                   int packed, Geom g, E ep) {
     constexpr int TM = 64 * FA, TN = 64 * FB, kRowsAll = TM + TN;
+    constexpr bool GATED = kGated<E>;
+    static_assert(!GATED || FB == 2, "64 rows of each weight");
+    constexpr int TC = GATED ? TN / 2 : TN;  // columns of the output
     constexpr int kOffScl = kRowsAll * 128, kStage = kRowsAll * 136;
     constexpr int kLoads = kRowsAll / 32;  // code loads (8 rows each) per wave and stage
     static_assert(kLoads * (N - 2) <= 63 && N >= 2, "the wait counts at most 63 loads");
@@ -218,8 +270,10 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
     const int band = u / (kBand * g.tiles_n), within = u % (kBand * g.tiles_n);
     const int band_rows = g.tiles_m - band * kBand < kBand ? g.tiles_m - band * kBand : kBand;
     const int tm = band * kBand + within % band_rows, tn = within / band_rows;
-    const int64_t m0 = (int64_t)tm * TM, n0 = (int64_t)tn * TN;
-    const int rows_a = (int)(ep.m - m0 < TM ? ep.m - m0 : TM), rows_w = (int)(ep.n - n0 < TN ? ep.n - n0 : TN);
+    const int64_t m0 = (int64_t)tm * TM, n0 = (int64_t)tn * TC;
+    const int rows_a = (int)(ep.m - m0 < TM ? ep.m - m0 : TM), rows_w = (int)(ep.n - n0 < TC ? ep.n - n0 : TC);
+    const uint8_t *cu = cw, *su = sw;
+    if constexpr (GATED) cu = ep.cu, su = ep.su;
 
     if (w == 4) {
         // Rows lane + 64 i of the tile: A's first, then W's. A padding row takes the last row's
@@ -230,9 +284,9 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const bool is_a = i < FA;
-            const int row = lane + 64 * (is_a ? i : i - FA), last = (is_a ? rows_a : rows_w) - 1;
+            const int row = lane + 64 * (is_a ? i : GATED ? 0 : i - FA), last = (is_a ? rows_a : rows_w) - 1;
             const int64_t g_row = (is_a ? m0 : n0) + (row < last ? row : last);
-            at[i] = (is_a ? sa : sw) + g_row * (packed ? 8 : g.kblocks);
+            at[i] = (is_a ? sa : GATED && i > FA ? su : sw) + g_row * (packed ? 8 : g.kblocks);
             step[i] = 8 * (is_a ? ep.m : ep.n);
         }
         // this slot held stage s - N, whose reads ended before the barrier of stage s - N + 1
@@ -317,13 +371,15 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
 
     const i32x4_t dca = sdesc(ca + m0 * g.kbytes, (uint32_t)(rows_a * g.kbytes));
     const i32x4_t dcw = sdesc(cw + n0 * g.kbytes, (uint32_t)(rows_w * g.kbytes));
+    const i32x4_t dcu = sdesc(cu + n0 * g.kbytes, (uint32_t)(rows_w * g.kbytes));
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
     // load j of wave w: staged rows 8 (kLoads w + j) + lane / 8 (A's TM rows, then W's), slot lane % 8
     const int chunk[2] = {(lane & 7) ^ swz8(lane >> 3), (lane & 7) ^ swz8(8 + (lane >> 3))};
     uint32_t voff[kLoads];
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-        const int r0 = 8 * (kLoads * w + j), row = (r0 < TM ? r0 : r0 - TM) + (lane >> 3);
+        const int r0 = 8 * (kLoads * w + j);
+        const int row = (r0 < TM ? r0 : GATED && r0 >= TM + TC ? r0 - TM - TC : r0 - TM) + (lane >> 3);
         voff[j] = (uint32_t)(row * g.kbytes) + 16u * (uint32_t)chunk[j & 1];
     }
     // Past k (whole stages too): past the record count, zeros. The count is compared with the scalar
@@ -335,11 +391,18 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
         for (int j = 0; j < kLoads; ++j) {
             const int r0 = 8 * (kLoads * w + j);
             const uint32_t off = in[j & 1] ? voff[j] : 0x80000000u;
-            dma16(r0 < TM ? dca : dcw, lds0 + (uint32_t)(slot * kStage + r0 * 128), off, (uint32_t)kb);
+            i32x4_t dw = dcw;
+            if (GATED) {
+                dw.x = __builtin_amdgcn_readfirstlane(r0 >= TM + TC ? dcu.x : dcw.x);
+                dw.y = __builtin_amdgcn_readfirstlane(r0 >= TM + TC ? dcu.y : dcw.y);
+            }
+            dma16(r0 < TM ? dca : dw, lds0 + (uint32_t)(slot * kStage + r0 * 128), off, (uint32_t)kb);
         }
     };
     const int r = lane & 31, hi = lane >> 5;
-    const int wm = (w >> 1) * (TM / 2), wn = (w & 1) * (TN / 2);
+    const int wm = (w >> 1) * (TM / 2), wn = (w & 1) * (TC / 2);
+    // staged row of W at which the wave's fragment b starts
+    auto frag = [&](int b) { return wn + (GATED ? TC * b : 32 * b); };
     int rdo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) rdo[j] = r * 128 + 16 * ((2 * j + hi) ^ swz8(r & 15));
@@ -370,7 +433,7 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
                 xa[a] = *reinterpret_cast<const uint32_t *>(st + kOffScl + 8 * (wm + 32 * a + r) + 4 * hi);
 #pragma unroll
             for (int b = 0; b < FB; ++b)
-                xw[b] = *reinterpret_cast<const uint32_t *>(st + kOffScl + 8 * (TM + wn + 32 * b + r) + 4 * hi);
+                xw[b] = *reinterpret_cast<const uint32_t *>(st + kOffScl + 8 * (TM + frag(b) + r) + 4 * hi);
             auto step = [&](auto jc) {
                 constexpr int j = decltype(jc)::value;
                 i32x8_t fa[FA], fw[FB];
@@ -381,7 +444,7 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
                 }
 #pragma unroll
                 for (int b = 0; b < FB; ++b) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(st + (TM + wn + 32 * b) * 128 + rdo[j]);
+                    const uint4 q = *reinterpret_cast<const uint4 *>(st + (TM + frag(b)) * 128 + rdo[j]);
                     fw[b] = i32x8_t{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
                 }
 #pragma unroll
@@ -400,9 +463,11 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
 
     constexpr int WM = TM / 2, WN = TN / 2, CH = WN / 4;
     Bias<T, WM, WN> bias;
-    bias.load(ep, n0 + wn);
     Residual<T, WM, WN> add;
-    add.load(ep, m0 + wm, rows_a - wm, n0 + wn, 0);
+    if constexpr (!GATED) {
+        bias.load(ep, n0 + wn);
+        add.load(ep, m0 + wm, rows_a - wm, n0 + wn, 0);
+    }
     // every load into LDS has landed (the ones past k too) and every wave is done with the stages
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     // Each wave stages its block in fp32 in its own region, rows of 32 FB columns with 16-byte chunk c
@@ -419,7 +484,8 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
                     floatx4_t{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
             }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn, bias, add);
+    if constexpr (GATED) finish_gated_staged<T, WM>(reg, ep, m0 + wm, rows_a - wm, n0 + wn);
+    else finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn, bias, add);
 }
 
 // Backward of the epilogue: wave w of workgroup (x, p) takes 512
@@ -492,6 +558,78 @@ __global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO,
     }
 }
 
+// Backward of the gated epilogue, as backward_kernel: three reads and two writes per element, and both biases' sums.
+// The outputs may be inputs: a lane has read an element of each before it writes any.
+template <class T, bool NT, bool VEC>
+__global__ __launch_bounds__(256) void gated_backward_kernel(const T *dO, int64_t lddo,
+                                                             const T *G, int64_t ldg,
+                                                             const T *U, int64_t ldu, int64_t m, int64_t n,
+                                                             int act, T *dG, int64_t lddg,
+                                                             T *dU, int64_t lddu, int64_t group_rows,
+                                                             float *__restrict__ part_g, float *__restrict__ part_u) {
+    constexpr int R = 4;  // rows in flight per wave
+    __shared__ float4 join[4][4][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t c0 = (int64_t)blockIdx.x * 512, left = n - c0 < 512 ? n - c0 : 512;
+    const int64_t bytes = left * (int)sizeof(T);
+    const uint32_t ch = Lanes<VEC>::first(0, lane);
+    const int p = (int)blockIdx.y;
+    float s[2][8] = {};
+    const int64_t end = m - p * group_rows < group_rows ? m : (p + 1) * group_rows;
+    for (int64_t i = p * group_rows + wave; i < end; i += 4 * R) {
+        Chunk<T, VEC> d[R], g[R], u[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = i + 4 * k < end ? i + 4 * k : i, some = i + 4 * k < end ? bytes : 0;
+            d[k].template load<NT>(row_rsrc(dO + row * lddo + c0, some), ch);
+            g[k].template load<NT>(row_rsrc(G + row * ldg + c0, some), ch);
+            u[k].template load<NT>(row_rsrc(U + row * ldu + c0, some), ch);
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = i + 4 * k;
+            if (row >= end) break;
+            float v[8], x[8], y[8];
+            d[k].widen(v);
+            g[k].widen(x);
+            u[k].widen(y);
+            activate_gated_grad(v, y, x, act);
+            if (dG) store8<NT, VEC>(row_rsrc(dG + row * lddg + c0, bytes), ch, v, dG);
+            if (dU) store8<NT, VEC>(row_rsrc(dU + row * lddu + c0, bytes), ch, y, dU);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s[0][e] += v[e];
+                s[1][e] += y[e];
+            }
+        }
+    }
+    if (!part_g && !part_u) return;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        join[wave][2 * k][lane] = make_float4(s[k][0], s[k][1], s[k][2], s[k][3]);
+        join[wave][2 * k + 1][lane] = make_float4(s[k][4], s[k][5], s[k][6], s[k][7]);
+    }
+    __syncthreads();
+    // wave w: half w % 2 of the columns of the gate's (w < 2) or the other's sums
+    float *part = wave < 2 ? part_g : part_u;
+    if (!part) return;
+    float4 a = join[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+        const float4 o = join[w][wave][lane];
+        a.x += o.x; a.y += o.y; a.z += o.z; a.w += o.w;
+    }
+    const int64_t c = c0 + ch + 4 * (wave & 1) * Lanes<VEC>::kStep;
+    if (VEC) {
+        if (c < n) *reinterpret_cast<float4 *>(part + p * n + c) = a;
+    } else {
+        const float one[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + 64 * e < n) part[p * n + c + 64 * e] = one[e];
+    }
+}
+
 }  // namespace linear
 }  // namespace kq
 
@@ -502,6 +640,9 @@ namespace kqhost {
 kq_status gemm256_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
                          const uint8_t *scales_w, int packed, int64_t k, int type, const kq::Epi &ep,
                          kq_stream_t stream);  // kq_gemm256.hip
+kq_status gemm256_gated(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_g,
+                        const uint8_t *scales_g, int packed, int64_t k, int type, const kq::GatedEpi &ep,
+                        kq_stream_t stream);  // kq_gemm256.hip
 }
 
 namespace {
@@ -540,25 +681,26 @@ void launch_backward(const void *dO, int64_t lddo, const void *Z, int64_t ldz, i
 // The launch's work-items are counted in 32 bits.
 bool groups_fit(int64_t groups, int threads) { return groups <= (int64_t)0xFFFFFFFF / threads; }
 
-template <class T, int SC, int MF, int NF, int WK, int D>
+template <class T, int SC, int MF, int NF, int WK, int D, class E>
 kq_status launch_product(const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, const uint8_t *sw,
-                         kq::linear::Geom g, const kq::Epi &ep, kq_stream_t stream) {
+                         kq::linear::Geom g, const E &ep, kq_stream_t stream) {
     const int64_t tiles_m = (ep.m + 16 * MF - 1) / (16 * MF), tiles_n = (ep.n + 16 * NF - 1) / (16 * NF);
     g.tiles_n = (int)tiles_n;
     if (!groups_fit(tiles_m * tiles_n, 64 * WK)) return KQ_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((kq::linear::product_kernel<T, SC, MF, NF, WK, D>), dim3((unsigned)(tiles_m * tiles_n)),
+    hipLaunchKernelGGL((kq::linear::product_kernel<T, SC, MF, NF, WK, D, E>), dim3((unsigned)(tiles_m * tiles_n)),
                        dim3(64 * WK), 0, (hipStream_t)stream, ca, sa, cw, sw, g, ep);
     return launched();
 }
 
-template <class T, int FA, int FB, int N>
+template <class T, int FA, int FB, int N, class E>
 kq_status launch_tiles(const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, const uint8_t *sw, int packed,
-                       kq::linear::Geom g, const kq::Epi &ep, kq_stream_t stream) {
-    const int64_t tiles_m = (ep.m + 64 * FA - 1) / (64 * FA), tiles_n = (ep.n + 64 * FB - 1) / (64 * FB);
+                       kq::linear::Geom g, const E &ep, kq_stream_t stream) {
+    constexpr int cols = kq::linear::kGated<E> ? 32 * FB : 64 * FB;
+    const int64_t tiles_m = (ep.m + 64 * FA - 1) / (64 * FA), tiles_n = (ep.n + cols - 1) / cols;
     g.tiles_n = (int)tiles_n;
     g.tiles_m = (int)tiles_m;
     if (!groups_fit(tiles_m * tiles_n, 320)) return KQ_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((kq::linear::tile_kernel<T, FA, FB, N>), dim3((unsigned)(tiles_m * tiles_n)), dim3(320), 0,
+    hipLaunchKernelGGL((kq::linear::tile_kernel<T, FA, FB, N, E>), dim3((unsigned)(tiles_m * tiles_n)), dim3(320), 0,
                        (hipStream_t)stream, ca, sa, cw, sw, packed, g, ep);
     return launched();
 }
@@ -571,13 +713,15 @@ using kq::linear::kTile256;
 using kq::linear::kTile64;
 using kq::linear::kTile64Deep;
 
-template <class T, int MF, int NF, int WK>
+template <class T, int MF, int NF, int WK, class E>
 kq_status launch_any_product(const uint8_t *ca, const uint8_t *sa, const uint8_t *cw, const uint8_t *sw, int packed,
-                             const kq::linear::Geom &g, const kq::Epi &ep, kq_stream_t stream) {
-    if (packed) return launch_product<T, kq::linear::kPacked8, MF, NF, WK, 1>(ca, sa, cw, sw, g, ep, stream);
-    if (g.kblocks % 8 == 0 && aligned(sa, 8) && aligned(sw, 8))
-        return launch_product<T, kq::linear::kRows8, MF, NF, WK, 1>(ca, sa, cw, sw, g, ep, stream);
-    return launch_product<T, kq::linear::kBytes, MF, NF, WK, 1>(ca, sa, cw, sw, g, ep, stream);
+                             const kq::linear::Geom &g, const E &ep, kq_stream_t stream) {
+    if (packed) return launch_product<T, kq::linear::kPacked8, MF, NF, WK, 1, E>(ca, sa, cw, sw, g, ep, stream);
+    bool rows8 = g.kblocks % 8 == 0 && aligned(sa, 8) && aligned(sw, 8);
+    if constexpr (kq::linear::kGated<E>) rows8 = rows8 && aligned(ep.su, 8);
+    if (rows8)
+        return launch_product<T, kq::linear::kRows8, MF, NF, WK, 1, E>(ca, sa, cw, sw, g, ep, stream);
+    return launch_product<T, kq::linear::kBytes, MF, NF, WK, 1, E>(ca, sa, cw, sw, g, ep, stream);
 }
 
 template <class T>
@@ -591,6 +735,43 @@ kq_status launch_linear(Kernel k, const uint8_t *ca, const uint8_t *sa, const ui
         case kTile64: return launch_tiles<T, 1, 1, 2>(ca, sa, cw, sw, packed, g, ep, stream);
         default: return launch_tiles<T, 2, 2, 2>(ca, sa, cw, sw, packed, g, ep, stream);
     }
+}
+
+using kq::linear::GatedKernel;
+using kq::linear::kGatedProduct1;
+using kq::linear::kGatedProduct2;
+using kq::linear::kGatedTile256;
+using kq::linear::kGatedTile64;
+using kq::linear::kGatedTile64Deep;
+
+template <class T>
+kq_status launch_gated(GatedKernel k, const uint8_t *ca, const uint8_t *sa, const uint8_t *cg, const uint8_t *sg,
+                       int packed, const kq::linear::Geom &g, const kq::GatedEpi &ep, kq_stream_t stream) {
+    switch (k) {
+        case kGatedProduct1: return launch_any_product<T, 1, 1, 8>(ca, sa, cg, sg, packed, g, ep, stream);
+        case kGatedProduct2: return launch_any_product<T, 2, 1, 4>(ca, sa, cg, sg, packed, g, ep, stream);
+        case kGatedTile64Deep: return launch_tiles<T, 1, 2, 4>(ca, sa, cg, sg, packed, g, ep, stream);
+        case kGatedTile64: return launch_tiles<T, 1, 2, 2>(ca, sa, cg, sg, packed, g, ep, stream);
+        default: return launch_tiles<T, 2, 2, 2>(ca, sa, cg, sg, packed, g, ep, stream);
+    }
+}
+
+template <class T>
+void launch_gated_backward(const void *dO, int64_t lddo, const void *G, int64_t ldg, const void *U, int64_t ldu, int64_t m,
+                           int64_t n, int act, void *dG, int64_t lddg, void *dU, int64_t lddu, int64_t parts,
+                           float *part_g, float *part_u, bool vec, kq_stream_t stream) {
+    const int64_t rows = (m + parts - 1) / parts;
+    const dim3 grid((unsigned)((n + 511) / 512), (unsigned)parts);
+    auto go = [&](auto NT, auto VEC) {
+        hipLaunchKernelGGL((kq::linear::gated_backward_kernel<T, NT(), VEC()>), grid, dim3(256), 0, (hipStream_t)stream,
+                           (const T *)dO, lddo, (const T *)G, ldg, (const T *)U, ldu, m, n, act, (T *)dG, lddg, (T *)dU,
+                           lddu, rows, part_g, part_u);
+    };
+    const bool nt = kq::streamed_once(5 * m * n * (int)sizeof(T));
+    if (vec && nt) go(std::true_type(), std::true_type());
+    else if (vec) go(std::false_type(), std::true_type());
+    else if (nt) go(std::true_type(), std::false_type());
+    else go(std::false_type(), std::false_type());
 }
 
 }  // namespace
@@ -676,6 +857,91 @@ kq_status kq_mxfp4_linear_backward(const void *dO, int64_t lddo, const void *Z, 
     const kq_status s = launched();
     if (s != KQ_OK) return s;
     if (dbias && parts > 1) return kqhost::reduce_parts(part, nullptr, parts, n, dbias, nullptr, stream);
+    return KQ_OK;
+}
+
+kq_status kq_mxfp4_gated_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_g,
+                                const uint8_t *scales_g, const uint8_t *codes_u, const uint8_t *scales_u, int packed,
+                                int64_t m, int64_t n, int64_t k, const float *bias_g, const float *bias_u, int act,
+                                int type, void *O, int64_t ldo, void *G, int64_t ldg, void *U, int64_t ldu,
+                                kq_stream_t stream) {
+    if (m < 0 || n < 0 || k < 0 || k % 32 != 0 || (packed && k % 256 != 0) || ldo < n || (G && ldg < n) || (U && ldu < n))
+        return KQ_ERR_SHAPE;
+    if (!G) ldg = 0;
+    if (!U) ldu = 0;
+    if (!good_type(type) || !good_act(act) || !sizes_fit({m, n, k, ldo, ldg, ldu})) return KQ_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return KQ_OK;
+    if (!O || (k > 0 && (!codes_a || !scales_a || !codes_g || !scales_g || !codes_u || !scales_u))) return KQ_ERR_NULL;
+    const int es = type == KQ_BF16 ? 2 : 4;
+    if (!aligned(codes_a, 16) || !aligned(codes_g, 16) || !aligned(codes_u, 16) ||
+        (packed && (!aligned(scales_a, 8) || !aligned(scales_g, 8) || !aligned(scales_u, 8))) || !aligned(bias_g, 4) ||
+        !aligned(bias_u, 4) || !aligned(O, es) || !aligned(G, es) || !aligned(U, es))
+        return KQ_ERR_ALIGN;
+    // buffer record counts and offsets are 32-bit
+    const int64_t lim = (int64_t)1 << 31;
+    if (256 * (k / 2) >= lim || m * (k / 32) >= lim || n * (k / 32) >= lim || (255 * ldo + n) * es >= lim ||
+        (255 * ldg + n) * es >= lim || (255 * ldu + n) * es >= lim)
+        return KQ_ERR_UNSUPPORTED;
+    kq::GatedEpi ep{bias_g, bias_u, O, G, U, m, n, ldo, ldg, ldu, act, 16, codes_u, scales_u};
+    while (ep.align > es && (!aligned(O, ep.align) || !aligned(G, ep.align) || !aligned(U, ep.align) ||
+                             ((ldo | ldg | ldu) * es) % ep.align != 0))
+        ep.align /= 2;
+    const kq::linear::Geom g{(int)(k / 2), (int)(k / 32), (int)((k + 255) / 256), 0, 0};
+    if (k == 0) packed = 0;  // as kq_mxfp4_linear
+    const int s_align = packed ? 16 : 4;
+    const bool big = k > 0 && (packed || k % 128 == 0) && aligned(scales_a, s_align) && aligned(scales_g, s_align) &&
+                     aligned(scales_u, s_align);
+    const GatedKernel kernel = kq::linear::choose_gated_kernel(m, n, g.stages, packed != 0, big, kqhost::compute_units());
+    if (kernel == kGatedTile256)
+        return kqhost::gemm256_gated(codes_a, scales_a, codes_g, scales_g, packed, k, type, ep, stream);
+    return type == KQ_BF16 ? launch_gated<uint16_t>(kernel, codes_a, scales_a, codes_g, scales_g, packed, g, ep, stream)
+                           : launch_gated<float>(kernel, codes_a, scales_a, codes_g, scales_g, packed, g, ep, stream);
+}
+
+kq_status kq_mxfp4_gated_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t *bytes) {
+    if (!bytes) return KQ_ERR_NULL;
+    *bytes = 0;
+    if (m < 0 || n < 0) return KQ_ERR_SHAPE;
+    if (!sizes_fit({m, n})) return KQ_ERR_UNSUPPORTED;
+    const int64_t parts = column_parts(m, n);
+    if (parts > 1) *bytes = parts * 2 * n * 4;
+    return KQ_OK;
+}
+
+kq_status kq_mxfp4_gated_linear_backward(const void *dO, int64_t lddo, const void *G, int64_t ldg, const void *U,
+                                         int64_t ldu, int type, int64_t m, int64_t n, int act, void *dG, int64_t lddg,
+                                         void *dU, int64_t lddu, float *dbias_g, float *dbias_u, void *workspace,
+                                         int64_t workspace_bytes, kq_stream_t stream) {
+    if (m < 0 || n < 0 || lddo < n || ldg < n || ldu < n || (dG && lddg < n) || (dU && lddu < n)) return KQ_ERR_SHAPE;
+    if (!dG) lddg = 0;
+    if (!dU) lddu = 0;
+    if (!good_type(type) || !good_act(act) || !sizes_fit({m, n, lddo, ldg, ldu, lddg, lddu})) return KQ_ERR_UNSUPPORTED;
+    if (n == 0) return KQ_OK;
+    if (!aligned(dbias_g, 4) || !aligned(dbias_u, 4)) return KQ_ERR_ALIGN;
+    const bool sums = dbias_g || dbias_u;
+    if (m == 0) return sums ? kqhost::reduce_parts(nullptr, nullptr, 0, n, dbias_g, dbias_u, stream) : KQ_OK;
+    if (!dO || !G || !U || (!dG && !dU && !sums)) return KQ_ERR_NULL;
+    const uintptr_t es = type == KQ_BF16 ? 2 : 4;
+    if (!aligned(dO, es) || !aligned(G, es) || !aligned(U, es) || !aligned(dG, es) || !aligned(dU, es)) return KQ_ERR_ALIGN;
+    const int64_t parts = column_parts(m, n);
+    float *part_g = dbias_g, *part_u = dbias_u;
+    if (sums && parts > 1) {
+        if (!workspace) return KQ_ERR_NULL;
+        if (!aligned(workspace, 16)) return KQ_ERR_ALIGN;
+        if (workspace_bytes < parts * 2 * n * 4) return KQ_ERR_SHAPE;
+        part_g = static_cast<float *>(workspace);
+        part_u = part_g + parts * n;
+    }
+    const int64_t per16 = 16 / es;
+    const bool vec = n % 8 == 0 && aligned(dO, 16) && aligned(G, 16) && aligned(U, 16) && aligned(dG, 16) && aligned(dU, 16) &&
+                     (lddo | ldg | ldu | lddg | lddu) % per16 == 0 && aligned(part_g, 16) && aligned(part_u, 16);
+    if (type == KQ_BF16)
+        launch_gated_backward<uint16_t>(dO, lddo, G, ldg, U, ldu, m, n, act, dG, lddg, dU, lddu, parts, part_g, part_u, vec, stream);
+    else
+        launch_gated_backward<float>(dO, lddo, G, ldg, U, ldu, m, n, act, dG, lddg, dU, lddu, parts, part_g, part_u, vec, stream);
+    const kq_status s = launched();
+    if (s != KQ_OK) return s;
+    if (sums && parts > 1) return kqhost::reduce_parts(part_g, part_u, parts, n, dbias_g, dbias_u, stream);
     return KQ_OK;
 }
 
