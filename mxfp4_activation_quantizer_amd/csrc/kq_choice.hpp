@@ -50,29 +50,53 @@ inline Kernel choose_kernel(int64_t m, int64_t n, int stages, bool packed, bool 
     return best;
 }
 
-// The same for kq_mxfp4_gated_linear, whose tiles hold as many columns of both weights: `n` is the output's. Tiles of
-// 16 x 16, 32 x 16, 64 x 64 (deep and not), 128 x 64 and 256 x 128 outputs.
+// The same for kq_mxfp4_gated_linear, whose tiles hold as many columns of both weights (`n` is the output's): tiles of
+// 16 x 16 and 32 x 16 outputs with k split over four waves, 64 x 64 four stages deep and two, 128 x 64, and 256 x 128 on
+// persistent workgroups. Six estimates for each layout of the scales, fitted to 1043 measured products
+// (profiles/gated_products_by_kernel.md: m = 1 .. 8192, n = 512 .. 11008, k = 256 .. 8192; the choice is 1.5%
+// slower than the fastest on average, 50% at worst). The split of k wins while its tiles are few for the compute units;
+// one token of n = 11008, k = 4096 takes 11.4 us on either the first kernel or the third.
+// Measured at n = 11008, k = 4096, packed scales, in the order of the list (us):
+//       1 row   11.4         11.4  13.2
+//      64              29.7  12.1  13.7  15.8
+//     256              99.6  32.2  26.6  28.8  24.7
+//    1024                   108.7  83.5  76.3  52.2
+//    8192                   785.7 610.0 514.2 343.1
 enum GatedKernel { kGatedProduct1, kGatedProduct2, kGatedTile64Deep, kGatedTile64, kGatedTile128, kGatedTile256 };
 
+// can256: the scales' alignment and k allow the 256 x 128 kernel.
 inline GatedKernel choose_gated_kernel(int64_t m, int64_t n, int stages, bool packed, bool can256, int cus) {
+    struct Estimate {
+        double split1[4], split2[4];   // a + b stages + tiles (c stages + d), tiles per compute unit
+        double deep[3];                // a + rounds (b stages + c)
+        double tile64[5], tile128[5];  // a + the larger of b stages and c stages + tiles (d stages + e)
+        double big[5];                 // a + rounds (b + c stages), the last one d + e stages if it leaves half idle
+    };
+    static const Estimate layouts[2] = {
+        {{2.76, 0.156, 0.197, 0.084}, {2.94, 0.199, 0.308, 0.132}, {1.20, 0.451, 3.48}, {4.12, 0.534, 0.250, 0.389, 1.69},
+         {5.14, 0.650, 0.177, 0.719, 2.65}, {3.15, 5.66, 1.85, 2.70, 1.44}},  // MX layout
+        {{2.85, 0.117, 0.184, 0.095}, {3.04, 0.159, 0.252, 0.216}, {1.23, 0.440, 2.74}, {3.34, 0.537, 0.166, 0.397, 1.20},
+         {4.15, 0.650, 0.239, 0.705, 1.61}, {2.69, 6.26, 1.52, 4.08, 0.92}}};  // packed
+    const Estimate &e = layouts[packed ? 1 : 0];
     const double st = stages;
     auto tiles = [&](int64_t tm, int64_t tn) {  // per compute unit
         return (double)((m + tm - 1) / tm) * (double)((n + tn - 1) / tn) / cus;
     };
     GatedKernel best = kGatedProduct1;
-    double least = 2.6 + ceil(tiles(16, 16)) * (0.21 * st + 0.13);
+    double least = HUGE_VAL;
     auto consider = [&](GatedKernel k, double us) {
         if (us < least) best = k, least = us;
     };
-    if (m <= 16) return best;
-    consider(kGatedProduct2, 2.6 + ceil(tiles(32, 16)) * (0.277 * st + 0.27));
-    consider(kGatedTile64Deep, 2.5 + ceil(tiles(64, 64)) * (0.45 * st + 2.69));
-    consider(kGatedTile64, 2.8 + fmax(0.63 * st, 0.25 * st + tiles(64, 64) * (0.35 * st + 1.3)));
-    consider(kGatedTile128, 2.9 + ceil(tiles(128, 64)) * (0.65 * st + 2.65));
+    auto split = [&](const double (&x)[4], double t) { return x[0] + x[1] * st + t * (x[2] * st + x[3]); };
+    auto shared = [&](const double (&x)[5], double t) { return x[0] + fmax(x[1] * st, x[2] * st + t * (x[3] * st + x[4])); };
+    if (m <= 16) consider(kGatedProduct1, split(e.split1, tiles(16, 16)));
+    else if (m <= 256) consider(kGatedProduct2, split(e.split2, tiles(32, 16)));  // measured up to there
+    consider(kGatedTile64Deep, e.deep[0] + ceil(tiles(64, 64)) * (e.deep[1] * st + e.deep[2]));
+    consider(kGatedTile64, shared(e.tile64, tiles(64, 64)));
+    consider(kGatedTile128, shared(e.tile128, tiles(128, 64)));
     if (can256) {
-        const double full = packed ? 13.55 + 1.41 * st : 2.1 + 2.33 * st, half = packed ? 6.07 + 1.05 * st : 3.16 + 1.48 * st;
-        const double t256 = tiles(256, 128), rem = t256 - floor(t256);
-        consider(kGatedTile256, 1.65 + floor(t256) * full + (rem == 0 ? 0 : rem <= 0.5 ? half : full));
+        const double t = tiles(256, 128), rem = t - floor(t), full = e.big[1] + e.big[2] * st;
+        consider(kGatedTile256, e.big[0] + floor(t) * full + (rem == 0 ? 0 : rem <= 0.5 ? e.big[3] + e.big[4] * st : full));
     }
     return best;
 }

@@ -128,22 +128,16 @@ typedef float floatx4_t __attribute__((ext_vector_type(4)));
 // of one (k % 128 == 0): chunks and scales past k are pushed past the record counts and
 // read zeros.
 //
-// EPI with E = GatedEpi: the tile's TN staged rows of W are TN / 2 of each of the two weights (the second's, and their
-// scales, behind the first's), its outputs TN / 2 columns. A wave's fragments b are of the two weights in turn, so
-// that both sums of an output are the same lane's; a half tile is 64 columns.
-//
 // One tile (run-order number u; half h of it when TN = 128) of one workgroup;
 // smem holds 2 stages of the full-width layout plus 1 KB.
-template <bool LR, int TN, bool B16, bool LRS = false, bool NS = false, bool EPI = false, class E = Epi>
+template <bool LR, int TN, bool B16, bool LRS = false, bool NS = false, bool EPI = false>
 __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, const uint8_t *__restrict__ psa,
                                              const uint8_t *__restrict__ cw, const uint8_t *__restrict__ psw,
                                              const Geom g, const void *__restrict__ lr0,
                                              const void *__restrict__ lr1, const void *__restrict__ lr2,
                                              void *__restrict__ O, int u, int h, uint8_t *smem,
-                                             const E &ep = E()) {
+                                             const Epi &ep = Epi()) {
     static_assert(TN == 256 || TN == 128, "tile width");
-    constexpr bool GATED = std::is_same<E, GatedEpi>::value;
-    constexpr int TC = GATED ? TN / 2 : TN;  // columns of the output
     using L = Lay<TN>;
     constexpr int NB = L::NB, LW = L::LW;
     // stage buffers at kStage of the full-width layout (the spare 1 KB after two
@@ -155,19 +149,13 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     const int band = u / (kGroupM * g.tiles_n), within = u % (kGroupM * g.tiles_n);
     const int gm = min(kGroupM, g.tiles_m - band * kGroupM);
     const int tm = band * kGroupM + within % gm, tn = within / gm;
-    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * (GATED ? kTile / 2 : kTile) + (TN == 256 ? 0 : TC * h);
-    const int rows_a = (int)min<int64_t>(kTile, g.m - m0), rows_w = (int)min<int64_t>(TC, g.n - n0);
+    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile + (TN == 256 ? 0 : 128 * h);
+    const int rows_a = (int)min<int64_t>(kTile, g.m - m0), rows_w = (int)min<int64_t>(TN, g.n - n0);
     if (rows_w <= 0) return;  // the right half of a tile narrower than 129 columns (whole workgroup)
 
     // codes: rows past m or n are past the record count and read zero
     const i32x4_t dca = sdesc(ca + m0 * g.kbytes, (uint32_t)(rows_a * g.kbytes));
-    // (gated) waves 0 and 1 load the first weight, 2 and 3 the second; their scales are wave 2's and wave 3's
-    const uint8_t *cw_own = cw, *psw_own = psw;
-    if constexpr (GATED) {
-        if (w >= 2) cw_own = ep.cu;
-        if (w == 3) psw_own = ep.su;
-    }
-    const i32x4_t dcw = sdesc(cw_own + n0 * g.kbytes, (uint32_t)(rows_w * g.kbytes));
+    const i32x4_t dcw = sdesc(cw + n0 * g.kbytes, (uint32_t)(rows_w * g.kbytes));
     // packed scales: stage s of row i at 8 (s rows + i), the whole offset in the
     // range-checked vector offset (the scalar offset is not checked), so every
     // read stays inside the packed array: a padding row past m or n reads a
@@ -176,7 +164,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     constexpr bool kTail = NS && EPI;
     const int kblocks = kTail ? g.kbytes / 16 : 8 * g.stages;
     const i32x4_t dsa = sdesc(psa, (uint32_t)(kblocks * g.m));
-    const i32x4_t dsw = sdesc(psw_own, (uint32_t)(kblocks * g.n));
+    const i32x4_t dsw = sdesc(psw, (uint32_t)(kblocks * g.n));
     // (NS) scales in the MX layout [rows][k / 32]: row i's eight bytes of stage s at
     // (k / 32) i + 8 s, blocks in order; same record counts (k / 32 = 8 stages)
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
@@ -191,7 +179,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     }
 #pragma unroll
     for (int j = 0; j < LW; ++j) {
-        const int row = (TN / 4) * (GATED ? w & 1 : w) + 8 * j + (lane >> 3);
+        const int row = (TN / 4) * w + 8 * j + (lane >> 3);
         cvoffw[j] = (uint32_t)(row * g.kbytes) + 16u * (uint32_t)((lane & 7) ^ swz8(row & 15));
     }
     // (kTail) the lane's chunk of an even and of an odd load (rows of a load start at
@@ -212,16 +200,15 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     // wave 3's load is then past the record count and lands in the spare LDS).
     // Written without branches (the wave index is uniform: scalar selects), so
     // that the loop body stays one block and the order fixed below holds.
-    // (gated) wave 2 loads the first weight's and wave 3 the second's: 128 rows each, of which a half tile uses 64
-    const bool sw_a = w < 2, sw_none = TN == 128 && !GATED && w == 3;
-    const int srow = (GATED && !sw_a ? 0 : 128 * (w & 1)) + 2 * lane;
+    const int srow = 128 * (w & 1) + 2 * lane;
+    const bool sw_a = w < 2, sw_none = TN == 128 && w == 3;
     const i32x4_t dss = sw_a ? dsa : dsw;
     const uint32_t srow_off = (uint32_t)(8 * ((sw_a ? m0 : n0) + srow)), s_stride = (uint32_t)(8 * (sw_a ? g.m : g.n));
     const uint32_t s_lds = sw_none ? (uint32_t)(2 * kStage) : (uint32_t)((sw_a ? L::kOffSA : L::kOffSW) + 1024 * (w & 1));
     // (NS) four loads of 256 bytes per wave and stage: load j, lane l: row
     // 128 (w & 1) + 32 j + l / 2 of the wave's operand, its dword l & 1 of the stage,
     // into the same [rows][8] bytes of LDS (blocks in order instead of even first)
-    const uint32_t ns_row = (uint32_t)(((sw_a ? m0 : n0) + (GATED && !sw_a ? 0 : 128 * (w & 1)) + (lane >> 1)) * (int64_t)kblocks) +
+    const uint32_t ns_row = (uint32_t)(((sw_a ? m0 : n0) + 128 * (w & 1) + (lane >> 1)) * (int64_t)kblocks) +
                             4u * (uint32_t)(lane & 1);
     auto issue_scl_ns = [&](int s, int j) {
         const bool past = kTail && 8 * s + 4 * (lane & 1) >= kblocks;
@@ -239,10 +226,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     };
 
     const int r = lane & 31, hi = lane >> 5;
-    const int wm = (w >> 1) * 128, wn = (w & 1) * (TC / 2);
-    // staged row of W (of its codes, and of its scales) at which the wave's fragment b starts
-    auto frag = [&](int b) { return GATED ? wn + TC * (b & 1) + 32 * (b >> 1) : wn + 32 * b; };
-    auto frag_scl = [&](int b) { return GATED ? wn + 128 * (b & 1) + 32 * (b >> 1) : wn + 32 * b; };
+    const int wm = (w >> 1) * 128, wn = (w & 1) * (TN / 2);
     int rdo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) rdo[j] = r * 128 + 16 * ((2 * j + hi) ^ swz8(r & 15));
@@ -261,7 +245,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const uint2 d = *reinterpret_cast<const uint2 *>(sc + L::kOffSW + 8 * frag_scl(b));
+                const uint2 d = *reinterpret_cast<const uint2 *>(sc + L::kOffSW + 8 * (wn + 32 * b));
                 S.sb[b] = __builtin_amdgcn_perm(d.y, d.x, ns_sel);
             }
             return;
@@ -270,7 +254,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
 #pragma unroll
         for (int a = 0; a < 4; ++a) S.sa[a] = *reinterpret_cast<const uint32_t *>(sc + L::kOffSA + 8 * (wm + 32 * a));
 #pragma unroll
-        for (int b = 0; b < NB; ++b) S.sb[b] = *reinterpret_cast<const uint32_t *>(sc + L::kOffSW + 8 * frag_scl(b));
+        for (int b = 0; b < NB; ++b) S.sb[b] = *reinterpret_cast<const uint32_t *>(sc + L::kOffSW + 8 * (wn + 32 * b));
     };
     // step j of stage s: 16-byte fragments (k group 2 j + hi)
     auto read_frags = [&](int s, int j, Frag<NB> &F) {
@@ -282,7 +266,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(st + L::kOffW + frag(b) * 128 + rdo[j]);
+            const uint4 q = *reinterpret_cast<const uint4 *>(st + L::kOffW + (wn + 32 * b) * 128 + rdo[j]);
             F.b[b] = i32x8_t{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
         }
     };
@@ -575,7 +559,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     const bool whole = g.rows16 && n0 + TN <= g.n;
     typedef typename std::conditional<B16, uint16_t, float>::type T;
     Bias<T, 128, 64> bias[NB / 2];
-    if constexpr (EPI && !GATED) {
+    if constexpr (EPI) {
 #pragma unroll
         for (int pass = 0; pass < NB / 2; ++pass) bias[pass].load(ep, n0 + wn + 64 * pass);
     }
@@ -589,7 +573,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
 #pragma unroll
         for (int pass = 0; pass < NB / 2; ++pass) {
             Residual<T, 128, 64> add;
-            if constexpr (!GATED) add.load(ep, m0 + wm, rows_a - wm, n0 + wn + 64 * pass, 0);
+            add.load(ep, m0 + wm, rows_a - wm, n0 + wn + 64 * pass, 0);
 #pragma unroll
             for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -601,8 +585,7 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
                             acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
                     }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            if constexpr (GATED) finish_gated_staged<T, 128>(reg, ep, m0 + wm, rows_a - wm, n0 + wn + 32 * pass);
-            else finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn + 64 * pass, bias[pass], add);
+            finish_staged(reg, ep, m0 + wm, rows_a - wm, n0 + wn + 64 * pass, bias[pass], add);
         }
         return;
     }
@@ -682,19 +665,19 @@ __global__ __launch_bounds__(kThreads) void gemm256_kernel(const uint8_t *__rest
 }
 
 // The same with kq_mxfp4_linear's epilogue.
-template <bool B16, bool NS, class E>
+template <bool B16, bool NS>
 __global__ __launch_bounds__(kThreads) void gemm256_epilogue_kernel(const uint8_t *__restrict__ ca,
                                                                     const uint8_t *__restrict__ psa,
                                                                     const uint8_t *__restrict__ cw,
                                                                     const uint8_t *__restrict__ psw, Geom g,
-                                                                    E ep) {
+                                                                    Epi ep) {
     __shared__ __attribute__((aligned(16))) uint8_t smem[2 * Lay<256>::kStage + 1024];
     const TileWork wk = tile_work((int)blockIdx.x, g.order);
     if (wk.half < 0)
-        gemm256_tile<false, 256, B16, false, NS, true, E>(ca, psa, cw, psw, g, nullptr, nullptr, nullptr, nullptr, wk.tile,
+        gemm256_tile<false, 256, B16, false, NS, true>(ca, psa, cw, psw, g, nullptr, nullptr, nullptr, nullptr, wk.tile,
                                                        0, smem, ep);
     else
-        gemm256_tile<false, 128, B16, false, NS, true, E>(ca, psa, cw, psw, g, nullptr, nullptr, nullptr, nullptr, wk.tile,
+        gemm256_tile<false, 128, B16, false, NS, true>(ca, psa, cw, psw, g, nullptr, nullptr, nullptr, nullptr, wk.tile,
                                                        wk.half, smem, ep);
 }
 
@@ -854,14 +837,12 @@ kq_status gemm256_mx_lowrank(const uint8_t *codes_a, const uint8_t *scales_a, co
                              kq_stream_t stream) {
     return gemm_lowrank<true>(codes_a, scales_a, codes_w, scales_w, m, n, k, Z, codes_l, scales_l, r, O, ldo, stream);
 }
-// kq_mxfp4_linear and kq_mxfp4_gated_linear on these tiles; their arguments are checked by the caller. Packed scales
+// kq_mxfp4_linear on these tiles; its arguments are checked by the caller. Packed scales
 // 16-byte aligned and k % 256 == 0, or MX-layout scales 4-byte aligned and k % 128 == 0.
-template <class E>
-static kq_status gemm256_epilogue(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
-                                  const uint8_t *scales_w, int packed, int64_t k, int type, const E &ep,
-                                  kq_stream_t stream) {
-    constexpr int cols = std::is_same<E, kq::GatedEpi>::value ? 128 : 256;
-    const int64_t tiles_m = (ep.m + 255) / 256, tiles_n = (ep.n + cols - 1) / cols;
+kq_status gemm256_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
+                         const uint8_t *scales_w, int packed, int64_t k, int type, const kq::Epi &ep,
+                         kq_stream_t stream) {
+    const int64_t tiles_m = (ep.m + 255) / 256, tiles_n = (ep.n + 255) / 256;
     if (tiles_m * tiles_n >= (int64_t)1 << 23) return KQ_ERR_UNSUPPORTED;  // work-items are counted in 32 bits
     kq::g256::Geom g;
     g.m = ep.m;
@@ -876,9 +857,9 @@ static kq_status gemm256_epilogue(const uint8_t *codes_a, const uint8_t *scales_
     g.r = 0;
     g.order = kq::g256::make_tile_order(g.nwg, kq::g256::cu_count());
     const dim3 grid((unsigned)kq::g256::tile_order_groups(g.order)), block(kq::g256::kThreads);
-#define KQ_LINEAR(B16, NS)                                                                                     \
-    hipLaunchKernelGGL((kq::g256::gemm256_epilogue_kernel<B16, NS, E>), grid, block, 0, (hipStream_t)stream,   \
-                       codes_a, scales_a, codes_w, scales_w, g, ep)
+#define KQ_LINEAR(B16, NS)                                                                                         \
+    hipLaunchKernelGGL((kq::g256::gemm256_epilogue_kernel<B16, NS>), grid, block, 0, (hipStream_t)stream, codes_a, \
+                       scales_a, codes_w, scales_w, g, ep)
     if (type == KQ_BF16) {
         if (packed) KQ_LINEAR(true, false);
         else KQ_LINEAR(true, true);
@@ -888,16 +869,6 @@ static kq_status gemm256_epilogue(const uint8_t *codes_a, const uint8_t *scales_
     }
 #undef KQ_LINEAR
     return launched();
-}
-kq_status gemm256_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
-                         const uint8_t *scales_w, int packed, int64_t k, int type, const kq::Epi &ep,
-                         kq_stream_t stream) {
-    return gemm256_epilogue(codes_a, scales_a, codes_w, scales_w, packed, k, type, ep, stream);
-}
-kq_status gemm256_gated(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_g,
-                        const uint8_t *scales_g, int packed, int64_t k, int type, const kq::GatedEpi &ep,
-                        kq_stream_t stream) {
-    return gemm256_epilogue(codes_a, scales_a, codes_g, scales_g, packed, k, type, ep, stream);
 }
 }  // namespace kqhost
 

@@ -640,9 +640,10 @@ namespace kqhost {
 kq_status gemm256_linear(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_w,
                          const uint8_t *scales_w, int packed, int64_t k, int type, const kq::Epi &ep,
                          kq_stream_t stream);  // kq_gemm256.hip
-kq_status gemm256_gated(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_g,
-                        const uint8_t *scales_g, int packed, int64_t k, int type, const kq::GatedEpi &ep,
-                        kq_stream_t stream);  // kq_gemm256.hip
+kq_status gated256_bf16(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_g, const uint8_t *scales_g,
+                        int packed, int64_t k, const kq::GatedEpi &ep, kq_stream_t stream);  // kq_gated256_bf16.hip
+kq_status gated256_f32(const uint8_t *codes_a, const uint8_t *scales_a, const uint8_t *codes_g, const uint8_t *scales_g,
+                       int packed, int64_t k, const kq::GatedEpi &ep, kq_stream_t stream);  // kq_gated256_f32.hip
 }
 
 namespace {
@@ -748,7 +749,7 @@ template <class T>
 kq_status launch_gated(GatedKernel k, const uint8_t *ca, const uint8_t *sa, const uint8_t *cg, const uint8_t *sg,
                        int packed, const kq::linear::Geom &g, const kq::GatedEpi &ep, kq_stream_t stream) {
     switch (k) {
-        case kGatedProduct1: return launch_any_product<T, 1, 1, 8>(ca, sa, cg, sg, packed, g, ep, stream);
+        case kGatedProduct1: return launch_any_product<T, 1, 1, 4>(ca, sa, cg, sg, packed, g, ep, stream);
         case kGatedProduct2: return launch_any_product<T, 2, 1, 4>(ca, sa, cg, sg, packed, g, ep, stream);
         case kGatedTile64Deep: return launch_tiles<T, 1, 2, 4>(ca, sa, cg, sg, packed, g, ep, stream);
         case kGatedTile64: return launch_tiles<T, 1, 2, 2>(ca, sa, cg, sg, packed, g, ep, stream);
@@ -889,11 +890,12 @@ kq_status kq_mxfp4_gated_linear(const uint8_t *codes_a, const uint8_t *scales_a,
     const kq::linear::Geom g{(int)(k / 2), (int)(k / 32), (int)((k + 255) / 256), 0, 0};
     if (k == 0) packed = 0;  // as kq_mxfp4_linear
     const int s_align = packed ? 16 : 4;
-    const bool big = k > 0 && (packed || k % 128 == 0) && aligned(scales_a, s_align) && aligned(scales_g, s_align) &&
+    const bool big = k > 256 && (packed || k % 128 == 0) && aligned(scales_a, s_align) && aligned(scales_g, s_align) &&
                      aligned(scales_u, s_align);
     const GatedKernel kernel = kq::linear::choose_gated_kernel(m, n, g.stages, packed != 0, big, kqhost::compute_units());
     if (kernel == kGatedTile256)
-        return kqhost::gemm256_gated(codes_a, scales_a, codes_g, scales_g, packed, k, type, ep, stream);
+        return type == KQ_BF16 ? kqhost::gated256_bf16(codes_a, scales_a, codes_g, scales_g, packed, k, ep, stream)
+                               : kqhost::gated256_f32(codes_a, scales_a, codes_g, scales_g, packed, k, ep, stream);
     return type == KQ_BF16 ? launch_gated<uint16_t>(kernel, codes_a, scales_a, codes_g, scales_g, packed, g, ep, stream)
                            : launch_gated<float>(kernel, codes_a, scales_a, codes_g, scales_g, packed, g, ep, stream);
 }

@@ -89,12 +89,25 @@ def test_many_rows(torch, kq, m, n, k):
             check(torch, kq, m, n, k, ACTS[(m + k // 32 + i + j) % 5], dt, packed, bias=j == 0, seed=m, pad=(0, 8, 5)[(m + j) % 3])
 
 
+# the 256 x 128 kernel: one tile per workgroup and several, whole ones and halves, and a workgroup that goes from one kind
+# to the other; two stages of k, odd and even numbers of them, a partial one
+BIG = [(4000, 5000, 1024), (4100, 5501, 512), (4097, 11001, 768), (2048, 5504, 2048), (5000, 8193, 1280), (1024, 5504, 4096),
+       (2500, 6401, 1152), (8192, 2752, 896), (1030, 11008, 2304), (1000, 2751, 2048), (768, 4096, 4096), (2500, 7000, 1920), (4096, 4224, 512)]
+
+
+@pytest.mark.parametrize("m,n,k", BIG)
+def test_large_tiles(torch, kq, m, n, k):
+    for i, packed in enumerate([False, True] if k % 256 == 0 else [False]):
+        for j, dt in enumerate(("bfloat16", "float32")):
+            check(torch, kq, m, n, k, ACTS[(m // 100 + k // 128 + 2 * i + j) % 5], dt, packed, bias=(i + j) % 2 == 0, seed=n,
+                  pad=8 * (n % 8 == 0))
+
+
 @pytest.mark.parametrize("name", ACTS)
 @pytest.mark.parametrize("dt", ["bfloat16", "float32"])
 def test_activations(torch, kq, name, dt):
     """Every activation over a wide range of g (the bias spreads it), on kernels for few and for many rows."""
-    for m in (5, 300, 2100):
-        n, k = 1024, 256
+    for m, n, k in ((5, 1024, 256), (300, 1024, 256), (2100, 1024, 256), (4096, 4096, 512)):
         ops = [operand(torch, kq, r, k, i, s) for i, (r, s) in enumerate(((m, 1.0), (n, k ** -0.5), (n, k ** -0.5)))]
         bg = torch.linspace(-12, 12, n, device="cuda")
         flat = [t for o in ops for t in o]
