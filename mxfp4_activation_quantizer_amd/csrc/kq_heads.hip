@@ -1039,6 +1039,9 @@ kq_status launch_backward(const Tensor &dy, const Tensor &x, const Tensor &dx, c
         // a part's tokens in as few blocks as two tables of 32 KB allow (one of 32 tokens is level with four of 8)
         const int64_t per = (g.m + parts - 1) / parts;
         int64_t want = kBackTable / (rope.half + V);
+        // a block's passes times `per` stay below 2^32 (Divisor)
+        const int64_t per_token = a.per.n > b.per.n ? a.per.n : b.per.n;
+        if (want * per_token > ((int64_t)1 << 32) / per_token) want = ((int64_t)1 << 32) / (per_token * per_token);
         if (want < 1) want = 1;
         const int64_t rounds = per > want ? (per + want - 1) / want : 1;
         g.tokens = (int)((per + rounds - 1) / rounds);

@@ -280,6 +280,65 @@ def test_other_streams_and_graphs(torch, kq):
         assert all(torch.equal(a, b) for a, b in zip(out, want)), step
 
 
+@pytest.mark.parametrize("m", [5, 8])
+def test_most_heads(torch, kq, m):
+    """As many heads as there can be, one wave each, several tokens to a workgroup: their passes are divided into tokens."""
+    g = torch.Generator("cuda").manual_seed(m)
+    heads, d = 65536, 34
+    x, dy = (torch.randn(m, heads, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    kw = dict(eps=EPS, **call_args(make_rope(torch, g, m, 34, False)))
+    y, (dx, dq, dk) = kq.headnorm_rope(x, **kw), kq.headnorm_rope_backward(dy, x, q_heads=heads - 1, **kw)
+    parts = []
+    for i in range(0, heads, 8192):
+        a, b = x[:, i:i + 8192], dy[:, i:i + 8192]
+        da, q, k = kq.headnorm_rope_backward(b, a, q_heads=min(8192, heads - 1 - i), **kw)
+        assert torch.equal(y[:, i:i + 8192], kq.headnorm_rope(a, **kw)), i
+        assert torch.equal(dx[:, i:i + 8192], da), i
+        parts.append((q.double(), k.double()))
+    # the same terms in another order: chains of at most m heads / 8 of them and the joins, in both
+    e, h = dy.float().abs(), x.float().abs()
+    size = ((e + e.roll(17, -1)) * h * h.square().mean(-1, keepdim=True).rsqrt()).sum((0, 1), dtype=torch.float64)
+    for got, want in zip((dq, dk), zip(*parts)):
+        assert bool(((got - sum(want)).abs() <= 2 * (m * heads / 8 + 64) * 2.0 ** -24 * size).all())
+    alone = kq.headnorm_rope_backward(dy[:, -1:], x[:, -1:], q_heads=0, **kw)[2]
+    assert bool(((dk - alone).abs() <= 64 * 2.0 ** -24 * (dy[:, -1].abs().float() * 8).sum(0).max()).all())
+
+
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (20, 8, True), (30, 30, False)])
+@pytest.mark.parametrize("heads", [8, 1])
+def test_strides_past_a_pass(torch, kq, d, rot, inter, heads):
+    """Heads (or tokens) so far from each other that the lanes of a wave, on several at once, would not reach the last of
+    them with 31 bits."""
+    g = torch.Generator("cuda").manual_seed(d)
+    n, gap = 8, -(-(1 << 30) // (2 if d == 30 else 6))
+    gap += -gap % 128
+    m = 3 if heads == 8 else n
+
+    def far():
+        flat = torch.empty((n - 1) * gap + 3 * d + 128, dtype=torch.bfloat16, device="cuda")
+        return flat.as_strided((m, heads, d), (d, gap, 1) if heads == 8 else (gap, d, 1))
+
+    x, dy, out, dx = (far() for _ in range(4))
+    x.copy_(make_heads(torch, g, m, heads, d, torch.bfloat16))
+    dy.copy_(torch.randn(m, heads, d, generator=g, device="cuda"))
+    rope = make_rope(torch, g, m, rot, inter)
+    kw = dict(eps=EPS, **call_args(rope))
+    kq.headnorm_rope(x, out=out, **kw)
+    want, tol = ref.forward(x, None, None, heads, EPS, rope)
+    layer_ref.assert_near(out, want, tol, "y")
+    _, dq, _ = kq.headnorm_rope_backward(dy, x, dx=dx, **kw)
+    want, tol = ref.backward(dy, x, None, None, heads, EPS, rope)
+    layer_ref.assert_near(dx, want[0], tol[0], "dx")
+    layer_ref.assert_near(dq, want[1], tol[1], "dweight")
+    if d % 32 == 0:
+        codes = torch.zeros(2, m, heads, d // 2, dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(2, m, heads, d // 32, dtype=torch.uint8, device="cuda")
+        near = x.contiguous()
+        for i, t in enumerate((x, near)):
+            kq.cache_write_mxfp4(torch.arange(m, device="cuda"), v=t, codes_v=codes[i], scales_v=scales[i])
+        assert torch.equal(codes[0], codes[1]) and torch.equal(scales[0], scales[1])
+
+
 def test_many_tokens_and_far_addresses(torch, kq):
     """Rows past 2^31 bytes of each tensor, in heads side by side and in tokens side by side."""
     m, heads, d = 40000, 17, 4 * 256  # 1.4 GB a tensor in bf16, and 2.8 with the stride below
