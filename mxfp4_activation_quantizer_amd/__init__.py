@@ -11,7 +11,9 @@ with the MXFP4 format of Sec. 4.1 / Appendix D.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import numpy as np
 
@@ -876,14 +878,20 @@ def _packed_scales(t, name, rows, k, index, packed):
     return _bytes(t, name, rows, k // 32, index)
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(name, rows, cols):
+    n = ctypes.c_int64(0)
+    _check(name, getattr(lib(), name)(rows, cols, ctypes.byref(n)))
+    return n.value
+
+
 def _workspace(name, rows, cols, workspace, like):
     """(tensor, its bytes) for a call that sums over rows: the caller's, or one of this call's own on
     the device of ``like``."""
-    n = ctypes.c_int64(0)
-    _check(name, getattr(lib(), name)(rows, cols, ctypes.byref(n)))
+    n = _workspace_bytes(name, rows, cols)
     if workspace is None:
-        workspace = like.new_empty(n.value, dtype=_torch().uint8)
-    elif workspace.device != like.device or not workspace.is_contiguous():
+        return like.new_empty(n, dtype=_torch().uint8), n
+    if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
     return workspace, workspace.numel() * workspace.element_size()
 
@@ -1204,10 +1212,13 @@ def mxfp4_gated_linear_backward(dout, g, u, act="silu", dg=None, du=None, dbias_
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}  # kq_rope_scaling
 
 
-class _Rope(ctypes.Structure):  # kq_rope
+class _Rope(ctypes.Structure):  # kq_rope, for calls of lib() itself
     _fields_ = [("positions", ctypes.c_void_p), ("freq", ctypes.c_void_p), ("rot", ctypes.c_int64),
                 ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float), ("axes", ctypes.c_int),
                 ("axis_pairs", ctypes.c_int64 * 4)]
+
+
+_ROPE = struct.Struct("@PPqifi4xqqqq")  # its bytes, a third of the time of filling in a _Rope
 
 
 def rope_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, original=0.0, low=1.0, high=32.0):
@@ -1225,7 +1236,7 @@ def rope_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, original=0.
 
 
 def _rope(positions, freq, m, index, interleaved, amplitude, axis_pairs):
-    """kq_rope of the rotation's arguments on device ``index``, by reference (freq None: NULL)."""
+    """kq_rope of the rotation's arguments on device ``index``, as bytes (freq None: NULL)."""
     if freq is None:
         return None
     torch = _torch()
@@ -1243,8 +1254,8 @@ def _rope(positions, freq, m, index, interleaved, amplitude, axis_pairs):
     pairs = tuple(axis_pairs) if axis_pairs is not None else (n,)
     if len(pairs) != axes:
         raise ValueError("axis_pairs must name the pairs of each of the %d axes" % axes)
-    return ctypes.byref(_Rope(positions.data_ptr(), freq.data_ptr(), 2 * n, 1 if interleaved else 0, amplitude, axes,
-                              pairs))
+    return _ROPE.pack(positions.data_ptr(), freq.data_ptr(), 2 * n, 1 if interleaved else 0, amplitude, axes,
+                      *pairs, *(0,) * (4 - axes))
 
 
 def _heads(t, name, dtype, index, shape=None):

@@ -160,3 +160,9 @@ def test_the_code_check_rejects_mistakes(orc):
             c[4, 7] ^= 1 if mistake == "code" else 8
         with pytest.raises(AssertionError):
             ref.assert_codes_near(c, s, y, tol)
+
+
+def test_packed_rotation():
+    """The binding's bytes of a kq_rope are the structure's."""
+    r = kq._Rope(1 << 40, 1 << 41, 64, 1, 1.5, 3, (20, 10, 2, 0))
+    assert kq._ROPE.pack(1 << 40, 1 << 41, 64, 1, 1.5, 3, 20, 10, 2, 0) == bytes(r)
