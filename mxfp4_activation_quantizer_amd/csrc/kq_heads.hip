@@ -165,6 +165,23 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
+// Sum over the lanes at the same place of every head of the wave. (Through LDS, as __shfl_xor goes, the gradients of
+// both weights took 2.5 us more: one token of 24 x 64 8.5 instead of 6.0.)
+template <int LG>
+__device__ __forceinline__ float slots_sum(float v) {
+    if (LG <= 32) {
+        const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+    }
+    if (LG <= 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    }
+    if (LG <= 8) v += moved<0x128>(v);  // 8 lanes on in a ring of 16
+    if (LG <= 4) v += moved<0x124>(v);  // and 4
+    return v;
+}
+
 // Where unit u of a head lies: its first piece at channel a, its second at b, whether they exist, and the pairs that
 // they (each by itself, for pairs inside a piece) start with; `half` for none.
 struct Place {
@@ -596,9 +613,7 @@ __global__ __launch_bounds__(kBackThreads) void backward_kernel(const T *dY, int
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    float v = k ? acc1[u][b][e] : acc0[u][b][e];
-#pragma unroll
-                    for (int o = LG; o < 64; o *= 2) v += __shfl_xor(v, o);
+                    const float v = slots_sum<LG>(k ? acc1[u][b][e] : acc0[u][b][e]);
                     if (slot == 0) join[(wave * 2 + k) * kWave + ((u * 2 + b) * V + e) * LG + sub] = v;
                 }
     __syncthreads();
@@ -892,10 +907,10 @@ kq_status read_rope(const kq_rope *r, int64_t m, int64_t d, Rope &out) {
     return KQ_OK;
 }
 
-// Channels per piece: 8 or 4 where the halves of the rotated part (the whole of it with neighbouring pairs), the head
-// and every address are multiples of it.
-int piece_width(int es, const Rope &rope, bool inter, std::initializer_list<Tensor> tensors) {
-    for (int v = 8; v >= 4; v /= 2) {
+// Channels per piece, at most `most`: 8 or 4 where the halves of the rotated part (the whole of it with neighbouring
+// pairs), the head and every address are multiples of it.
+int piece_width(int most, int es, const Rope &rope, bool inter, std::initializer_list<Tensor> tensors) {
+    for (int v = most; v >= 4; v /= 2) {
         const int bytes = v * es < 16 ? v * es : 16;
         bool ok = rope.d % v == 0 && (inter ? 2 * rope.half : rope.half) % v == 0;
         for (const Tensor &t : tensors)
@@ -915,10 +930,11 @@ template <int V, int LG, int U>
 struct Form {
     static constexpr int kV = V, kLG = LG, kU = U;
 };
-template <class F>
+template <int MOST, class F>
 void choose_form(int v, int units, F f) {
-    if (v == 8) {
-        if (units <= 4) f(Form<8, 4, 1>());
+    if (MOST == 8 && v == 8) {
+        if constexpr (MOST < 8) return;
+        else if (units <= 4) f(Form<8, 4, 1>());
         else if (units <= 8) f(Form<8, 8, 1>());
         else if (units <= 16) f(Form<8, 16, 1>());
         else if (units <= 32) f(Form<8, 32, 1>());
@@ -958,22 +974,22 @@ bool offsets_fit(const kq::heads::Kind &k, int hp, int d, int es, std::initializ
     return true;
 }
 
-// f(V, LG, U) for these tensors, a first kind of n0 heads and a second of n1: the fastest form whose offsets fit. A
-// whole wave per head has none but its own channels'.
-template <class F>
+// f(V, LG, U) for these tensors, a first kind of n0 heads and a second of n1: the fastest form of pieces of at most MOST
+// channels whose offsets fit. A whole wave per head has none but its own channels'.
+template <int MOST, class F>
 kq_status choose(int es, const Rope &rope, bool inter, int64_t n0, int64_t n1, std::initializer_list<Tensor> tensors, F f) {
-    const int v = piece_width(es, rope, inter, tensors), units = units_of(rope, inter, v);
+    const int v = piece_width(MOST, es, rope, inter, tensors), units = units_of(rope, inter, v);
     kq_status status = KQ_OK;
     auto go = [&](auto form) {
         constexpr int hp = 64 / decltype(form)::kLG;
         status = f(form, kind_of(n0, 0, hp), kind_of(n1, n0, hp));
     };
     bool fits = true;
-    choose_form(v, units, [&](auto form) {
+    choose_form<MOST>(v, units, [&](auto form) {
         constexpr int hp = 64 / decltype(form)::kLG;
         fits = offsets_fit(kind_of(n0, 0, hp), hp, rope.d, es, tensors) && offsets_fit(kind_of(n1, n0, hp), hp, rope.d, es, tensors);
     });
-    choose_form(v, fits ? units : v == 8 ? 64 : v == 4 ? (units > 64 ? units : 64) : (units > 64 ? units : 64), go);
+    choose_form<MOST>(v, fits ? units : v == 8 ? 64 : v == 4 ? (units > 64 ? units : 64) : (units > 64 ? units : 64), go);
     return status;
 }
 
@@ -1002,10 +1018,16 @@ Plan plan_of(int64_t m, const kq::heads::Kind &a, const kq::heads::Kind &b, int 
     return p;
 }
 
+// Pieces of 16 bytes: two loads side by side for one of 32 take each line twice (fp32 8192 x 40 x 128 71.0 us with 8
+// channels and 64.2 with 4, its gradients 112 and 107; 4096 x 32 x 72 19.7 and 18.4, 32.5 and 27.6), and past the caches
+// their non-temporal form (59.6, 101).
+template <class T>
+constexpr int kMost = 16 / (int)sizeof(T);
+
 template <class T>
 kq_status launch_forward(const Tensor &x, const Tensor &y, const float *w0, const float *w1, int64_t heads, int64_t q_heads,
                          Geom g, const Rope &rope, bool inter, kq_stream_t stream) {
-    return choose(sizeof(T), rope, inter, q_heads, heads - q_heads, {x, y}, [&](auto form, auto a, auto b) {
+    return choose<kMost<T>>(sizeof(T), rope, inter, q_heads, heads - q_heads, {x, y}, [&](auto form, auto a, auto b) {
         constexpr int V = decltype(form)::kV, LG = decltype(form)::kLG, U = decltype(form)::kU;
         const Plan p = plan_of(g.m, a, b, rope.half, 64 / LG);
         if (p.blocks >= (int64_t)1 << 24) return KQ_ERR_UNSUPPORTED;
@@ -1014,7 +1036,7 @@ kq_status launch_forward(const Tensor &x, const Tensor &y, const float *w0, cons
         g.tokens = p.tokens;
         const size_t lds = (size_t)p.tokens * (rope.half + V) * sizeof(float2);
         auto go = [&](auto I, auto NT) {
-            hipLaunchKernelGGL((kq::heads::forward_kernel<T, V, LG, U, I(), V == 8 && NT()>),
+            hipLaunchKernelGGL((kq::heads::forward_kernel<T, V, LG, U, I(), V * sizeof(T) == 16 && NT()>),
                                dim3((unsigned)p.blocks, (unsigned)p.splits), dim3(kq::heads::kThreads), lds,
                                (hipStream_t)stream, (const T *)x.p, x.ld, x.hs, w0, w1, g, rope,
                                (T *)const_cast<void *>(y.p), y.ld, y.hs);
@@ -1033,7 +1055,7 @@ kq_status launch_backward(const Tensor &dy, const Tensor &x, const Tensor &dx, c
                           int64_t heads, int64_t q_heads, Geom g, const Rope &rope, bool inter, int parts, float *p0,
                           float *p1, kq_stream_t stream) {
     const Tensor &x_or = g.norm ? x : dy;
-    return choose(sizeof(T), rope, inter, q_heads, heads - q_heads, {dy, x_or, dx}, [&](auto form, auto a, auto b) {
+    return choose<kMost<T>>(sizeof(T), rope, inter, q_heads, heads - q_heads, {dy, x_or, dx}, [&](auto form, auto a, auto b) {
         constexpr int V = decltype(form)::kV, LG = decltype(form)::kLG, U = decltype(form)::kU;
         constexpr int waves = kq::heads::kBackWaves;
         // a part's tokens in as few blocks as two tables of 32 KB allow (one of 32 tokens is level with four of 8)
@@ -1050,7 +1072,7 @@ kq_status launch_backward(const Tensor &dy, const Tensor &x, const Tensor &dx, c
         const size_t tables = 2 * (size_t)g.tokens * (rope.half + V) * sizeof(float2);
         const size_t join = (size_t)waves * 2 * LG * U * 2 * V * sizeof(float);
         auto go = [&](auto I, auto NT) {
-            hipLaunchKernelGGL((kq::heads::backward_kernel<T, V, LG, U, I(), V == 8 && NT()>), dim3((unsigned)parts),
+            hipLaunchKernelGGL((kq::heads::backward_kernel<T, V, LG, U, I(), V * sizeof(T) == 16 && NT()>), dim3((unsigned)parts),
                                dim3(kq::heads::kBackThreads), tables > join ? tables : join, (hipStream_t)stream,
                                (const T *)dy.p, dy.ld, dy.hs, (const T *)x.p, x.ld, x.hs, w0, w1, g, rope,
                                (T *)const_cast<void *>(dx.p), dx.ld, dx.hs, parts, p0, p1);
@@ -1067,7 +1089,7 @@ kq_status launch_backward(const Tensor &dy, const Tensor &x, const Tensor &dx, c
 template <class T>
 kq_status launch_write(const Tensor &k, const Tensor &v, const float *w, int64_t k_heads, int64_t v_heads, Geom g,
                        const Rope &rope, bool inter, const kq::heads::Cache &cache, kq_stream_t stream) {
-    return choose(sizeof(T), rope, inter, k_heads, v_heads, {k, v}, [&](auto form, auto a, auto b) {
+    return choose<8>(sizeof(T), rope, inter, k_heads, v_heads, {k, v}, [&](auto form, auto a, auto b) {
         constexpr int V = decltype(form)::kV, LG = decltype(form)::kLG, U = decltype(form)::kU;
         const Plan p = plan_of(g.m, a, b, rope.half, 64 / LG);
         if (p.blocks >= (int64_t)1 << 24) return KQ_ERR_UNSUPPORTED;
