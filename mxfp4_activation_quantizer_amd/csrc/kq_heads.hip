@@ -932,14 +932,17 @@ struct Form {
 };
 template <int MOST, class F>
 void choose_form(int v, int units, F f) {
-    if (MOST == 8 && v == 8) {
-        if constexpr (MOST < 8) return;
-        else if (units <= 4) f(Form<8, 4, 1>());
-        else if (units <= 8) f(Form<8, 8, 1>());
-        else if (units <= 16) f(Form<8, 16, 1>());
-        else if (units <= 32) f(Form<8, 32, 1>());
-        else f(Form<8, 64, 1>());
-    } else if (v == 4) {
+    if constexpr (MOST == 8) {
+        if (v == 8) {
+            if (units <= 4) f(Form<8, 4, 1>());
+            else if (units <= 8) f(Form<8, 8, 1>());
+            else if (units <= 16) f(Form<8, 16, 1>());
+            else if (units <= 32) f(Form<8, 32, 1>());
+            else f(Form<8, 64, 1>());
+            return;
+        }
+    }
+    if (v == 4) {
         if (units <= 8) f(Form<4, 8, 1>());
         else if (units <= 16) f(Form<4, 16, 1>());
         else if (units <= 32) f(Form<4, 32, 1>());
