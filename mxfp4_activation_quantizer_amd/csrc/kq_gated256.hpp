@@ -11,6 +11,11 @@
 // stage; the epilogue, on outputs gated in registers and staged once, in their own type, has a little LDS of its own.
 // Stores are counted with the loads and come back in their order, so that a wait for a load waits for the stores before
 // it: with both stages asked for in front of them, an epilogue's stores have two stages' time to leave.
+//
+// 8192 x 11008 x 4096 bf16 silu, packed scales: 343 to 356 us with the clock the board settles at (4.1 to 4.3 PFLOP/s; FP4
+// matrix instructions alone 5.5), 410 as one launch of a workgroup per tile. What is left over the matrix unit's time is 4 us
+// of epilogue a tile, 32 outputs gated per lane and 4 KB block with nothing to cover them: a second set of sums does not fit
+// the registers. Cached stores in place of non-temporal ones: 374 us.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -360,6 +360,10 @@ struct Weights {
 // X and Y may be the same memory: a lane has read all of its pieces before it writes any of them.
 // A workgroup takes the heads of a few tokens, a wave G passes in turn, each one's next loads asked for when it is
 // done. The table of angles is made once per token and read back by every head.
+//
+// Bound by HBM once it is large: 8192 x 40 x 128 bf16 32.4 us (168 MB, 5.2 TB/s; a 1 GiB copy 5.0), fp32 59.5; one
+// token of 40 x 128 3.3, a launch and the latency of its positions, frequencies and heads. A head that does not fill
+// its lanes leaves some idle: 4096 x 32 x 72 fp32 (9 of 16 lanes) 18.4 us, 4.1 TB/s.
 template <class T, int V, int LG, int U, bool INTER, bool NT>
 __global__ __launch_bounds__(kThreads) void forward_kernel(const T *X, int64_t ldx, int64_t hsx,
                                                            const float *__restrict__ w0, const float *__restrict__ w1,
@@ -469,6 +473,10 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(const T *X, int64_t l
 //   dx = s (g - h sum(g h) / d), dw = sum of e h over the rows of that weight.
 // Workgroup p of `parts` takes the blocks of tokens p, p + parts, ...; its lanes keep their channels of both dw in
 // registers, and row p of the partial sums gets them at the end, the waves joined in their order. dX may be dY or X.
+//
+// Bound by HBM: 8192 x 40 x 128 bf16 53 us and 4 for the partial sums' (252 MB, 4.7 TB/s), 4096 x 32 x 72 fp32 25 and 4.
+// Parts of 512 threads (768 are level, 1024 take 120 us) with one pass of each kind in flight (two and three are
+// level). Both dweights cost 1.9 us at one token (the joins) and 4 where a second launch adds the parts.
 template <class T, int V, int LG, int U, bool INTER, bool NT>
 __global__ __launch_bounds__(kBackThreads) void backward_kernel(const T *dY, int64_t lddy, int64_t hsdy, const T *X,
                                                                 int64_t ldx, int64_t hsx,
@@ -633,6 +641,9 @@ __global__ __launch_bounds__(kBackThreads) void backward_kernel(const T *dY, int
 // every four lanes' first pieces, and their second ones, are a block of 32 channels each (V = 8, and the two pieces of
 // a unit a multiple of 32 channels apart), so they are quantized where they are. Otherwise a wave's heads meet in LDS,
 // where four lanes take each block.
+//
+// Bound by HBM: 8192 x (8 + 8) x 128 bf16 11.0 us, a launch's 2 and 42 MB at 4.7 TB/s, into slots in any order (8.8 with none
+// written); 64 tokens 3.1. The values' first loads beside the keys' are slower (11.7).
 struct Cache {
     const int64_t *slots;  // [m]
     int64_t n;             // slots of the cache
@@ -786,6 +797,8 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(const T *__restri
 // Rows of the cache decoded: a lane takes 8 channels (a dword of codes) of R places of the workgroup's tokens (or
 // of its part of one token), all of whose loads are in flight together. A row whose slot lies outside the cache is
 // zeros.
+// Eight places hide the two dependent loads (slot, then codes and scale): 131072 x 8 x 128 bf16 49.9 us (340 MB, 6.8 TB/s
+// with the cache partly in the Infinity Cache), 97 with one. One place for calls that would not fill the card: 509 tokens 2.4.
 struct Read {
     int64_t m, n;             // tokens, slots
     int tokens, pieces;       // tokens per workgroup; 8-channel pieces of a token

@@ -249,7 +249,8 @@ __global__ __launch_bounds__(64 * WK) void product_kernel(const uint8_t *__restr
 // level).
 //
 // With GatedEpi (FB = 2) half of the staged rows of W are the first weight's and half the second's, and each wave
-// multiplies one fragment of both, so that both sums of an output are the same lane's.
+// multiplies one fragment of both, so that both sums of an output are the same lane's. One token of n = 11008, k = 4096
+// takes 11.4 us so (47.9 MB of weights, 4.2 TB/s), 256 rows 32.2 with four stages and 26.6 with two.
 template <class T, int FA, int FB, int N, class E>
 __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict__ ca, const uint8_t *__restrict__ sa,
                                                    const uint8_t *__restrict__ cw, const uint8_t *__restrict__ sw,
@@ -560,6 +561,8 @@ __global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO,
 
 // Backward of the gated epilogue, as backward_kernel: three reads and two writes per element, and both biases' sums.
 // The outputs may be inputs: a lane has read an element of each before it writes any.
+// 8192 x 11008 bf16 silu 158 us (902 MB, 5.7 TB/s) and 6 for the sums of 256 parts; 301 x 4607 fp32, element by element,
+// 9.6 and 4: a launch, the latency of one row a wave, and 2.8 MB of partial sums.
 template <class T, bool NT, bool VEC>
 __global__ __launch_bounds__(256) void gated_backward_kernel(const T *dO, int64_t lddo,
                                                              const T *G, int64_t ldg,
