@@ -1105,6 +1105,14 @@ def mxfp4_linear_backward(dout, z=None, act="none", dz=None, dbias=None, workspa
     return dz, dbias
 
 
+def _sums(t, name, d, index, like):
+    """(fp32 vector of length d, its pointer): t, or one of this call's own on the device of ``like``."""
+    if t is None:
+        t = like.new_empty(d, dtype=_torch().float32)
+        return t, t.data_ptr()
+    return t, _vector(t, name, d, index)
+
+
 def mxfp4_gated_linear(codes_a, scales_a, codes_g, scales_g, codes_u, scales_u, bias_g=None, bias_u=None, act="silu",
                        out=None, g=None, u=None, bf16=True, packed=False, want_pre=False, stream=None):
     """act(deq(A) deq(Wg)^T + bias_g) * (deq(A) deq(Wu)^T + bias_u) from MXFP4 operands, bf16 (or fp32) [m][n]: both
@@ -1133,7 +1141,7 @@ def mxfp4_gated_linear(codes_a, scales_a, codes_g, scales_g, codes_u, scales_u, 
     n, k = sg[0], 2 * kb
     dtype = torch.bfloat16 if bf16 else torch.float32
     if out is None:
-        out, ldo = codes_a.new_empty((m, n), dtype=dtype), n
+        out, ldo = codes_a.new_empty(m, n, dtype=dtype), n
     else:
         ldo = _matrix(out, "out", dtype, index, m, n)
     gp = up = None
@@ -1141,9 +1149,9 @@ def mxfp4_gated_linear(codes_a, scales_a, codes_g, scales_g, codes_u, scales_u, 
     want_pre = want_pre or g is not None or u is not None
     if want_pre:
         if g is None:
-            g = codes_a.new_empty((m, n), dtype=dtype)
+            g = codes_a.new_empty(m, n, dtype=dtype)
         if u is None:
-            u = codes_a.new_empty((m, n), dtype=dtype)
+            u = codes_a.new_empty(m, n, dtype=dtype)
         ldg, ldu = _matrix(g, "g", dtype, index, m, n), _matrix(u, "u", dtype, index, m, n)
         gp, up = g.data_ptr(), u.data_ptr()
     _check("kq_mxfp4_gated_linear",
@@ -1167,7 +1175,6 @@ def mxfp4_gated_linear_backward(dout, g, u, act="silu", dg=None, du=None, dbias_
     g, u: the two products (mxfp4_gated_linear's). ``biases=False``: None for the sums. dg and du may be halves of
     one [m][2 n] tensor. The operands' gradients are dg deq(Wg) + du deq(Wu), dg^T deq(A) and du^T deq(A).
     """
-    torch = _torch()
     bf16, index = _activation(dout, "dout")
     here = _elsewhere(index, stream)
     if here is not None:
@@ -1180,27 +1187,25 @@ def mxfp4_gated_linear_backward(dout, g, u, act="silu", dg=None, du=None, dbias_
     m, n = dout.shape
     ldg, ldu = _matrix(g, "g", dtype, index, m, n), _matrix(u, "u", dtype, index, m, n)
     if dg is None:
-        dg, lddg = dout.new_empty((m, n)), n
+        dg, lddg = dout.new_empty(m, n), n
     else:
         lddg = _matrix(dg, "dg", dtype, index, m, n)
     if du is None:
-        du, lddu = dout.new_empty((m, n)), n
+        du, lddu = dout.new_empty(m, n), n
     else:
         lddu = _matrix(du, "du", dtype, index, m, n)
     ws, ws_bytes = None, 0
+    gp = up = None
     if biases:
-        if dbias_g is None:
-            dbias_g = dout.new_empty(n, dtype=torch.float32)
-        if dbias_u is None:
-            dbias_u = dout.new_empty(n, dtype=torch.float32)
+        dbias_g, gp = _sums(dbias_g, "dbias_g", n, index, dout)
+        dbias_u, up = _sums(dbias_u, "dbias_u", n, index, dout)
         ws, ws_bytes = _workspace("kq_mxfp4_gated_linear_backward_workspace_bytes", m, n, workspace, dout)
     elif dbias_g is not None or dbias_u is not None:
         raise ValueError("biases=False computes neither dbias_g nor dbias_u")
     _check("kq_mxfp4_gated_linear_backward",
            lib().kq_mxfp4_gated_linear_backward(dout.data_ptr(), lddo, g.data_ptr(), ldg, u.data_ptr(), ldu, int(bf16), m,
                                                 n, ACTS[act], dg.data_ptr(), lddg, du.data_ptr(), lddu,
-                                                _vector(dbias_g, "dbias_g", n, index),
-                                                _vector(dbias_u, "dbias_u", n, index),
+                                                gp, up,
                                                 ws.data_ptr() if ws is not None else None, ws_bytes,
                                                 _current_stream(index)))
     return dg, du, dbias_g, dbias_u
@@ -1296,7 +1301,7 @@ def headnorm_rope(x, positions=None, freq=None, weight_q=None, weight_k=None, q_
     ldx, hsx = _heads(x, "x", x.dtype, index)
     m, heads, d = x.shape
     if out is None:
-        out, ldy, hsy = x.new_empty((m, heads, d)), heads * d, d
+        out, ldy, hsy = x.new_empty(m, heads, d), heads * d, d
     else:
         ldy, hsy = _heads(out, "out", x.dtype, index, x.shape)
     _check("kq_headnorm_rope",
@@ -1317,7 +1322,6 @@ def headnorm_rope_backward(dy, x=None, positions=None, freq=None, weight_q=None,
     others. workspace: at least kq_headnorm_rope_backward_workspace_bytes bytes, or None
     (allocated for this call). The rest as headnorm_rope.
     """
-    torch = _torch()
     bf16, index = _activation(dy, "dy")
     here = _elsewhere(index, stream)
     if here is not None:
@@ -1332,15 +1336,14 @@ def headnorm_rope_backward(dy, x=None, positions=None, freq=None, weight_q=None,
             raise ValueError("x is required with norm=True")
         ldx, hsx = _heads(x, "x", dy.dtype, index, dy.shape)
     if dx is None:
-        dx, lddx, hsdx = dy.new_empty((m, heads, d)), heads * d, d
+        dx, lddx, hsdx = dy.new_empty(m, heads, d), heads * d, d
     else:
         lddx, hsdx = _heads(dx, "dx", dy.dtype, index, dy.shape)
     ws, ws_bytes = None, 0
+    qp = kp = None
     if params and norm:
-        if dweight_q is None:
-            dweight_q = dy.new_empty(d, dtype=torch.float32)
-        if dweight_k is None:
-            dweight_k = dy.new_empty(d, dtype=torch.float32)
+        dweight_q, qp = _sums(dweight_q, "dweight_q", d, index, dy)
+        dweight_k, kp = _sums(dweight_k, "dweight_k", d, index, dy)
         ws, ws_bytes = _workspace("kq_headnorm_rope_backward_workspace_bytes", m, d, workspace, dy)
     elif dweight_q is not None or dweight_k is not None:
         raise ValueError("params=False and norm=False compute no dweight")
@@ -1351,8 +1354,7 @@ def headnorm_rope_backward(dy, x=None, positions=None, freq=None, weight_q=None,
                                            _vector(weight_k, "weight_k", d, index),
                                            heads if q_heads is None else q_heads, eps,
                                            _rope(positions, freq, m, index, interleaved, amplitude, axis_pairs),
-                                           dx.data_ptr(), lddx, hsdx, _vector(dweight_q, "dweight_q", d, index),
-                                           _vector(dweight_k, "dweight_k", d, index),
+                                           dx.data_ptr(), lddx, hsdx, qp, kp,
                                            ws.data_ptr() if ws is not None else None, ws_bytes,
                                            _current_stream(index)))
     return dx, dweight_q, dweight_k
@@ -1434,7 +1436,7 @@ def cache_read_mxfp4(slots, codes, scales, bf16=True, out=None, stream=None):
     dtype = torch.bfloat16 if bf16 else torch.float32
     m = slots.numel()
     if out is None:
-        out, ldy, hsy = codes.new_empty((m, heads, d), dtype=dtype), heads * d, d
+        out, ldy, hsy = codes.new_empty(m, heads, d, dtype=dtype), heads * d, d
     else:
         ldy, hsy = _heads(out, "out", dtype, index, (m, heads, d))
     _check("kq_cache_read_mxfp4",
