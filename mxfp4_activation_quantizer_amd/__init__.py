@@ -1384,7 +1384,7 @@ def cache_write_mxfp4(slots, k=None, codes_k=None, scales_k=None, v=None, codes_
                       axis_pairs=None, stream=None):
     """Quantizes keys and values (bf16 or fp32 [m][heads][d]; either may be None) into their cache of MXFP4: codes
     uint8 [slots][heads][d/2] and scales uint8 [slots][heads][d/32]. Token i goes to slot slots[i] (int64 [m]);
-    one that is negative or past the cache is left out. Keys are normed (``norm``, with weight) and rotated
+    one that is negative or past the cache is left out, and two tokens must not share one. Keys are normed (``norm``, with weight) and rotated
     first, as by headnorm_rope, without a rounding in between; values go in as they are.
     """
     one = k if k is not None else v

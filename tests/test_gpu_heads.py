@@ -418,6 +418,40 @@ def test_cache_write_and_read(torch, kq, m, heads, d, rot, norm, inter, dtype):
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("heads,d,rot,dtype", [(2, 64, 64, "bfloat16"), (8, 128, 128, "bfloat16"), (3, 96, 32, "float32"),
+                                               (1, 32, 32, "bfloat16")])
+def test_cache_padding_may_hold_anything(torch, kq, heads, d, rot, dtype):
+    """Padding tokens between the others, with NaN and infinities, the least and the greatest positions and slots of every
+    wrong kind: the others' rows are those of a call without them."""
+    g = torch.Generator("cuda").manual_seed(d)
+    m, n = 150, 200
+    k, v = (make_heads(torch, g, m, heads, d, getattr(torch, dtype)) for _ in range(2))
+    slots = torch.randperm(n, generator=torch.Generator().manual_seed(d))[:m].cuda()
+    rope = make_rope(torch, g, m, rot, False)
+    pad = torch.arange(m, device="cuda") % 3 == 1
+    bad = torch.tensor([-1, n, -2 ** 63, 2 ** 63 - 1, 2 ** 32, -(2 ** 32)], device="cuda")
+    slots[pad] = bad[torch.arange(int(pad.sum()), device="cuda") % 6]
+    junk = torch.tensor([math.nan, math.inf, -math.inf, torch.finfo(k.dtype).max], device="cuda").to(k.dtype)
+    for t in (k, v):
+        t[pad] = junk[torch.randint(0, 4, (int(pad.sum()), heads, d), generator=g, device="cuda")]
+    rope["positions"][pad] = torch.tensor([-2 ** 63, 2 ** 63 - 1], device="cuda")[torch.arange(int(pad.sum()), device="cuda") % 2]
+    weight = 1 + 0.1 * torch.randn(d, generator=g, device="cuda")
+
+    def write(keep):
+        codes = torch.full((2, n, heads, d // 2), 0x5A, dtype=torch.uint8, device="cuda")
+        scales = torch.full((2, n, heads, d // 32), 0x5A, dtype=torch.uint8, device="cuda")
+        args = {**call_args(rope), "positions": rope["positions"][keep].contiguous()}
+        kq.cache_write_mxfp4(slots[keep].contiguous(), k=k[keep], codes_k=codes[0], scales_k=scales[0], v=v[keep],
+                             codes_v=codes[1], scales_v=scales[1], norm=True, weight=weight, eps=EPS, **args)
+        return codes, scales
+
+    got, want = write(torch.ones_like(pad)), write(~pad)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # wrong slots read as zeros
+    back = kq.cache_read_mxfp4(slots, got[0][0], got[1][0])
+    assert not back[pad].any() and bool((back[~pad] != 0).any())
+
+
 def test_cache_read_every_scale_and_strides(torch, kq):
     """All scale bytes but NaN's with all codes, the same slot many times, rows apart."""
     codes = torch.arange(256, device="cuda").to(torch.uint8).repeat_interleave(16 * 4).view(256, 4, 16).contiguous()
