@@ -887,10 +887,10 @@ def _workspace_bytes(name, rows, cols):
 
 def _workspace(name, rows, cols, workspace, like):
     """(tensor, its bytes) for a call that sums over rows: the caller's, or one of this call's own on
-    the device of ``like``."""
+    the device of ``like`` (None where it needs none)."""
     n = _workspace_bytes(name, rows, cols)
     if workspace is None:
-        return like.new_empty(n, dtype=_torch().uint8), n
+        return (like.new_empty(n, dtype=_torch().uint8) if n else None), n
     if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
     return workspace, workspace.numel() * workspace.element_size()
@@ -1101,7 +1101,8 @@ def mxfp4_linear_backward(dout, z=None, act="none", dz=None, dbias=None, workspa
     _check("kq_mxfp4_linear_backward",
            lib().kq_mxfp4_linear_backward(dout.data_ptr(), lddo, None if z is None else z.data_ptr(), ldz, int(bf16),
                                           m, n, ACTS[act], dz.data_ptr(), lddz, _vector(dbias, "dbias", n, index),
-                                          ws.data_ptr(), ws_bytes, _current_stream(index)))
+                                          ws.data_ptr() if ws is not None else None, ws_bytes,
+                                          _current_stream(index)))
     return dz, dbias
 
 

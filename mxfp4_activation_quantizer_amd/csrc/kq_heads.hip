@@ -165,23 +165,6 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// Sum over the lanes at the same place of every head of the wave. (Through LDS, as __shfl_xor goes, the gradients of
-// both weights took 2.5 us more: one token of 24 x 64 8.5 instead of 6.0.)
-template <int LG>
-__device__ __forceinline__ float slots_sum(float v) {
-    if (LG <= 32) {
-        const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = __uint_as_float(q[0]) + __uint_as_float(q[1]);
-    }
-    if (LG <= 16) {
-        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-    }
-    if (LG <= 8) v += moved<0x128>(v);  // 8 lanes on in a ring of 16
-    if (LG <= 4) v += moved<0x124>(v);  // and 4
-    return v;
-}
-
 // Where unit u of a head lies: its first piece at channel a, its second at b, whether they exist, and the pairs that
 // they (each by itself, for pairs inside a piece) start with; `half` for none.
 struct Place {

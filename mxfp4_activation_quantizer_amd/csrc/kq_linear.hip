@@ -15,6 +15,7 @@
 #include "kq_dma.hpp"
 #include "kq_epilogue.hpp"
 #include "kq_host.hpp"
+#include "kq_lanesum.hpp"
 #include "kq_tileorder.hpp"
 
 namespace kq {
@@ -559,10 +560,23 @@ __global__ __launch_bounds__(256) void backward_kernel(const T *__restrict__ dO,
     }
 }
 
+// V neighbouring elements, one or whole 16 bytes of them.
+template <class T, int V>
+__device__ __forceinline__ void load_some(const T *p, float (&x)[V]) {
+    if constexpr (V > 1) load_piece(p, x);
+    else if constexpr (sizeof(T) == 2) x[0] = bf16_lo(*p);
+    else x[0] = *p;
+}
+template <class T, int V>
+__device__ __forceinline__ void store_some(T *p, const float (&x)[V]) {
+    if constexpr (V == 1) store1(p, x[0]);
+    else if constexpr (sizeof(T) == 4) *reinterpret_cast<floatx4_t *>(p) = floatx4_t{x[0], x[1], x[2], x[3]};
+    else *reinterpret_cast<u32x4_t *>(p) = u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+}
+
 // Backward of the gated epilogue, as backward_kernel: three reads and two writes per element, and both biases' sums.
 // The outputs may be inputs: a lane has read an element of each before it writes any.
-// 8192 x 11008 bf16 silu 158 us (902 MB, 5.7 TB/s) and 6 for the sums of 256 parts; 301 x 4607 fp32, element by element,
-// 9.6 and 4: a launch, the latency of one row a wave, and 2.8 MB of partial sums.
+// 8192 x 11008 bf16 silu 158 us (902 MB, 5.7 TB/s) and 6 for the sums of 256 parts.
 template <class T, bool NT, bool VEC>
 __global__ __launch_bounds__(256) void gated_backward_kernel(const T *dO, int64_t lddo,
                                                              const T *G, int64_t ldg,
@@ -631,6 +645,62 @@ __global__ __launch_bounds__(256) void gated_backward_kernel(const T *dO, int64_
         for (int e = 0; e < 4; ++e)
             if (c + 64 * e < n) part[p * n + c + 64 * e] = one[e];
     }
+}
+
+// The same for few rows: a workgroup owns all rows of 32 columns, so that the sums need no second launch (nor partial sums):
+// V neighbouring columns a lane, the rows dealt to the lanes' groups in turn, the waves joined in their order. Bound by the
+// latency of its few loads and, with more rows, by what a compute unit takes in: 64 x 4608 bf16 3.6 us, 301 x 4607 fp32, element
+// by element, 9.9 (27.7 MB, 2.8 TB/s on 144 of 256 compute units).
+template <class T, int V, int THREADS>
+__global__ __launch_bounds__(THREADS) void gated_strip_kernel(const T *dO, int64_t lddo, const T *G, int64_t ldg, const T *U,
+                                                              int64_t ldu, int64_t m, int64_t n, int act, T *dG, int64_t lddg,
+                                                              T *dU, int64_t lddu, float *__restrict__ dbias_g,
+                                                              float *__restrict__ dbias_u) {
+    constexpr int C = 32, LR = C / V, step = THREADS / LR, K = 4, kWaves = THREADS / 64;
+    __shared__ float join[2][kWaves][C];
+    const int tid = threadIdx.x, c = tid % LR * V;
+    const int64_t col = (int64_t)blockIdx.x * C + c;
+    const bool in = col < n;
+    float s[2][V] = {};
+    for (int64_t i = tid / LR; in && i < m; i += K * step) {
+        float d[K][V], z[K][V], u[K][V];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t row = i + k * step < m ? i + k * step : i;
+            load_some(dO + row * lddo + col, d[k]);
+            load_some(G + row * ldg + col, z[k]);
+            load_some(U + row * ldu + col, u[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t row = i + k * step;
+            if (row >= m) break;
+            activate_gated_grad(d[k], u[k], z[k], act);
+            if (dG) store_some(dG + row * lddg + col, d[k]);
+            if (dU) store_some(dU + row * lddu + col, u[k]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                s[0][e] += d[k][e];
+                s[1][e] += u[k][e];
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float v = slots_sum<LR>(s[k][e]);
+            if (tid % 64 < LR) join[k][tid / 64][c + e] = v;
+        }
+    __syncthreads();
+    if (tid >= 2 * C) return;
+    const int k = tid / C, j = tid % C;
+    float *out = k ? dbias_u : dbias_g;
+    if (!out || (int64_t)blockIdx.x * C + j >= n) return;
+    float v = join[k][0][j];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += join[k][w][j];
+    out[(int64_t)blockIdx.x * C + j] = v;
 }
 
 }  // namespace linear
@@ -758,6 +828,25 @@ kq_status launch_gated(GatedKernel k, const uint8_t *ca, const uint8_t *sa, cons
         case kGatedTile64: return launch_tiles<T, 1, 2, 2>(ca, sa, cg, sg, packed, g, ep, stream);
         default: return launch_tiles<T, 2, 2, 2>(ca, sa, cg, sg, packed, g, ep, stream);
     }
+}
+
+// Rows up to which the gated gradients are taken in strips of columns, in one launch: with both biases bf16 64 x 4608 5.8 us
+// by rows and 3.6 by strips, 301 x 4608 9.1 and 7.6, 512 x 4608 11.4 and 10.5, 1024 x 4608 15.4 and 16.7, 512 x 28672 42 and 50;
+// fp32, element by element, 64 x 4607 6.6 and 4.1, 301 x 4607 11.5 and 9.9, 512 x 11009 32 and 42. 256 threads for 16-byte pieces (1024:
+// 301 x 28672 25.5 and 34.9), 1024 for elements (256: 301 x 4607 9.0 and 16.7).
+constexpr int64_t kStripRows = 384;
+
+template <class T>
+void launch_gated_strips(const void *dO, int64_t lddo, const void *G, int64_t ldg, const void *U, int64_t ldu, int64_t m,
+                         int64_t n, int act, void *dG, int64_t lddg, void *dU, int64_t lddu, float *dbias_g,
+                         float *dbias_u, bool vec, kq_stream_t stream) {
+    auto go = [&](auto V, auto THREADS) {
+        hipLaunchKernelGGL((kq::linear::gated_strip_kernel<T, V(), THREADS()>), dim3((unsigned)((n + 31) / 32)),
+                           dim3(THREADS()), 0, (hipStream_t)stream, (const T *)dO, lddo, (const T *)G, ldg, (const T *)U,
+                           ldu, m, n, act, (T *)dG, lddg, (T *)dU, lddu, dbias_g, dbias_u);
+    };
+    if (vec) go(std::integral_constant<int, 16 / (int)sizeof(T)>(), std::integral_constant<int, 256>());
+    else go(std::integral_constant<int, 1>(), std::integral_constant<int, 1024>());
 }
 
 template <class T>
@@ -909,7 +998,7 @@ kq_status kq_mxfp4_gated_linear_backward_workspace_bytes(int64_t m, int64_t n, i
     if (m < 0 || n < 0) return KQ_ERR_SHAPE;
     if (!sizes_fit({m, n})) return KQ_ERR_UNSUPPORTED;
     const int64_t parts = column_parts(m, n);
-    if (parts > 1) *bytes = parts * 2 * n * 4;
+    if (m > kStripRows) *bytes = parts * 2 * n * 4;
     return KQ_OK;
 }
 
@@ -928,25 +1017,35 @@ kq_status kq_mxfp4_gated_linear_backward(const void *dO, int64_t lddo, const voi
     if (!dO || !G || !U || (!dG && !dU && !sums)) return KQ_ERR_NULL;
     const uintptr_t es = type == KQ_BF16 ? 2 : 4;
     if (!aligned(dO, es) || !aligned(G, es) || !aligned(U, es) || !aligned(dG, es) || !aligned(dU, es)) return KQ_ERR_ALIGN;
+    const int64_t per16 = 16 / es;
+    const bool strips = sums && m <= kStripRows;
+    bool vec = n % 8 == 0 && aligned(dO, 16) && aligned(G, 16) && aligned(U, 16) && aligned(dG, 16) && aligned(dU, 16) &&
+               (lddo | ldg | ldu | lddg | lddu) % per16 == 0;
+    if (strips) {
+        if (!groups_fit((n + 31) / 32, 1024)) return KQ_ERR_UNSUPPORTED;
+        if (type == KQ_BF16)
+            launch_gated_strips<uint16_t>(dO, lddo, G, ldg, U, ldu, m, n, act, dG, lddg, dU, lddu, dbias_g, dbias_u, vec, stream);
+        else
+            launch_gated_strips<float>(dO, lddo, G, ldg, U, ldu, m, n, act, dG, lddg, dU, lddu, dbias_g, dbias_u, vec, stream);
+        return launched();
+    }
     const int64_t parts = column_parts(m, n);
-    float *part_g = dbias_g, *part_u = dbias_u;
-    if (sums && parts > 1) {
+    float *part_g = nullptr, *part_u = nullptr;
+    if (sums) {
         if (!workspace) return KQ_ERR_NULL;
         if (!aligned(workspace, 16)) return KQ_ERR_ALIGN;
         if (workspace_bytes < parts * 2 * n * 4) return KQ_ERR_SHAPE;
         part_g = static_cast<float *>(workspace);
         part_u = part_g + parts * n;
     }
-    const int64_t per16 = 16 / es;
-    const bool vec = n % 8 == 0 && aligned(dO, 16) && aligned(G, 16) && aligned(U, 16) && aligned(dG, 16) && aligned(dU, 16) &&
-                     (lddo | ldg | ldu | lddg | lddu) % per16 == 0 && aligned(part_g, 16) && aligned(part_u, 16);
+    vec = vec && aligned(part_g, 16) && aligned(part_u, 16);
     if (type == KQ_BF16)
         launch_gated_backward<uint16_t>(dO, lddo, G, ldg, U, ldu, m, n, act, dG, lddg, dU, lddu, parts, part_g, part_u, vec, stream);
     else
         launch_gated_backward<float>(dO, lddo, G, ldg, U, ldu, m, n, act, dG, lddg, dU, lddu, parts, part_g, part_u, vec, stream);
     const kq_status s = launched();
     if (s != KQ_OK) return s;
-    if (sums && parts > 1) return kqhost::reduce_parts(part_g, part_u, parts, n, dbias_g, dbias_u, stream);
+    if (sums) return kqhost::reduce_parts(part_g, part_u, parts, n, dbias_g, dbias_u, stream);
     return KQ_OK;
 }
 

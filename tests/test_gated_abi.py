@@ -39,11 +39,11 @@ def backward(dO=GOOD, lddo=8, G=GOOD, ldg=8, U=GOOD, ldu=8, type=0, m=40, n=8, a
     (forward(O=P(0x10001)), ALIGN), (forward(G=P(0x10001)), ALIGN), (forward(U=P(0x10001)), ALIGN),
     (forward(m=0, ca=None, O=None), OK), (forward(n=0, cg=None, O=None), OK),
     (backward(m=-1), SHAPE), (backward(n=-1), SHAPE), (backward(lddo=7), SHAPE), (backward(ldg=7), SHAPE), (backward(ldu=7), SHAPE),
-    (backward(lddg=7), SHAPE), (backward(lddu=7), SHAPE), (backward(ws_bytes=639), SHAPE), (backward(act=9), UNSUPPORTED),
+    (backward(lddg=7), SHAPE), (backward(lddu=7), SHAPE), (backward(m=400, ws_bytes=6399), SHAPE), (backward(act=9), UNSUPPORTED),
     (backward(type=-1), UNSUPPORTED), (backward(m=BIG), UNSUPPORTED), (backward(lddu=BIG), UNSUPPORTED), (backward(dO=None), NULL),
-    (backward(G=None), NULL), (backward(U=None), NULL), (backward(ws=None), NULL), (backward(dG=None, dU=None, bg=None, bu=None), NULL),
+    (backward(G=None), NULL), (backward(U=None), NULL), (backward(m=400, ws=None, ws_bytes=6400), NULL), (backward(dG=None, dU=None, bg=None, bu=None), NULL),
     (backward(dO=P(0x10002)), ALIGN), (backward(G=P(0x10002)), ALIGN), (backward(U=P(0x10002)), ALIGN), (backward(dG=P(0x10002)), ALIGN),
-    (backward(dU=P(0x10002)), ALIGN), (backward(bg=P(0x10002)), ALIGN), (backward(bu=P(0x10001)), ALIGN), (backward(ws=P(0x10008)), ALIGN),
+    (backward(dU=P(0x10002)), ALIGN), (backward(bg=P(0x10002)), ALIGN), (backward(bu=P(0x10001)), ALIGN), (backward(m=400, ws=P(0x10008), ws_bytes=6400), ALIGN),
     (backward(n=0, dO=None), OK), (backward(m=0, dO=None, bg=None, bu=None), OK),
 ])
 def test_host_argument_checks(call, status):
@@ -54,10 +54,11 @@ def test_workspace_bytes():
     n = ctypes.c_int64(-1)
     ask = kq.lib().kq_mxfp4_gated_linear_backward_workspace_bytes
     one = ctypes.c_int64(-1)
-    for m, cols in ((0, 8), (4, 8), (5, 8), (301, 4607), (8192, 11008), (9, 0), (0, 0), (BIG - 1, BIG - 1)):
+    for m, cols in ((0, 8), (4, 8), (301, 4607), (384, 8), (385, 8), (8192, 11008), (400, 0), (9, 0), (0, 0), (BIG - 1, BIG - 1)):
         assert ask(m, cols, ctypes.byref(n)) == OK
         kq.lib().kq_mxfp4_linear_backward_workspace_bytes(m, cols, ctypes.byref(one))
-        assert n.value == 2 * one.value
+        # up to 384 rows one workgroup sums all rows of a column
+        assert n.value == (2 * one.value if m > 384 else 0)
     assert ask(4, 4, None) == NULL and ask(-1, 4, ctypes.byref(n)) == SHAPE and ask(4, BIG, ctypes.byref(n)) == UNSUPPORTED
 
 

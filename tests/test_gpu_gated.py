@@ -187,7 +187,7 @@ def test_halves_of_one_weight(torch, kq, m, n):
 
 
 GRADS = [(1, 1), (1, 4096), (7, 100), (33, 513), (301, 4607), (500, 512), (64, 8192), (1000, 4001), (1030, 2048), (4096, 24),
-         (5, 11008), (2, 70000)]
+         (5, 11008), (2, 70000), (384, 1000), (385, 1000), (384, 517), (129, 24)]
 
 
 @pytest.mark.parametrize("dt", ["bfloat16", "float32"])
@@ -228,7 +228,7 @@ def test_gradients_in_place_and_halves(torch, kq):
 
 def test_summed_gradients_of_integers(torch, kq):
     """Every row counts once in either sum: integers, exact in fp32."""
-    for m, n in ((1, 40), (3, 513), (37, 24), (300, 1000), (1025, 520), (5000, 9)):
+    for m, n in ((1, 40), (3, 513), (37, 24), (300, 1000), (384, 40), (384, 33), (385, 40), (1025, 520), (5000, 9)):
         for dt in (torch.bfloat16, torch.float32):
             dout, g, u = (torch.randint(-3, 4, (m, n), generator=gen(torch, m + i), device="cuda").to(dt) for i in range(3))
             dg, du, bg, bu = kq.mxfp4_gated_linear_backward(dout, g, u, act="none")
@@ -331,6 +331,6 @@ def test_refusals_of_the_binding(torch, kq):
                       (dict(dg=torch.zeros(1, 8, device="cuda").expand(4, 8)), kq.KQError)]:
         with pytest.raises(error):
             kq.mxfp4_gated_linear_backward(**{"dout": d, "g": d, "u": d, **kw})
-    d = torch.zeros(40, 8, device="cuda")
+    d = torch.zeros(400, 8, device="cuda")
     with pytest.raises(kq.KQError):
         kq.mxfp4_gated_linear_backward(d, d, d, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
