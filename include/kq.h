@@ -686,7 +686,8 @@ kq_status kq_mxfp4_gated_linear(const uint8_t *codes_a, const uint8_t *scales_a,
  *                     wanted. dG may be dO, G or U with its stride, and dU likewise, but not both one.
  *   dbias_g, dbias_u  device, fp32 [n], or NULL; written, not added to
  *   workspace         as kq_layernorm_backward, kq_mxfp4_gated_linear_backward_workspace_bytes(m, n)
- *                     (0, and not read, up to 384 rows, where one launch does both)
+ *                     (0, and not read, up to 384 rows of up to 2^26 columns,
+ *                     where one launch does both)
  * With m == 0 and n > 0 the dbiases are set to zeros.
  */
 kq_status kq_mxfp4_gated_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t *bytes);

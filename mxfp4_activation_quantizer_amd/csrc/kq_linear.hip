@@ -835,6 +835,7 @@ kq_status launch_gated(GatedKernel k, const uint8_t *ca, const uint8_t *sa, cons
 // fp32, element by element, 64 x 4607 6.6 and 4.1, 301 x 4607 11.5 and 9.9, 512 x 11009 32 and 42. 256 threads for 16-byte pieces (1024:
 // 301 x 28672 25.5 and 34.9), 1024 for elements (256: 301 x 4607 9.0 and 16.7).
 constexpr int64_t kStripRows = 384;
+bool in_strips(int64_t m, int64_t n) { return m <= kStripRows && groups_fit((n + 31) / 32, 1024); }
 
 template <class T>
 void launch_gated_strips(const void *dO, int64_t lddo, const void *G, int64_t ldg, const void *U, int64_t ldu, int64_t m,
@@ -998,7 +999,7 @@ kq_status kq_mxfp4_gated_linear_backward_workspace_bytes(int64_t m, int64_t n, i
     if (m < 0 || n < 0) return KQ_ERR_SHAPE;
     if (!sizes_fit({m, n})) return KQ_ERR_UNSUPPORTED;
     const int64_t parts = column_parts(m, n);
-    if (m > kStripRows) *bytes = parts * 2 * n * 4;
+    if (!in_strips(m, n)) *bytes = parts > 1 ? parts * 2 * n * 4 : 0;
     return KQ_OK;
 }
 
@@ -1018,11 +1019,9 @@ kq_status kq_mxfp4_gated_linear_backward(const void *dO, int64_t lddo, const voi
     const uintptr_t es = type == KQ_BF16 ? 2 : 4;
     if (!aligned(dO, es) || !aligned(G, es) || !aligned(U, es) || !aligned(dG, es) || !aligned(dU, es)) return KQ_ERR_ALIGN;
     const int64_t per16 = 16 / es;
-    const bool strips = sums && m <= kStripRows;
     bool vec = n % 8 == 0 && aligned(dO, 16) && aligned(G, 16) && aligned(U, 16) && aligned(dG, 16) && aligned(dU, 16) &&
                (lddo | ldg | ldu | lddg | lddu) % per16 == 0;
-    if (strips) {
-        if (!groups_fit((n + 31) / 32, 1024)) return KQ_ERR_UNSUPPORTED;
+    if (sums && in_strips(m, n)) {
         if (type == KQ_BF16)
             launch_gated_strips<uint16_t>(dO, lddo, G, ldg, U, ldu, m, n, act, dG, lddg, dU, lddu, dbias_g, dbias_u, vec, stream);
         else
@@ -1030,8 +1029,8 @@ kq_status kq_mxfp4_gated_linear_backward(const void *dO, int64_t lddo, const voi
         return launched();
     }
     const int64_t parts = column_parts(m, n);
-    float *part_g = nullptr, *part_u = nullptr;
-    if (sums) {
+    float *part_g = dbias_g, *part_u = dbias_u;
+    if (sums && parts > 1) {
         if (!workspace) return KQ_ERR_NULL;
         if (!aligned(workspace, 16)) return KQ_ERR_ALIGN;
         if (workspace_bytes < parts * 2 * n * 4) return KQ_ERR_SHAPE;
@@ -1045,7 +1044,7 @@ kq_status kq_mxfp4_gated_linear_backward(const void *dO, int64_t lddo, const voi
         launch_gated_backward<float>(dO, lddo, G, ldg, U, ldu, m, n, act, dG, lddg, dU, lddu, parts, part_g, part_u, vec, stream);
     const kq_status s = launched();
     if (s != KQ_OK) return s;
-    if (sums) return kqhost::reduce_parts(part_g, part_u, parts, n, dbias_g, dbias_u, stream);
+    if (sums && parts > 1) return kqhost::reduce_parts(part_g, part_u, parts, n, dbias_g, dbias_u, stream);
     return KQ_OK;
 }
 

@@ -54,11 +54,12 @@ def test_workspace_bytes():
     n = ctypes.c_int64(-1)
     ask = kq.lib().kq_mxfp4_gated_linear_backward_workspace_bytes
     one = ctypes.c_int64(-1)
-    for m, cols in ((0, 8), (4, 8), (301, 4607), (384, 8), (385, 8), (8192, 11008), (400, 0), (9, 0), (0, 0), (BIG - 1, BIG - 1)):
+    for m, cols in ((0, 8), (4, 8), (301, 4607), (384, 8), (385, 8), (8192, 11008), (400, 0), (9, 0), (0, 0), (BIG - 1, BIG - 1),
+                    (384, 1 << 26), (3, 1 << 28), (384, 1 << 28)):
         assert ask(m, cols, ctypes.byref(n)) == OK
         kq.lib().kq_mxfp4_linear_backward_workspace_bytes(m, cols, ctypes.byref(one))
         # up to 384 rows one workgroup sums all rows of a column
-        assert n.value == (2 * one.value if m > 384 else 0)
+        assert n.value == (2 * one.value if m > 384 or cols >= 1 << 27 else 0)
     assert ask(4, 4, None) == NULL and ask(-1, 4, ctypes.byref(n)) == SHAPE and ask(4, BIG, ctypes.byref(n)) == UNSUPPORTED
 
 

@@ -226,6 +226,17 @@ def test_gradients_in_place_and_halves(torch, kq):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_gradients_of_very_many_columns(torch, kq):
+    """More columns than a launch has strips for: few rows, taken by rows."""
+    n = (1 << 27) + 24
+    dout, g, u = (torch.randn(2, n, generator=gen(torch, i), device="cuda").to(torch.bfloat16) for i in range(3))
+    got = kq.mxfp4_gated_linear_backward(dout, g, u)
+    for at in (slice(0, 3000), slice(n // 2 - 7, n // 2 + 3000), slice(n - 3000, n)):
+        want, tol = ref.backward(dout[:, at], g[:, at], u[:, at], "silu")
+        for what, a, b, t in zip(("dg", "du", "dbias_g", "dbias_u"), got, want, tol):
+            layer_ref.assert_near(a[..., at], b, t, what)
+
+
 def test_summed_gradients_of_integers(torch, kq):
     """Every row counts once in either sum: integers, exact in fp32."""
     for m, n in ((1, 40), (3, 513), (37, 24), (300, 1000), (384, 40), (384, 33), (385, 40), (1025, 520), (5000, 9)):
