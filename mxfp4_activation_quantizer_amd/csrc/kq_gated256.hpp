@@ -10,7 +10,9 @@
 // stage of this one, into the buffer that its last stage leaves free, and its second when every wave has read that last
 // stage; the epilogue, on outputs gated in registers and staged once, in their own type, has a little LDS of its own.
 // Stores are counted with the loads and come back in their order, so that a wait for a load waits for the stores before
-// it: with both stages asked for in front of them, an epilogue's stores have two stages' time to leave.
+// it: with both stages asked for in front of them, an epilogue's stores have two stages' time to leave. Where no tile of
+// the same kind follows, those loads have no records and no scalar offset. Halves of a tile without a column inside n
+// are passed over.
 //
 // 8192 x 11008 x 4096 bf16 silu, packed scales: 343 to 356 us with the clock the board settles at (4.1 to 4.3 PFLOP/s; FP4
 // matrix instructions alone 5.5), 410 as one launch of a workgroup per tile. What is left over the matrix unit's time is 4 us
@@ -50,13 +52,14 @@ struct Geom {
     TileOrder order;
 };
 
-// One tile's place and operands; TC: its columns of the output (128, or 64 for a half).
+// One tile's place and operands.
 struct Place {
     int64_t m0, n0;
-    int rows, cols;
+    int rows;
     i32x4_t a, w;   // this wave's descriptors of codes
     i32x4_t s;      // and of scales
     uint32_t s_at;  // the lane's offset into the scales
+    uint32_t step;  // scalar offset of stage 1: 0 where there is nothing to load
 };
 
 // Values of one output in the matrix layout (16 neighbouring rows' worth of a lane: groups q of columns 8 q + 4 hi ..)
@@ -133,17 +136,24 @@ struct Tile {
         return (uint64_t)(uint32_t)(band * kGroupM + within % gm) << 32 | (uint32_t)(within / gm) << 2 | (uint32_t)(work.half + 1);
     }
 
-    // TN: staged rows of W, 256 or, for a half tile, 128. none: no record of its operands, so that its loads are zeros.
+    // Whether a work, a whole tile or a half, has a column inside n.
+    __device__ __forceinline__ bool some(uint32_t tn_half) const {
+        return g256::gated_cols((int)(tn_half >> 2), (int)(tn_half & 3) - 1, ep.n).count > 0;
+    }
+
+    // TN: staged rows of W, 256 or, for a half tile, 128. none: nothing to load.
     template <int TN>
     __device__ __forceinline__ Place place(uint32_t tm, uint32_t tn_half, bool none) const {
-        constexpr int TC = TN / 2;
         Place p;
+        const g256::GatedCols c = g256::gated_cols((int)(tn_half >> 2), TN == 256 ? -1 : (int)(tn_half & 3) - 1, ep.n);
         p.m0 = (int64_t)tm * kTile;
-        p.n0 = (int64_t)(tn_half >> 2) * (kTile / 2) + (TN == 256 ? 0 : TC * ((int)(tn_half & 3) - 1));
+        p.n0 = c.first;
         p.rows = (int)min<int64_t>(kTile, ep.m - p.m0);
-        p.cols = (int)max<int64_t>(0, min<int64_t>(TC, ep.n - p.n0));
-        p.a = sdesc(ca + p.m0 * g.kbytes, none ? 0u : (uint32_t)(p.rows * g.kbytes));
-        p.w = sdesc(cw + p.n0 * g.kbytes, none ? 0u : (uint32_t)(p.cols * g.kbytes));
+        const g256::CodeSpan a = g256::code_span(p.m0, none ? 0 : p.rows, g.kbytes);
+        const g256::CodeSpan w_ = g256::code_span(p.n0, none ? 0 : c.count, g.kbytes);
+        p.a = sdesc(ca + a.first, a.bytes);
+        p.w = sdesc(cw + w_.first, w_.bytes);
+        p.step = a.step;
         // scales: the whole array, so that every read stays inside it (a padding row past m or n reads a later stage's
         // bytes, or zero past the last: its codes are zero and its outputs are not stored)
         const int kblocks = NS ? g.kbytes / 16 : 8 * g.stages;
@@ -188,9 +198,9 @@ struct Tile {
         }
         // the chunk of k of an even and of an odd load (their rows start at multiples of 8)
         const int chunk[2] = {(lane & 7) ^ swz8(lane >> 3), (lane & 7) ^ swz8(8 + (lane >> 3))};
-        // Load l of stage s of tile q into buffer `to`: 0 .. 7 A's codes, .. 7 + LW W's, then the scales.
-        auto issue = [&](const Place &q, int s, int to, int l) {
-            const uint32_t st = lds0 + (uint32_t)(to * kStage), kb = 128u * (uint32_t)s;
+        // Load l of stage s, kb bytes of k on, of tile q into buffer `to`: 0 .. 7 A's codes, .. 7 + LW W's, then the scales.
+        auto issue = [&](const Place &q, int s, uint32_t kb, int to, int l) {
+            const uint32_t st = lds0 + (uint32_t)(to * kStage);
             // chunks past k are pushed past the record count
             auto in = [&](uint32_t off, int j) { return !NS || 128 * s + 16 * chunk[j & 1] < g.kbytes ? off : 0x80000000u; };
             if (l < 8) {
@@ -287,7 +297,7 @@ struct Tile {
                     mma(F, S, jc, a, b);
                     if (j < kLoadSteps && NB * a + b < kPerStep && l < kAll) {
                         pin(a, b);
-                        issue(q, s, to, l);
+                        issue(q, s, 128u * (uint32_t)s, to, l);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -302,9 +312,9 @@ struct Tile {
             // what the tile before loaded for none to follow it
             asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-            for (int l = kAll - 1; l >= 0; --l) issue(p, 0, buf, l);
+            for (int l = kAll - 1; l >= 0; --l) issue(p, 0, 0u, buf, l);
 #pragma unroll
-            for (int l = kAll - 1; l >= 0; --l) issue(p, 1, buf ^ 1, l);
+            for (int l = kAll - 1; l >= 0; --l) issue(p, 1, p.step, buf ^ 1, l);
         }
         // Stage 0 has landed in every wave's part. After it came the loads of stage 1 and, of the tile before, the stores.
         auto landed = [&](auto younger) {
@@ -382,7 +392,7 @@ struct Tile {
         // every wave has read the last stage: its buffer takes the next tile's stage 1
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-        for (int l = 0; l < kAll; ++l) issue(next, 1, buf, l);
+        for (int l = 0; l < kAll; ++l) issue(next, 1, next.step, buf, l);
 
         // Epilogue: the wave's 128 rows x 32 NP columns, 4 KB at a time.
         const int64_t i0 = p.m0 + wm, j0 = p.n0 + wn;
@@ -498,15 +508,23 @@ __global__ __launch_bounds__(kThreads) void gated256_kernel(const uint8_t *__res
         const int mine = (k & ~63) + t.lane;
         tiles = t.tile_of((int)blockIdx.x + (mine < count ? mine : 0) * (int)gridDim.x);
     };
+    // n: the next work, from it on, that has a column inside n; `count` for none
+    uint32_t tm = 0, tn_half = 0;
+    auto seek = [&] {
+        for (; n < count; ++n) {
+            if ((n & 63) == 0) look(n);
+            work(n, tm, tn_half);
+            if (t.some(tn_half)) return;
+        }
+    };
     // works of one kind, whole or half tiles, as long as they follow each other
-    auto all = [&](auto TN, uint32_t tm, uint32_t tn_half) {
+    auto all = [&](auto TN) {
         Place here = t.template place<TN()>(tm, tn_half, false);
         for (;;) {
             ++n;
-            if ((n & 63) == 0) look(n);
-            work(n, tm, tn_half);
+            seek();
             const bool ahead = n < count && ((tn_half & 3) == 0) == (TN() == 256);
-            const Place next = t.template place<TN()>(ahead ? tm : 0, ahead ? tn_half : 0, !ahead);
+            const Place next = t.template place<TN()>(ahead ? tm : 0, ahead ? tn_half : TN() == 256 ? 0 : 1, !ahead);
             stores = t.template run<TN()>(here, buf, warm, warm && stores, next);
             // the buffer after the last stage's, where the next tile's first one is
             buf = (buf + g.stages) & 1;
@@ -515,12 +533,10 @@ __global__ __launch_bounds__(kThreads) void gated256_kernel(const uint8_t *__res
             here = next;
         }
     };
-    look(0);
+    seek();
     while (n < count) {
-        uint32_t tm, tn_half;
-        work(n, tm, tn_half);
-        if ((tn_half & 3) == 0) all(std::integral_constant<int, 256>(), tm, tn_half);
-        else all(std::integral_constant<int, 128>(), tm, tn_half);
+        if ((tn_half & 3) == 0) all(std::integral_constant<int, 256>());
+        else all(std::integral_constant<int, 128>());
     }
     // the loads for none to follow
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

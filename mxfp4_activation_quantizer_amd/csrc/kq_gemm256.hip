@@ -156,10 +156,9 @@ __device__ __forceinline__ void gemm256_tile(const uint8_t *__restrict__ ca, con
     // codes: rows past m or n are past the record count and read zero
     const i32x4_t dca = sdesc(ca + m0 * g.kbytes, (uint32_t)(rows_a * g.kbytes));
     const i32x4_t dcw = sdesc(cw + n0 * g.kbytes, (uint32_t)(rows_w * g.kbytes));
-    // packed scales: stage s of row i at 8 (s rows + i), the whole offset in the
-    // range-checked vector offset (the scalar offset is not checked), so every
-    // read stays inside the packed array: a padding row past m or n reads a
-    // later stage's bytes (harmless: its codes are zero and its outputs are
+    // packed scales: stage s of row i at 8 (s rows + i), the record count that of
+    // the whole array, so every read stays inside it: a padding row past m or n
+    // reads a later stage's bytes (harmless: its codes are zero and its outputs are
     // never stored), or zero on the last stage
     constexpr bool kTail = NS && EPI;
     const int kblocks = kTail ? g.kbytes / 16 : 8 * g.stages;

@@ -384,8 +384,8 @@ __global__ __launch_bounds__(320, 3) void tile_kernel(const uint8_t *__restrict_
         const int row = (r0 < TM ? r0 : GATED && r0 >= TM + TC ? r0 - TM - TC : r0 - TM) + (lane >> 3);
         voff[j] = (uint32_t)(row * g.kbytes) + 16u * (uint32_t)chunk[j & 1];
     }
-    // Past k (whole stages too): past the record count, zeros. The count is compared with the scalar
-    // offset taken off it, so that must not exceed it: 0 for the stages past the last.
+    // Past k (whole stages too): past the record count, zeros. The scalar offset stays below that count: 0 for the
+    // stages past the last.
     auto issue = [&](int s, int slot) {
         const bool in[2] = {128 * s + 16 * chunk[0] < g.kbytes, 128 * s + 16 * chunk[1] < g.kbytes};
         const int kb = s < g.stages ? 128 * s : 0;

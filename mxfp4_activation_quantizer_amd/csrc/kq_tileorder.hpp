@@ -18,7 +18,11 @@
 //    epilogue, bound by HBM writes when every CU stores at once) alternate
 //    instead of coinciding. The finish time in tile units is the same as the
 //    plain order's.
+//
+// And what the tiles of the gated product (256 rows by 128 columns) cover and load.
 #pragma once
+
+#include <cstdint>
 
 namespace kq {
 namespace g256 {
@@ -85,6 +89,28 @@ constexpr TileWork tile_work(int i, const TileOrder &o) {
     const int q = o.nwg / 8, rm = o.nwg % 8, x = p % 8, loc = p / 8;
     const int tile = x < rm ? x * (q + 1) + loc : rm * (q + 1) + (x - rm) * q + loc;
     return TileWork{tile, half};
+}
+
+// Columns [first, first + count) of the n of the output: column tile tn of the gated product, or half 0 or 1 of it
+// (half -1: all of it). A right half may have none.
+struct GatedCols {
+    int64_t first;
+    int count;
+};
+constexpr GatedCols gated_cols(int tn, int half, int64_t n) {
+    const int width = half < 0 ? 128 : 64;
+    const int64_t first = (int64_t)tn * 128 + (half > 0 ? 64 : 0), left = n - first;
+    return GatedCols{first, (int)(left <= 0 ? 0 : left < width ? left : width)};
+}
+
+// What one tile's loads of one operand's codes may touch: `bytes` from `first` on, stage s at the scalar offset
+// s step. No rows: nothing is read, and no offset passes that count.
+struct CodeSpan {
+    int64_t first;
+    uint32_t bytes, step;
+};
+constexpr CodeSpan code_span(int64_t row0, int rows, int kbytes) {
+    return rows > 0 ? CodeSpan{row0 * kbytes, (uint32_t)rows * (uint32_t)kbytes, 128u} : CodeSpan{0, 0u, 0u};
 }
 
 }  // namespace g256
