@@ -11,7 +11,7 @@
 // The angle is reduced in 64 bits: p f / (2 pi) less its nearest whole number is
 // off by 2^-52 of itself, so by 2e-8 turns at 10^8 turns, where 32 bits would
 // leave nothing of it past a few million. Sine and cosine of the rest are taken
-// in 32 bits.
+// in 32 bits, to 1.5 units in the last place (kq_turn.hpp).
 //
 // A head is held by LG neighbouring lanes. A lane has U units of it, each two
 // pieces of V neighbouring channels: for pairs (i, i + r / 2) the two pieces are
@@ -42,6 +42,7 @@
 #include "kq_device.hpp"
 #include "kq_host.hpp"
 #include "kq_lanesum.hpp"
+#include "kq_turn.hpp"
 
 namespace kq {
 namespace heads {
@@ -206,19 +207,6 @@ __device__ __forceinline__ Place place_of(int u, int d, int half) {
 // channels that are not rotated.
 template <int V>
 __device__ __forceinline__ int table_row(const Rope &rope) { return rope.half + V; }
-// cos and sin of a quarter turn times f, |f| <= 1/2: the series in x = pi f / 2 to x^10 and x^9 (what follows is below
-// 2^-33 and 2^-28 of them), Horner's rule in x^2, 1.5 units in the last place in all.
-__device__ __forceinline__ float2 quarter_turn(float f) {
-    const float x = f * 1.57079632679489662f, x2 = x * x;
-    float c = fmaf(x2, -2.75573192e-7f, 2.48015873e-5f), s = fmaf(x2, 2.75573192e-6f, -1.98412698e-4f);
-    c = fmaf(x2, c, -1.38888889e-3f);
-    s = fmaf(x2, s, 8.33333333e-3f);
-    c = fmaf(x2, c, 4.16666667e-2f);
-    s = fmaf(x2, s, -1.66666667e-1f);
-    c = fmaf(x2, c, -0.5f);
-    s = s * x2;
-    return make_float2(fmaf(x2, c, 1.0f), fmaf(x, s, x));
-}
 template <int V>
 __device__ __forceinline__ void fill_table(float2 *table, const Rope &rope, int64_t t0, int tokens, int tid, int threads) {
     const int row = table_row<V>(rope);
@@ -233,7 +221,7 @@ __device__ __forceinline__ void fill_table(float2 *table, const Rope &rope, int6
             // in quarter turns
             const double x = (double)rope.pos[(t0 + t) * rope.axes + axis] * (rope.freq[j] * 0.63661977236758134);
             const double n = rint(x);
-            v = quarter_turn((float)(x - n));
+            v = quarter_turn(x - n);
             const int64_t k = (int64_t)n;
             if (k & 1) v = make_float2(-v.y, v.x);
             if (k & 2) v = make_float2(-v.x, -v.y);
