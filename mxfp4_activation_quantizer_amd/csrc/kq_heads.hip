@@ -167,7 +167,7 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 // Where unit u of a head lies: its first piece at channel a, its second at b, whether they exist, and the pairs that
-// they (each by itself, for pairs inside a piece) start with; `half` for none.
+// they (each by itself, for pairs inside a piece) start with; -1 for none.
 struct Place {
     int a, b, pair_a, pair_b;
     bool in_a, in_b;
@@ -182,8 +182,8 @@ __device__ __forceinline__ Place place_of(int u, int d, int half) {
         p.in_b = u + h < n && p.in_a;
         p.a = V * u;
         p.b = V * (u + h);
-        p.pair_a = p.in_a && p.a < r ? p.a / 2 : half;
-        p.pair_b = p.in_b && p.b < r ? p.b / 2 : half;
+        p.pair_a = p.in_a && p.a < r ? p.a / 2 : -1;
+        p.pair_b = p.in_b && p.b < r ? p.b / 2 : -1;
     } else if (u < half / V) {
         p.a = INTER ? 2 * u : V * u;
         p.b = INTER ? 2 * u + 1 : half + V * u;
@@ -195,7 +195,7 @@ __device__ __forceinline__ Place place_of(int u, int d, int half) {
         p.in_b = w + h < n && p.in_a;
         p.a = r + V * w;
         p.b = r + V * (w + h);
-        p.pair_a = p.pair_b = half;
+        p.pair_a = p.pair_b = -1;
     }
     // a missing piece's weight is read where the head's first is
     if (!p.in_a) p.a = 0;
@@ -203,50 +203,52 @@ __device__ __forceinline__ Place place_of(int u, int d, int half) {
     return p;
 }
 
-// A token's row of the table of angles in LDS: (amp cos t, amp sin t) of its pairs and then V times (1, 0), for the
-// channels that are not rotated.
+// The table of angles in LDS: (amp cos t, amp sin t) of every pair of every token of a block, a token's row V longer than
+// its pairs, so that the rows' first entries are not all in one bank.
 template <int V>
 __device__ __forceinline__ int table_row(const Rope &rope) { return rope.half + V; }
 template <int V>
 __device__ __forceinline__ void fill_table(float2 *table, const Rope &rope, int64_t t0, int tokens, int tid, int threads) {
-    const int row = table_row<V>(rope);
-    const float inv = 1.0f / (float)row;
-    for (int i = tid; i < tokens * row; i += threads) {
-        const int t = (int)(((float)i + 0.5f) * inv), j = i - t * row;
-        float2 v = make_float2(1.0f, 0.0f);
-        if (j < rope.half) {
-            int axis = 0;
+    const float inv = 1.0f / (float)rope.half;
+    for (int i = tid; i < tokens * rope.half; i += threads) {
+        const int t = (int)(((float)i + 0.5f) * inv), j = i - t * rope.half;
+        int axis = 0;
 #pragma unroll
-            for (int a = 0; a < 3; ++a) axis += a + 1 < rope.axes && j >= rope.upto[a];
-            // in quarter turns
-            const double x = (double)rope.pos[(t0 + t) * rope.axes + axis] * (rope.freq[j] * 0.63661977236758134);
-            const double n = rint(x);
-            v = quarter_turn(x - n);
-            const int64_t k = (int64_t)n;
-            if (k & 1) v = make_float2(-v.y, v.x);
-            if (k & 2) v = make_float2(-v.x, -v.y);
-            v.x *= rope.amp;
-            v.y *= rope.amp;
-        }
-        table[i] = v;
+        for (int a = 0; a < 3; ++a) axis += a + 1 < rope.axes && j >= rope.upto[a];
+        // in quarter turns
+        const double x = (double)rope.pos[(t0 + t) * rope.axes + axis] * (rope.freq[j] * 0.63661977236758134);
+        const double n = rint(x);
+        float2 v = quarter_turn(x - n);
+        const int64_t k = (int64_t)n;
+        if (k & 1) v = make_float2(-v.y, v.x);
+        if (k & 2) v = make_float2(-v.x, -v.y);
+        v.x *= rope.amp;
+        v.y *= rope.amp;
+        table[t * table_row<V>(rope) + j] = v;
     }
 }
 
-// The pieces (a, b) of one unit turned by their angles, BACK: by the opposite ones. `row`: the token's row of the table.
+// The pieces (a, b) of one unit turned by their angles, BACK: by the opposite ones; a piece that no pair is in is left as it
+// is, to the sign of its zeros. `row`: the token's row of the table.
 template <int V, bool INTER, bool BACK>
 __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2 *row, const Place &p) {
     if (INTER && V > 1) {
-        const float2 *ta = row + p.pair_a, *tb = row + p.pair_b;
+        const float2 *ta = row + (p.pair_a < 0 ? 0 : p.pair_a), *tb = row + (p.pair_b < 0 ? 0 : p.pair_b);
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
             const float2 ca = ta[e / 2], cb = tb[e / 2];
             const float a0 = a[e], a1 = a[e + 1], b0 = b[e], b1 = b[e + 1];
-            a[e] = fmaf(a0, ca.x, BACK ? a1 * ca.y : -(a1 * ca.y));
-            a[e + 1] = fmaf(a1, ca.x, BACK ? -(a0 * ca.y) : a0 * ca.y);
-            b[e] = fmaf(b0, cb.x, BACK ? b1 * cb.y : -(b1 * cb.y));
-            b[e + 1] = fmaf(b1, cb.x, BACK ? -(b0 * cb.y) : b0 * cb.y);
+            const float s0 = fmaf(a0, ca.x, BACK ? a1 * ca.y : -(a1 * ca.y));
+            const float s1 = fmaf(a1, ca.x, BACK ? -(a0 * ca.y) : a0 * ca.y);
+            const float t0 = fmaf(b0, cb.x, BACK ? b1 * cb.y : -(b1 * cb.y));
+            const float t1 = fmaf(b1, cb.x, BACK ? -(b0 * cb.y) : b0 * cb.y);
+            a[e] = p.pair_a < 0 ? a0 : s0;
+            a[e + 1] = p.pair_a < 0 ? a1 : s1;
+            b[e] = p.pair_b < 0 ? b0 : t0;
+            b[e + 1] = p.pair_b < 0 ? b1 : t1;
         }
     } else {
+        if (p.pair_a < 0) return;
         const float2 *ta = row + p.pair_a;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
