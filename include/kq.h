@@ -701,7 +701,7 @@ kq_status kq_mxfp4_gated_linear_backward(const void *dO, int64_t lddo, const voi
  * t = p freq[i], p the token's position,
  *   (a, b) -> amplitude (a cos t - b sin t, b cos t + a sin t);
  * the other channels are left as they are. The angle is reduced in fp64 (p freq[i] is off
- * by 2^-52 of itself), sine and cosine are taken in fp32. Read by the host during the call.
+ * by at most 2^-51 of itself), sine and cosine are taken in fp32. Read by the host during the call.
  *   positions    device, int64 [m][axes], 8-byte aligned, any values
  *   freq         device, fp64 [rot / 2], radians per position (kq_rope_frequencies; an fp32
  *                table converts exactly)

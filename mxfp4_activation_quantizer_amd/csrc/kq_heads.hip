@@ -8,10 +8,11 @@
 //   (n_a, n_b) -> amp (n_a cos t - n_b sin t, n_b cos t + n_a sin t), t = p f_i,
 // for the pairs i < r / 2 of the first r channels; the others are n.
 //
-// The angle is reduced in 64 bits: p f / (2 pi) less its nearest whole number is
-// off by 2^-52 of itself, so by 2e-8 turns at 10^8 turns, where 32 bits would
-// leave nothing of it past a few million. Sine and cosine of the rest are taken
-// in 32 bits, to 1.5 units in the last place (kq_turn.hpp).
+// The angle is reduced in 64 bits: p f / (2 pi), less its nearest whole number. The
+// constant, its product with f, that with p and p itself are rounded: off by 2^-51 of
+// itself at most (1.2 2^-52 measured, 1.6 for p past 2^53), so by 4e-8 turns at 10^8
+// turns, where 32 bits would leave nothing of it past a few million. Sine and cosine of
+// the rest are taken in 32 bits, to 1.5 units in the last place (kq_turn.hpp).
 //
 // A head is held by LG neighbouring lanes. A lane has U units of it, each two
 // pieces of V neighbouring channels: for pairs (i, i + r / 2) the two pieces are
