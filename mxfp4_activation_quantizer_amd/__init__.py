@@ -1363,7 +1363,7 @@ def headnorm_rope_backward(dy, x=None, positions=None, freq=None, weight_q=None,
 
 def _slots(t, index):
     """Pointer of the int64 slot list t on device ``index``."""
-    if t.dtype is not _torch().int64 or t.dim() != 1 or not t.is_contiguous():
+    if not isinstance(t, _torch().Tensor) or t.dtype is not _torch().int64 or t.dim() != 1 or not t.is_contiguous():
         raise TypeError("slots must be a contiguous int64 vector")
     if t.get_device() != index:
         raise ValueError("slots is on %s, expected device %d" % (t.device, index))
@@ -1372,6 +1372,8 @@ def _slots(t, index):
 
 def _cache(codes, scales, name, heads, d, index, slots=None):
     """(slots, codes pointer, scales pointer) of one half of a cache."""
+    if codes is None or scales is None:
+        raise ValueError("codes%s and scales%s are required" % (name, name))
     n = codes.shape[0]
     if tuple(codes.shape) != (n, heads, d // 2) or tuple(scales.shape) != (n, heads, d // 32) or slots not in (None, n):
         raise ValueError("codes%s and scales%s have shapes %s and %s, expected [slots][%d][%d] and [slots][%d][%d]" % (
@@ -1410,13 +1412,14 @@ def cache_write_mxfp4(slots, k=None, codes_k=None, scales_k=None, v=None, codes_
         n, cp, sp = _cache(codes, scales, name, heads, d, index, n)
         parts.append((t.data_ptr(), ld, hs, heads, cp, sp))
     (kp, ldk, hsk, kh, ckp, skp), (vp, ldv, hsv, vh, cvp, svp) = parts
+    sp = _slots(slots, index)
     if slots.numel() != m:
         raise ValueError("slots has %d entries, expected %d" % (slots.numel(), m))
     _check("kq_cache_write_mxfp4",
            lib().kq_cache_write_mxfp4(kp, ldk, hsk, kh, vp, ldv, hsv, vh, int(bf16), m, d, 1 if norm else 0,
                                       _vector(weight, "weight", d, index), eps,
                                       _rope(positions, freq, m, index, interleaved, amplitude, axis_pairs),
-                                      _slots(slots, index), n, ckp, skp, cvp, svp, _current_stream(index)))
+                                      sp, n, ckp, skp, cvp, svp, _current_stream(index)))
 
 
 def cache_read_mxfp4(slots, codes, scales, bf16=True, out=None, stream=None):
@@ -1435,13 +1438,13 @@ def cache_read_mxfp4(slots, codes, scales, bf16=True, out=None, stream=None):
     heads, d = codes.shape[1], 2 * codes.shape[2]
     n, cp, sp = _cache(codes, scales, "", heads, d, index)
     dtype = torch.bfloat16 if bf16 else torch.float32
-    m = slots.numel()
+    slots_p, m = _slots(slots, index), slots.numel()
     if out is None:
         out, ldy, hsy = codes.new_empty(m, heads, d, dtype=dtype), heads * d, d
     else:
         ldy, hsy = _heads(out, "out", dtype, index, (m, heads, d))
     _check("kq_cache_read_mxfp4",
-           lib().kq_cache_read_mxfp4(_slots(slots, index), m, cp, sp, n, heads, d, 1 if bf16 else 0, out.data_ptr(),
+           lib().kq_cache_read_mxfp4(slots_p, m, cp, sp, n, heads, d, 1 if bf16 else 0, out.data_ptr(),
                                      ldy, hsy, _current_stream(index)))
     return out
 

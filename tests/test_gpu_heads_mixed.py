@@ -90,3 +90,23 @@ def test_gated_gradients_in_every_place(torch, kq, m, n):  # noqa: F811
             bg, bu = (torch.empty(n + 1, device="cuda")[1:] for _ in range(2))
             got = kq.mxfp4_gated_linear_backward(*t, act="gelu_tanh", dg=t[a], du=t[b], dbias_g=bg, dbias_u=bu)
             assert all(torch.equal(x, y) for x, y in zip(got, want)), (a, b)
+
+
+def test_missing_parts_of_a_cache(torch, kq):  # noqa: F811
+    """A tensor without its codes or scales, slots that are no tensor: refused by name, and nothing is written."""
+    x = torch.ones(4, 2, 64, device="cuda")
+    codes, scales = torch.zeros(9, 2, 32, dtype=torch.uint8, device="cuda"), torch.zeros(9, 2, 2, dtype=torch.uint8, device="cuda")
+    slots = torch.arange(4, device="cuda")
+    for kw in (dict(v=x, scales_v=scales), dict(v=x, codes_v=codes), dict(k=x, codes_k=codes), dict(k=x),
+               dict(k=x, codes_k=codes, scales_k=scales, v=x)):
+        with pytest.raises(ValueError, match="are required"):
+            kq.cache_write_mxfp4(slots, **kw)
+    for bad in (None, [0, 1, 2, 3]):
+        with pytest.raises(TypeError, match="slots"):
+            kq.cache_write_mxfp4(bad, v=x, codes_v=codes, scales_v=scales)
+        with pytest.raises(TypeError, match="slots"):
+            kq.cache_read_mxfp4(bad, codes, scales)
+    with pytest.raises(ValueError, match="are required"):
+        kq.cache_read_mxfp4(slots, codes, None)
+    torch.cuda.synchronize()
+    assert not codes.any() and not scales.any()
