@@ -758,7 +758,8 @@ kq_status kq_rope_frequencies(int64_t rot, double base, int scaling, double fact
  *   rope       host, or NULL (no rotation)
  * 1 <= d <= 1024 and heads <= 65536 (KQ_ERR_UNSUPPORTED above). A NaN or an infinity makes its
  * own head NaN or infinite and no other. Range: a head's sum of squares finite in fp32 (beyond it its
- * outputs are 0 or NaN) and its mean plus eps at least 2^-126 (below it NaN or infinite).
+ * outputs are 0 or NaN) and its mean plus eps at least 2^-126 (below it NaN or infinite). A launch holds fewer than
+ * 2^24 workgroups, each of one token or more: more tokens than that may be KQ_ERR_UNSUPPORTED.
  */
 kq_status kq_headnorm_rope(const void *X, int type, int64_t m, int64_t heads, int64_t d, int64_t ldx, int64_t hsx,
                            int norm, const float *weight_q, const float *weight_k, int64_t q_heads, float eps,

@@ -335,9 +335,11 @@ struct Weights {
 // A workgroup takes the heads of a few tokens, a wave G passes in turn, each one's next loads asked for when it is
 // done. The table of angles is made once per token and read back by every head.
 //
-// Bound by HBM once it is large: 8192 x 40 x 128 bf16 32.4 us (168 MB, 5.2 TB/s; a 1 GiB copy 5.0), fp32 59.5; one
-// token of 40 x 128 3.3, a launch and the latency of its positions, frequencies and heads. A head that does not fill
-// its lanes leaves some idle: 4096 x 32 x 72 fp32 (9 of 16 lanes) 18.4 us, 4.1 TB/s.
+// Bound by HBM once it is large: 8192 x 40 x 128 bf16 31.5 us (168 MB, 5.3 TB/s; a 1 GiB copy 4.7 to 5.0), fp32 59.7, 37.4
+// where half of the channels are turned (bf16); one token of 40 x 128 3.4, a launch and the latency of its positions,
+// frequencies and heads. A head that does not fill its lanes leaves some idle: 4096 x 32 x 72 fp32 (9 of 16 lanes) 15.3 us,
+// 4.9 TB/s. One by one (d = 65) 4096 x 32 takes 31.2 us in bf16 and 31.9 in fp32, 1.1 and 2.1 TB/s: a load and a store of 2 or 4
+// bytes for each channel of each lane.
 template <class T, int V, int LG, int U, bool INTER, bool NT>
 __global__ __launch_bounds__(kThreads) void forward_kernel(const T *X, int64_t ldx, int64_t hsx,
                                                            const float *__restrict__ w0, const float *__restrict__ w1,
@@ -448,7 +450,8 @@ __global__ __launch_bounds__(kThreads) void forward_kernel(const T *X, int64_t l
 // Workgroup p of `parts` takes the blocks of tokens p, p + parts, ...; its lanes keep their channels of both dw in
 // registers, and row p of the partial sums gets them at the end, the waves joined in their order. dX may be dY or X.
 //
-// Bound by HBM: 8192 x 40 x 128 bf16 53 us and 4 for the partial sums' (252 MB, 4.7 TB/s), 4096 x 32 x 72 fp32 25 and 4.
+// Bound by HBM: 8192 x 40 x 128 bf16 53 us and 4 for the partial sums' (252 MB, 4.7 TB/s), fp32 97 and 4, 4096 x 32 x 72 fp32
+// 25 and 4; one by one (4096 x 32 x 65) 44 in bf16 and 46 in fp32.
 // Parts of 512 threads (768 are level, 1024 take 120 us) with one pass of each kind in flight (two and three are
 // level). Both dweights cost 1.9 us at one token (the joins) and 4 where a second launch adds the parts.
 template <class T, int V, int LG, int U, bool INTER, bool NT>
@@ -616,8 +619,10 @@ __global__ __launch_bounds__(kBackThreads) void backward_kernel(const T *dY, int
 // a unit a multiple of 32 channels apart), so they are quantized where they are. Otherwise a wave's heads meet in LDS,
 // where four lanes take each block.
 //
-// Bound by HBM: 8192 x (8 + 8) x 128 bf16 11.0 us, a launch's 2 and 42 MB at 4.7 TB/s, into slots in any order (8.8 with none
-// written); 64 tokens 3.1. The values' first loads beside the keys' are slower (11.7).
+// 8192 x (8 + 8) x 128 bf16 takes 11.6 us (42 MB, 3.7 TB/s, into slots in any order) and 9.0 of them with no slot to write to:
+// what bounds it is reading, 34 MB at 3.8 TB/s with one pass of loads a wave in flight, and not the stores. fp32 15.6; staged,
+// d = 96 16.8 and d = 160 23.7; 64 tokens 4.2 by themselves, 3.3 one call after another. The values' first loads beside the keys'
+// are slower (11.7 to 11.0).
 struct Cache {
     const int64_t *slots;  // [m]
     int64_t n;             // slots of the cache
@@ -771,8 +776,9 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(const T *__restri
 // Rows of the cache decoded: a lane takes 8 channels (a dword of codes) of R places of the workgroup's tokens (or
 // of its part of one token), all of whose loads are in flight together. A row whose slot lies outside the cache is
 // zeros.
-// Eight places hide the two dependent loads (slot, then codes and scale): 131072 x 8 x 128 bf16 49.9 us (340 MB, 6.8 TB/s
-// with the cache partly in the Infinity Cache), 97 with one. One place for calls that would not fill the card: 509 tokens 2.4.
+// Eight places hide the two dependent loads (slot, then codes and scale): 131072 x 8 x 128 bf16 50 us (340 MB, 6.8 TB/s
+// with the cache partly in the Infinity Cache), 97 with one; in fp32 246 (608 MB, 2.5 TB/s): a lane's two stores of 16 bytes take
+// the lines that its neighbours write too. One place for calls that would not fill the card: 509 tokens 2.6.
 struct Read {
     int64_t m, n;             // tokens, slots
     int tokens, pieces;       // tokens per workgroup; 8-channel pieces of a token
@@ -979,7 +985,7 @@ kq_status choose(int es, const Rope &rope, bool inter, int64_t n0, int64_t n1, s
         constexpr int hp = 64 / decltype(form)::kLG;
         fits = offsets_fit(kind_of(n0, 0, hp), hp, rope.d, es, tensors) && offsets_fit(kind_of(n1, n0, hp), hp, rope.d, es, tensors);
     });
-    choose_form<MOST>(v, fits ? units : v == 8 ? 64 : v == 4 ? (units > 64 ? units : 64) : (units > 64 ? units : 64), go);
+    choose_form<MOST>(v, fits || units > 64 ? units : 64, go);
     return status;
 }
 

@@ -649,8 +649,8 @@ __global__ __launch_bounds__(256) void gated_backward_kernel(const T *dO, int64_
 
 // The same for few rows: a workgroup owns all rows of 32 columns, so that the sums need no second launch (nor partial sums):
 // V neighbouring columns a lane, the rows dealt to the lanes' groups in turn, the waves joined in their order. Bound by the
-// latency of its few loads and, with more rows, by what a compute unit takes in: 64 x 4608 bf16 3.6 us, 301 x 4607 fp32, element
-// by element, 9.9 (27.7 MB, 2.8 TB/s on 144 of 256 compute units).
+// latency of its few loads and, with more rows, by what a compute unit takes in: 64 x 4608 bf16 3.5 us, 301 x 4607 fp32, element
+// by element, 10.4 (27.7 MB, 2.7 TB/s on 144 of 256 compute units).
 template <class T, int V, int THREADS>
 __global__ __launch_bounds__(THREADS) void gated_strip_kernel(const T *dO, int64_t lddo, const T *G, int64_t ldg, const T *U,
                                                               int64_t ldu, int64_t m, int64_t n, int act, T *dG, int64_t lddg,
@@ -830,10 +830,18 @@ kq_status launch_gated(GatedKernel k, const uint8_t *ca, const uint8_t *sa, cons
     }
 }
 
-// Rows up to which the gated gradients are taken in strips of columns, in one launch: with both biases bf16 64 x 4608 5.8 us
-// by rows and 3.6 by strips, 301 x 4608 9.1 and 7.6, 512 x 4608 11.4 and 10.5, 1024 x 4608 15.4 and 16.7, 512 x 28672 42 and 50;
-// fp32, element by element, 64 x 4607 6.6 and 4.1, 301 x 4607 11.5 and 9.9, 512 x 11009 32 and 42. 256 threads for 16-byte pieces (1024:
-// 301 x 28672 25.5 and 34.9), 1024 for elements (256: 301 x 4607 9.0 and 16.7).
+// Rows up to which the gated gradients are taken in strips of columns, in one launch, by rows and by strips (us, both biases,
+// silu):
+//   bf16                       64        128        256        384        512         1024 rows
+//     4608 columns        5.6 3.5    6.5 4.0    8.2 6.6    9.8 8.6  11.4 10.5    15.4 16.7
+//     11008               7.4 4.3    9.2 7.3  12.6 10.6  15.7 14.6
+//     28672              12.1 8.7  15.6 13.2  23.1 21.5  32.9 38.0      42 50
+//   fp32, by element
+//     4607                6.3 3.9    8.2 5.7   11.0 8.7  13.0 11.7
+//     11009               9.3 6.4   12.1 9.7  17.9 17.2  23.3 25.3      32 42
+// One number for all of them, so that the workspace's size is a function of the sizes alone: at 257 to 384 rows of the
+// widest ones the strips are up to 15% slower. 256 threads for 16-byte pieces (1024: 301 x 28672 25.5 and 34.9), 1024 for
+// elements (256: 301 x 4607 9.0 and 16.7).
 constexpr int64_t kStripRows = 384;
 bool in_strips(int64_t m, int64_t n) { return m <= kStripRows && groups_fit((n + 31) / 32, 1024); }
 
