@@ -53,9 +53,13 @@ inline Kernel choose_kernel(int64_t m, int64_t n, int stages, bool packed, bool 
 // The same for kq_mxfp4_gated_linear, whose tiles hold as many columns of both weights (`n` is the output's): tiles of
 // 16 x 16 and 32 x 16 outputs with k split over four waves, 64 x 64 four stages deep and two, 128 x 64, and 256 x 128 on
 // persistent workgroups. Six estimates for each layout of the scales, fitted to 1043 measured products
-// (profiles/gated_products_by_kernel.md: m = 1 .. 8192, n = 512 .. 11008, k = 256 .. 8192; the choice is 1.5%
-// slower than the fastest on average, 50% at worst). The split of k wins while its tiles are few for the compute units;
-// one token of n = 11008, k = 4096 takes 11.4 us on either the first kernel or the third.
+// (profiles/gated_products_by_kernel.md: m = 1 .. 8192, n = 512 .. 11008, k = 256 .. 8192; the choice is 0.6%
+// slower than the fastest on average, 25% at worst). The split of k wins while its tiles are few for the compute units;
+// one token of n = 11008, k = 4096 takes 11.4 us on either the first kernel or the third. What counts of the tiles is mostly
+// the rounds they make: 258 tiles of 128 x 64 (768 x 2752) take longer than 256 by more than their number. The large kernel's
+// first round starts from cold, the next ones behind another tile's loads. (With estimates linear in the tiles 42 products
+// lost more than 10%, 50% at worst; 11 do now. On 1920 others drawn at random, ragged ones among them, the choice is 1.2%
+// slower on average and 33% at worst; 1.7% and 71% before.)
 // Measured at n = 11008, k = 4096, packed scales, in the order of the list (us):
 //       1 row   11.4         11.4  13.2
 //      64              29.7  12.1  13.7  15.8
@@ -66,37 +70,50 @@ enum GatedKernel { kGatedProduct1, kGatedProduct2, kGatedTile64Deep, kGatedTile6
 
 // can256: the scales' alignment and k allow the 256 x 128 kernel.
 inline GatedKernel choose_gated_kernel(int64_t m, int64_t n, int stages, bool packed, bool can256, int cus) {
+    // t: tiles per compute unit, or, by the last number of a list (0: as they are, 1: whole rounds), between
     struct Estimate {
-        double split1[4], split2[4];   // a + b stages + tiles (c stages + d), tiles per compute unit
+        double split1[5], split2[5];   // a + b stages + t (c stages + d)
         double deep[3];                // a + rounds (b stages + c)
-        double tile64[5], tile128[5];  // a + the larger of b stages and c stages + tiles (d stages + e)
-        double big[5];                 // a + rounds (b + c stages), the last one d + e stages if it leaves half idle
+        double tile64[6], tile128[6];  // a + the larger of b stages and c stages + t (d stages + e)
+        double big[10];                // a + the first round (b + c stages; in half tiles d + e stages) + each later one (f +
+                                       // g stages; a last one in half tiles h + i stages) + j (below)
     };
     static const Estimate layouts[2] = {
-        {{2.76, 0.156, 0.197, 0.084}, {2.94, 0.199, 0.308, 0.132}, {1.20, 0.451, 3.48}, {4.12, 0.534, 0.250, 0.389, 1.69},
-         {5.14, 0.650, 0.177, 0.719, 2.65}, {3.15, 5.66, 1.85, 2.70, 1.44}},  // MX layout
-        {{2.85, 0.117, 0.184, 0.095}, {3.04, 0.159, 0.252, 0.216}, {1.23, 0.440, 2.74}, {3.34, 0.537, 0.166, 0.397, 1.20},
-         {4.15, 0.650, 0.239, 0.705, 1.61}, {2.69, 6.26, 1.52, 4.08, 0.92}}};  // packed
+        {{2.73, 0.0308, 0.229, 0.0854, 0.697}, {2.85, 0.0451, 0.305, 0.149, 0.87}, {1.3, 0.453, 3.48},
+         {3.06, 0.577, 0.266, 0.343, 1.79, 0.58}, {3.06, 0.345, 0.0598, 0.675, 2.85, 0.791},
+         {1.75, 7.2, 1.81, 4.04, 1.46, 4.91, 1.83, 3.48, 1.57, 5.79}},  // MX layout
+        {{2.82, 0.00257, 0.216, 0.0894, 0.662}, {2.98, 0.000877, 0.27, 0.194, 0.869}, {0.81, 0.452, 3.2},
+         {2.65, 0.577, 0.235, 0.35, 1.3, 0.61}, {2.98, 0.224, 0.0471, 0.713, 1.73, 0.775},
+         {0.0112, 9.42, 1.4, 6.72, 0.92, 5.22, 1.59, 4.05, 1.12, 5.83}}};  // packed
     const Estimate &e = layouts[packed ? 1 : 0];
     const double st = stages;
     auto tiles = [&](int64_t tm, int64_t tn) {  // per compute unit
         return (double)((m + tm - 1) / tm) * (double)((n + tn - 1) / tn) / cus;
     };
+    auto between = [](double t, double whole) { return t + whole * (ceil(t) - t); };
     GatedKernel best = kGatedProduct1;
     double least = HUGE_VAL;
     auto consider = [&](GatedKernel k, double us) {
         if (us < least) best = k, least = us;
     };
-    auto split = [&](const double (&x)[4], double t) { return x[0] + x[1] * st + t * (x[2] * st + x[3]); };
-    auto shared = [&](const double (&x)[5], double t) { return x[0] + fmax(x[1] * st, x[2] * st + t * (x[3] * st + x[4])); };
+    auto split = [&](const double (&x)[5], double t) { return x[0] + x[1] * st + between(t, x[4]) * (x[2] * st + x[3]); };
+    auto shared = [&](const double (&x)[6], double t) {
+        return x[0] + fmax(x[1] * st, x[2] * st + between(t, x[5]) * (x[3] * st + x[4]));
+    };
     if (m <= 16) consider(kGatedProduct1, split(e.split1, tiles(16, 16)));
     else if (m <= 256) consider(kGatedProduct2, split(e.split2, tiles(32, 16)));  // measured up to there
     consider(kGatedTile64Deep, e.deep[0] + ceil(tiles(64, 64)) * (e.deep[1] * st + e.deep[2]));
     consider(kGatedTile64, shared(e.tile64, tiles(64, 64)));
     consider(kGatedTile128, shared(e.tile128, tiles(128, 64)));
     if (can256) {
-        const double t = tiles(256, 128), rem = t - floor(t), full = e.big[1] + e.big[2] * st;
-        consider(kGatedTile256, e.big[0] + floor(t) * full + (rem == 0 ? 0 : rem <= 0.5 ? e.big[3] + e.big[4] * st : full));
+        const double t = tiles(256, 128), rounds = floor(t), rem = t - rounds, later = e.big[5] + e.big[6] * st;
+        const bool halves = rem > 0 && rem <= 0.5;
+        double us = e.big[0] + (rounds > 0 || !halves ? e.big[1] + e.big[2] * st : e.big[3] + e.big[4] * st);
+        if (rounds > 0) us += (rounds - 1) * later + (rem == 0 ? 0 : halves ? e.big[7] + e.big[8] * st : later);
+        // a wave's 64 columns that n cuts short leave element by element: at the end of a single round nothing hides that (4096 x
+        // 1376 x 512 18.1 us, 2048 x 2752 x 512, as many tiles, 12.1)
+        if (t <= 1 && !halves && n % 64 != 0) us += e.big[9];
+        consider(kGatedTile256, us);
     }
     return best;
 }
