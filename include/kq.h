@@ -757,7 +757,7 @@ kq_status kq_rope_frequencies(int64_t rot, double base, int scaling, double fact
  *   eps        >= 0 and finite (KQ_ERR_SHAPE)
  *   rope       host, or NULL (no rotation)
  * 1 <= d <= 1024 and heads <= 65536 (KQ_ERR_UNSUPPORTED above). A NaN or an infinity makes its
- * own head NaN or infinite and no other. Range: a head's sum of squares finite in fp32 (beyond it its
+ * own head (with norm 0 its own pair, or itself alone where no pair is) NaN or infinite and no other. Range: a head's sum of squares finite in fp32 (beyond it its
  * outputs are 0 or NaN) and its mean plus eps at least 2^-126 (below it NaN or infinite). A launch holds fewer than
  * 2^24 workgroups, each of one token or more: more tokens than that may be KQ_ERR_UNSUPPORTED.
  */
