@@ -91,6 +91,12 @@ def lib():
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError("libkq.so is not built: run `python -m mxfp4_activation_quantizer_amd.build`")
+        # torch's HIP runtime first, so that libkq.so is bound to it: the other way round the process would have two, and
+        # libkq.so's would see no device
+        try:
+            _torch()
+        except ImportError:  # the host's helpers need none
+            pass
         L = ctypes.CDLL(LIB_PATH)
         p, i64, st, f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
         for name, args in {
