@@ -14,7 +14,7 @@
 // the same kind follows, those loads have no records and no scalar offset. Halves of a tile without a column inside n
 // are passed over.
 //
-// 8192 x 11008 x 4096 bf16 silu, packed scales: 343 to 367 us with the clock the board settles at (4.0 to 4.3 PFLOP/s; FP4
+// 8192 x 11008 x 4096 bf16 silu, packed scales: 337 to 367 us with the clock the board settles at (4.0 to 4.4 PFLOP/s; FP4
 // matrix instructions alone 5.5), 410 as one launch of a workgroup per tile. In one run: 365 us, fp32 outputs 372, with both
 // biases 388 (their loads come back behind the next tile's two stages), g and u kept 406, both 431, fp32 with g and u 463,
 // scales in the MX layout 420 (four loads of 4 bytes a lane each stage where the packed ones take one of 16). What is left
